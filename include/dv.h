@@ -154,7 +154,8 @@ const char* dv_status_string(dv_status status);
 const char* dv_last_error(void);
 
 /* Debugging.  A checked build of the library (built with DV_CHECKED=1, file
- * libdv_checked.so) checks every global access of its kernels against the
+ * libdv_checked.so) checks every global access of its copy kernels (pack,
+ * unpack, restore; not the attention operators below) against the
  * extents the host validated; an access outside them is skipped and the
  * first one is recorded (nothing traps).  dv_debug_fault waits for the device,
  * returns that record in *fault (0: none; else bit 63 set, bits 56..62 the
@@ -577,6 +578,138 @@ dv_status dv_delta_streamer_join(dv_delta_streamer* ds);
 dv_status dv_delta_streamer_wait(dv_delta_streamer* ds);
 
 void dv_delta_streamer_destroy(dv_delta_streamer* ds);
+
+/* ---- new tokens, attention and compaction over the cache ------------------ */
+
+/* The operators a decoder layer applies to the cache between two transfers:
+ * the new tokens' rows are written (dv_kv_append), read by attention
+ * (dv_prompt_attention, dv_tree_attention), and an accepted path of drafted
+ * tokens, or the rows an eviction leaves, are moved together
+ * (dv_kv_compact).  The pages have no counterpart: their compute is the
+ * host framework's.  [seq_start, seq_end) are, here too, host arrays of row
+ * ranges: the rows of the NEW tokens of each sequence.  Buffers with one entry per new
+ * token hold the sequences' tokens one after the other (packed, no padding),
+ * T = sum(seq_end - seq_start) of them; an empty range is a sequence that
+ * takes no part.  Every pointer is device memory; every call can be captured
+ * in a CUDA graph. */
+
+typedef enum { DV_DTYPE_FP16 = 0, DV_DTYPE_BF16 = 1 } dv_dtype;
+
+#define DV_MAX_ROT 256   /* rotated elements of a head */
+#define DV_MAX_TREE 64   /* drafted tokens of a sequence in one dv_tree_attention */
+#define DV_MAX_GROUP 128 /* query heads that share a key head */
+
+/* How rotary frequencies are scaled for contexts longer than the trained one. */
+typedef enum {
+  DV_ROPE_NONE = 0,   /* f_i = base^(-2i/rot_dim) */
+  DV_ROPE_LINEAR = 1, /* f_i / factor (position interpolation) */
+  DV_ROPE_NTK = 2,    /* base * factor^(rot_dim/(rot_dim-2)) in place of base */
+  DV_ROPE_PARTS = 3   /* by parts (YaRN): with r_i = original_max * f_i / 2 pi turns over the
+                         trained context and g = clamp((r_i - 1) / 31, 0, 1), g f_i +
+                         (1 - g) f_i / factor; rotated values times 0.1 ln(factor) + 1 */
+} dv_rope_scaling;
+
+/* A rotation, filled by dv_rope_init and owned by the caller (plain data; it
+ * may be copied).  turn[i] is pair i's frequency in turns per position as a
+ * 64-bit binary fraction: position * turn[i] modulo 2^64 is the angle, exact
+ * for any int32 position. */
+typedef struct {
+  int32_t rot_dim;     /* rotated elements, the first of each head; the rest pass through */
+  int32_t interleaved; /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i+1) */
+  float value_factor;  /* on cos and sin */
+  int32_t reserved;
+  uint64_t turn[DV_MAX_ROT / 2];
+} dv_rope;
+
+/* Host only.  rot_dim even, in [2, DV_MAX_ROT]; base > 1; factor >= 1 and
+ * original_max > 0 where the scaling uses them (DV_ROPE_NTK: rot_dim > 2);
+ * else DV_ERR_INVALID_ARG. */
+dv_status dv_rope_init(dv_rope* rope, int32_t rot_dim, int32_t interleaved, double base,
+                       int32_t scaling, double factor, int32_t original_max);
+
+/* New tokens of one layer: strides in elements from one token to the next
+ * (multiples of 8; at least heads * head_dim), heads and their elements
+ * contiguous, so that a fused projection's rows can be given as they are. */
+typedef struct {
+  int32_t dtype;   /* dv_dtype, of every buffer here and of the cache */
+  int32_t q_heads; /* 0: keys and values only */
+  const void* k;   /* [T][num_heads][head_dim] */
+  int64_t k_stride;
+  const void* v; /* [T][num_heads][head_dim] */
+  int64_t v_stride;
+  const void* q; /* [T][q_heads][head_dim] */
+  int64_t q_stride;
+  void* q_out; /* rotated queries; overlaps none of q, k, v */
+  int64_t q_out_stride;
+  const int32_t* positions; /* [T] position of each token; NULL: its cache row */
+  const dv_rope* rope;      /* NULL: nothing is rotated (q is copied) */
+} dv_new_tokens;
+
+/* Rotates q and k by their positions and writes k and v to rows
+ * [seq_start, seq_end) of layer `layer`, in the cache's layout.  Values are
+ * rotated in 32 bits and rounded once; elements past rot_dim, and v, are
+ * copied bit for bit.  elem_bytes must be 2.  Errors: DV_ERR_RANGE (layer,
+ * ranges), DV_ERR_INVALID_ARG (null or overlapping buffers, strides too
+ * small, unknown dtype, rot_dim above head_dim), DV_ERR_MISALIGNED,
+ * DV_ERR_BUFFER_TOO_SMALL (a buffer's allocation ends before its last token),
+ * DV_ERR_UNSUPPORTED (elem_bytes). */
+dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
+                       const int32_t* seq_end, const dv_new_tokens* tokens, dv_stream stream);
+
+/* Queries and output of one attention call. */
+typedef struct {
+  int32_t dtype;   /* dv_dtype of q, out and the cache */
+  int32_t q_heads; /* a multiple of num_heads, at most DV_MAX_GROUP times it; query head h
+                      reads key head h / (q_heads / num_heads) */
+  const void* q;   /* [T][q_heads][head_dim] */
+  int64_t q_stride; /* elements from one token to the next, a multiple of 8 */
+  void* out;        /* the same shape; does not overlap q */
+  int64_t out_stride;
+  float scale; /* on q.k; finite and positive */
+} dv_queries;
+
+/* Bytes of device workspace an attention call over these ranges needs (an upper bound for
+ * every layer of the cache; 0 when it needs none).  Host only. */
+dv_status dv_attention_workspace(const dv_cache* cache, const int32_t* seq_start,
+                                 const int32_t* seq_end, int32_t q_heads, size_t* bytes);
+
+/* Causal attention of prompts, or of chunks of prompts: the token at row r of
+ * its sequence attends rows [0, r] of the cache, which holds the earlier rows
+ * already and the new tokens' rows since their dv_kv_append:
+ *   out = sum_j w_j v_j,  w = softmax over the attended rows of scale * q.k_j.
+ * Scores, softmax sums and outputs are accumulated in 32 bits; the weights
+ * are rounded to `dtype` before they multiply v, the output once.  Rows that
+ * a token does not attend have no effect on it, whatever they hold (NaN and
+ * infinities included).  head_dim a multiple of 8 up to 128, elem_bytes 2
+ * (else DV_ERR_UNSUPPORTED).  `workspace`: device memory, 16-byte aligned,
+ * of dv_attention_workspace bytes (NULL when that is 0), for this call alone
+ * until the stream has passed it; it needs no initial value. */
+dv_status dv_prompt_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
+                              const int32_t* seq_end, const dv_queries* queries, void* workspace,
+                              size_t workspace_bytes, dv_stream stream);
+
+/* Attention of drafted tokens: at most DV_MAX_TREE new tokens of each
+ * sequence (else DV_ERR_UNSUPPORTED), the token i of sequence b at row
+ * seq_start[b] + i.  Every one attends rows [0, seq_start[b]) and, of the new
+ * rows, those whose bit is set in tree[T]'s entry for it (device memory, 8-byte aligned; bit j:
+ * row seq_start[b] + j; bits at or past the sequence's token count are ignored; usually its ancestors and itself).
+ * tree NULL: a chain (bits 0..i), and so a plain decode step for one token.
+ * A token that attends no row at all (an empty mask with an empty context)
+ * has a zero output.  Everything else as dv_prompt_attention. */
+dv_status dv_tree_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
+                            const int32_t* seq_end, const dv_queries* queries,
+                            const uint64_t* tree, void* workspace, size_t workspace_bytes,
+                            dv_stream stream);
+
+/* Moves rows together, in place, in layers [l0, l1): row seq_start[b] + i of
+ * sequence b (for every i below its range's length) gets what row
+ * keep[T-index of (b, i)] of the sequence held before the call.  keep: device
+ * memory, T int32 entries, 4-byte aligned.  An entry that is negative, not
+ * below max_seq, or below its own destination row leaves that row as it was
+ * (so that a list of fixed length can be padded with -1).  Rows outside the
+ * ranges are untouched.  Any elem_bytes. */
+dv_status dv_kv_compact(const dv_cache* cache, int32_t l0, int32_t l1, const int32_t* seq_start,
+                        const int32_t* seq_end, const int32_t* keep, dv_stream stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

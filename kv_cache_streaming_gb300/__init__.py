@@ -7,6 +7,10 @@ slices of a max-length-preallocated cache into one contiguous buffer, scatter
 host memory, stream the prompt cache layer by layer, and keep a host-side
 replica of decode deltas that a cache can be restored from.
 
+Over the same cache, the operators of a decoder layer between two transfers:
+new tokens appended with rotary positions, causal prompt attention, attention
+of drafted token trees (and plain decode), and rows compacted in place.
+
 All work runs in the hand-written sm_103a kernels of ``libdv.so`` behind the C
 ABI of ``include/dv.h``; this package only marshals arguments (see
 ``kv_cache_streaming_gb300.dv``).  Importing it fails if ``libdv.so`` has not
@@ -32,4 +36,8 @@ from .dv import (  # noqa: F401
     dv_swapper_wait, dv_swapper_destroy,
     DeltaStreamer, dv_delta_streamer_create, dv_delta_stream, dv_delta_streamer_join,
     dv_delta_streamer_wait, dv_delta_streamer_destroy,
+    DV_DTYPE_FP16, DV_DTYPE_BF16, DV_MAX_ROT, DV_MAX_TREE, DV_MAX_GROUP,
+    DV_ROPE_NONE, DV_ROPE_LINEAR, DV_ROPE_NTK, DV_ROPE_PARTS,
+    Rope, dv_rope, dv_rope_init, dv_kv_append, dv_attention_workspace, dv_prompt_attention,
+    dv_tree_attention, dv_kv_compact,
 )

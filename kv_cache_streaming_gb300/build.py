@@ -27,7 +27,7 @@ OBJ = PKG / "_build"
 LIB = PKG / "libdv.so"
 LIB_CHECKED = PKG / "libdv_checked.so"  # device-side bounds checks (debugging)
 SOURCES = ["dv_api.cu", "dv_replica.cu", "dv_sched.cu", "dv_hostmem.cu", "dv_kernels.cu",
-           "dv_noalloc.cu"]
+           "dv_noalloc.cu", "dv_append.cu", "dv_compact.cu", "dv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -59,7 +59,7 @@ def _stale(target: Path, deps) -> bool:
 def build(force: bool = False, checked: bool = False) -> Path:
     """Builds libdv.so, or with `checked` the bounds-checked libdv_checked.so."""
     lib = LIB_CHECKED if checked else LIB
-    deps = [CSRC / s for s in SOURCES] + [CSRC / "dv_plan.h", CSRC / "dv_host.h",
+    deps = [CSRC / s for s in SOURCES] + [CSRC / "dv_plan.h", CSRC / "dv_host.h", CSRC / "dv_ops.h",
                                           CSRC / "libdv.map", ROOT / "include" / "dv.h",
                                           Path(__file__)]
     if not force and not _stale(lib, deps):

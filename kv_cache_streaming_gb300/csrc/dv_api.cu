@@ -42,7 +42,10 @@ GetRangeFn get_range_fn() {
   return fn;
 }
 
-// A driver entry point fetched through the runtime (nullptr if unavailable).
+}  // namespace
+
+namespace dv {
+
 void* driver_fn(const char* name) {
   void* f = nullptr;
   cudaDriverEntryPointQueryResult q;
@@ -53,10 +56,6 @@ void* driver_fn(const char* name) {
   }
   return f;
 }
-
-}  // namespace
-
-namespace dv {
 
 dv_status fail(dv_status st, const char* fmt, ...) {
   char buf[512];
@@ -170,11 +169,12 @@ dv_status plan_ranges(const dv_cache* c, int32_t l0, int32_t l1, const int32_t* 
 
 // Device-visible address of `ptr` after checking its memory kind; when the
 // driver knows the allocation, also that [ptr, ptr + need) lies inside it.
-dv_status resolve(const void* ptr, size_t need, bool allow_host, const char* what, void** dev,
-                  bool* is_host) {
+static dv_status resolve_aligned(const void* ptr, size_t need, unsigned align, bool allow_host,
+                                 const char* what, void** dev, bool* is_host) {
   if (is_host) *is_host = false;
   if (!ptr) return fail(DV_ERR_INVALID_ARG, "%s is NULL", what);
-  if (!aligned16(ptr)) return fail(DV_ERR_MISALIGNED, "%s %p is not 16-byte aligned", what, ptr);
+  if ((reinterpret_cast<uintptr_t>(ptr) & (align - 1)) != 0)
+    return fail(DV_ERR_MISALIGNED, "%s %p is not %u-byte aligned", what, ptr, align);
   ensure_context();
   cudaPointerAttributes a;
   cudaError_t err = cudaPointerGetAttributes(&a, ptr);
@@ -218,6 +218,16 @@ dv_status resolve(const void* ptr, size_t need, bool allow_host, const char* wha
                   need, ptr, (size_t)((uintptr_t)base + size - p0));
   }
   return DV_OK;
+}
+
+dv_status resolve(const void* ptr, size_t need, bool allow_host, const char* what, void** dev,
+                  bool* is_host) {
+  return resolve_aligned(ptr, need, 16, allow_host, what, dev, is_host);
+}
+
+dv_status resolve_words(const void* ptr, size_t need, unsigned align, const char* what,
+                        void** dev) {
+  return resolve_aligned(ptr, need, align, false, what, dev, nullptr);
 }
 
 // Resolves the cache's K and V bases (device memory, extent of layers < l1).

@@ -1,0 +1,375 @@
+// dv_rope_init and dv_kv_append: rotary positions for the new tokens' queries
+// and keys, and their keys and values written to the cache's rows.
+//
+// Pair i of a head turns by the angle position * f_i:
+//   (x, y) -> m (x cos - y sin, x sin + y cos).
+// f_i is held in turns per position as a 64-bit binary fraction, so that
+// position * f_i mod 1 is one integer product, exact at any position; the top
+// 32 bits of it, as a signed fraction of half a turn, go to sincospi.  (A
+// float product of a position near 10^6 and f_0 = 1 would be 0.06 rad off.)
+//
+// Memory bound: every value is read once and written once (the half layout's
+// partner chunk comes from L1).  Two kernels:
+//  * append_tile_kernel: a warp covers 8 consecutive cache rows x 4 chunks of
+//    16 bytes, and walks over heads with its lanes' 8 cosines and sines in
+//    registers.  On the token-major side that is 64 contiguous bytes a token,
+//    on the x-interleaved K side 128 contiguous bytes a chunk row: whole
+//    32-byte sectors on both, with no transpose through shared memory.  Row
+//    groups start at multiples of 8, so a range's edges alone leave lanes idle.
+//  * append_token_kernel: decode steps and short trees, a CTA per token and
+//    slice of its chunks, the angles' table in shared memory.
+#include "dv_ops.h"
+
+namespace dv {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kTileRows = 8;  // cache rows of a warp in the tile kernel
+// Ranges of fewer tokens than this on average go to the token kernel: the
+// tile kernel's lanes are tied to 8 rows, so shorter ranges leave most idle.
+constexpr int kTileMinMean = 4;
+
+template <int MAXB>
+struct AppendParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  uint4* kc;  // K and V of the layer
+  uint4* vc;
+  const int32_t* positions;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int32_t Hq, H, D, C, S;
+  int32_t rot, half, interleaved;  // rot 0: nothing is rotated; half = rot / 2
+  float factor;
+  uint64_t turn[DV_MAX_ROT / 2];
+  SeqTable<MAXB> seq;
+  int32_t group_pre[MAXB + 1];  // tile kernel: 8-row groups before the sequence
+};
+
+__device__ __forceinline__ float2 cos_sin(uint64_t turn, int32_t pos, float factor) {
+  const int64_t a = (int64_t)((uint64_t)(int64_t)pos * turn);
+  // the angle in half turns, in [-1, 1): rounded to 24 bits, at most 2^-25 off
+  const float x = (float)(int32_t)(a >> 32) * 4.656612873077393e-10f;  // 2^-31
+  float s, c;
+  sincospif(x, &s, &c);
+  return make_float2(c * factor, s * factor);
+}
+
+// The frequency index of element d (d < rot), and the sign its partner's sine
+// takes: the first of a pair loses y sin, the second gains x sin.
+template <typename P>
+__device__ __forceinline__ int pair_of(const P& p, int d, float* sign) {
+  if (p.interleaved) {
+    *sign = (d & 1) ? 1.f : -1.f;
+    return d >> 1;
+  }
+  *sign = d < p.half ? -1.f : 1.f;
+  return d < p.half ? d : d - p.half;
+}
+
+// The partners of the 8 elements of chunk c of a head's row.
+template <typename P>
+__device__ __forceinline__ uint4 partner(const P& p, const uint16_t* row, int c, uint4 x) {
+  if (p.interleaved) {  // neighbours: swap the halves of each 32-bit word
+    return make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032),
+                      __byte_perm(x.z, 0, 0x1032), __byte_perm(x.w, 0, 0x1032));
+  }
+  const int d0 = c * 8;
+  if ((p.half & 7) == 0)  // a whole chunk of the other half
+    return __ldg(reinterpret_cast<const uint4*>(row) + (d0 < p.half ? c + (p.half >> 3) : c - (p.half >> 3)));
+  uint16_t y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int d = d0 + i;
+    y[i] = d >= p.rot ? (uint16_t)0 : __ldg(row + (d < p.half ? d + p.half : d - p.half));
+  }
+  return make_uint4(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16,
+                    y[4] | (uint32_t)y[5] << 16, y[6] | (uint32_t)y[7] << 16);
+}
+
+// x cos + y sin for 8 elements, rounded once; the first `n` of them rotate,
+// the others keep their bits.
+template <typename T>
+__device__ __forceinline__ uint4 rotate(uint4 x, uint4 y, const float* cs, const float* sn, int n) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = Pack2<T>::unpack(xs[i]), b = Pack2<T>::unpack(ys[i]);
+    const uint32_t w = Pack2<T>::pack(fmaf(b.x, sn[2 * i], a.x * cs[2 * i]),
+                                      fmaf(b.y, sn[2 * i + 1], a.y * cs[2 * i + 1]));
+    r[i] = 2 * i + 1 < n ? w : 2 * i < n ? (w & 0xffffu) | (xs[i] & 0xffff0000u) : xs[i];
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <typename T, int MAXB>
+__global__ __launch_bounds__(kAppendThreads) void append_tile_kernel(
+    const __grid_constant__ AppendParams<MAXB> p) {
+  ops_pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const int gid = blockIdx.y * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int quads = (p.C + 3) >> 2;
+  const int step = (gridDim.y * (kAppendThreads / 32)) / quads;  // warps over the heads
+  const int quad = gid % quads, h0 = gid / quads;
+  if (h0 >= step) return;
+  const int b = find_span(p.group_pre, p.seq.batch, blockIdx.x);
+  const int s = p.seq.start[b];
+  const int row = ((s >> 3) + (blockIdx.x - p.group_pre[b])) * kTileRows + (lane & 7);
+  const int c = quad * 4 + (lane >> 3);
+  const int n = p.seq.pre[b + 1] - p.seq.pre[b];
+  if (row < s || row >= s + n || c >= p.C) return;
+  const int64_t tok = p.seq.pre[b] + (row - s);
+
+  const int nrot = min(8, max(0, p.rot - c * 8));  // rotated elements of the chunk
+  float cs[8], sn[8];
+  if (nrot > 0) {
+    const int32_t pos = p.positions ? p.positions[tok] : row;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < nrot) {
+        float sign;
+        const int f = pair_of(p, c * 8 + i, &sign);
+        if (p.interleaved && (i & 1)) {  // the pair's first element has them
+          cs[i] = cs[i - 1];
+          sn[i] = -sn[i - 1];
+        } else {
+          const float2 w = cos_sin(p.turn[f], pos, p.factor);
+          cs[i] = w.x;
+          sn[i] = sign * w.y;
+        }
+      } else {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+      }
+    }
+  }
+  constexpr int U = 4;  // heads in flight
+  const auto rows = [&](const uint16_t* base, int heads, bool turn, auto&& put) {
+    for (int h = h0; h < heads; h += U * step) {
+      uint4 x[U], y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * step < heads) {
+          const uint16_t* r = base + (int64_t)(h + u * step) * p.D;
+          x[u] = __ldg(reinterpret_cast<const uint4*>(r) + c);
+          if (turn) y[u] = partner(p, r, c, x[u]);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * step < heads) put(h + u * step, turn ? rotate<T>(x[u], y[u], cs, sn, nrot) : x[u]);
+    }
+  };
+  const int64_t head0 = (int64_t)b * p.H;
+  rows(p.q + tok * p.q_stride, p.Hq, nrot > 0, [&](int h, uint4 x) {
+    reinterpret_cast<uint4*>(p.q_out + tok * p.q_out_stride + (int64_t)h * p.D)[c] = x;
+  });
+  rows(p.k + tok * p.k_stride, p.H, nrot > 0, [&](int h, uint4 x) {
+    p.kc[((head0 + h) * p.C + c) * p.S + row] = x;
+  });
+  rows(p.v + tok * p.v_stride, p.H, false, [&](int h, uint4 x) {
+    p.vc[((head0 + h) * p.S + row) * p.C + c] = x;
+  });
+}
+
+template <typename T, int MAXB>
+__global__ __launch_bounds__(kAppendThreads) void append_token_kernel(
+    const __grid_constant__ AppendParams<MAXB> p) {
+  __shared__ float2 table[DV_MAX_ROT / 2];
+  ops_pdl_enter();
+  const int64_t tok = blockIdx.x;
+  const int b = find_span(p.seq.pre, p.seq.batch, blockIdx.x);
+  const int row = p.seq.start[b] + (blockIdx.x - p.seq.pre[b]);
+  const int32_t pos = p.positions ? p.positions[tok] : row;
+  for (int i = threadIdx.x; i < p.half; i += kAppendThreads)
+    table[i] = cos_sin(p.turn[i], pos, p.factor);
+  __syncthreads();
+  const int total = (p.Hq + 2 * p.H) * p.C;
+  for (int i = blockIdx.y * kAppendThreads + threadIdx.x; i < total;
+       i += gridDim.y * kAppendThreads) {
+    const int g = i / p.C, c = i - g * p.C;
+    const int kind = g < p.Hq ? 0 : g < p.Hq + p.H ? 1 : 2;
+    const int h = kind == 0 ? g : kind == 1 ? g - p.Hq : g - p.Hq - p.H;
+    const uint16_t* r = (kind == 0   ? p.q + tok * p.q_stride
+                         : kind == 1 ? p.k + tok * p.k_stride
+                                     : p.v + tok * p.v_stride) +
+                        (int64_t)h * p.D;
+    uint4 x = __ldg(reinterpret_cast<const uint4*>(r) + c);
+    const int nrot = min(8, max(0, p.rot - c * 8));
+    if (kind != 2 && nrot > 0) {
+      const uint4 y = partner(p, r, c, x);
+      float cs[8], sn[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float sign = 0.f;
+        const float2 w = k < nrot ? table[pair_of(p, c * 8 + k, &sign)] : make_float2(1.f, 0.f);
+        cs[k] = w.x;
+        sn[k] = sign * w.y;
+      }
+      x = rotate<T>(x, y, cs, sn, nrot);
+    }
+    const int64_t head = (int64_t)b * p.H + h;
+    if (kind == 0)
+      reinterpret_cast<uint4*>(p.q_out + tok * p.q_out_stride + (int64_t)h * p.D)[c] = x;
+    else if (kind == 1)
+      p.kc[(head * p.C + c) * p.S + row] = x;
+    else
+      p.vc[(head * p.S + row) * p.C + c] = x;
+  }
+}
+
+template <typename T, int MAXB>
+cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t stream) {
+  AppendParams<MAXB> kp;
+  kp.q = static_cast<const uint16_t*>(t.q);
+  kp.k = static_cast<const uint16_t*>(t.k);
+  kp.v = static_cast<const uint16_t*>(t.v);
+  kp.q_out = static_cast<uint16_t*>(t.q_out);
+  kp.kc = static_cast<uint4*>(p.k) + p.l0 * p.layer_chunks;
+  kp.vc = static_cast<uint4*>(p.v) + p.l0 * p.layer_chunks;
+  kp.positions = t.positions;
+  kp.q_stride = t.q_stride;
+  kp.k_stride = t.k_stride;
+  kp.v_stride = t.v_stride;
+  kp.q_out_stride = t.q_out_stride;
+  kp.Hq = t.q_heads;
+  kp.H = p.H;
+  kp.D = p.D;
+  kp.C = p.C;
+  kp.S = p.S;
+  kp.rot = t.rope ? t.rope->rot_dim : 0;
+  kp.half = kp.rot / 2;
+  kp.interleaved = t.rope ? t.rope->interleaved : 0;
+  kp.factor = t.rope ? t.rope->value_factor : 1.f;
+  for (int i = 0; i < kp.half; ++i) kp.turn[i] = t.rope->turn[i];
+  fill_table(p, &kp.seq);
+  constexpr int kWarps = kAppendThreads / 32;
+  const int heads = t.q_heads + 2 * p.H;
+  if (p.tokens < (int64_t)kTileMinMean * p.active) {
+    const int slices = (int)(((int64_t)heads * p.C + kAppendThreads - 1) / kAppendThreads);
+    // one chunk a thread while the grid is small, more once it fills the GPU
+    const int fit = (int)((int64_t)152 * 64 / p.tokens);
+    const int y = slices < fit ? slices : fit > 1 ? fit : 1;
+    return ops_launch(append_token_kernel<T, MAXB>, dim3((unsigned)p.tokens, y < 65535 ? y : 65535),
+                      kAppendThreads, 0, stream, kp);
+  }
+  int64_t groups = 0;
+  for (int b = 0; b < p.B; ++b) {
+    kp.group_pre[b] = (int32_t)groups;
+    const int64_t s = p.seq_start[b], e = s + p.seq_len[b];
+    if (e > s) groups += (e + kTileRows - 1) / kTileRows - s / kTileRows;
+  }
+  kp.group_pre[p.B] = (int32_t)groups;
+  // Warps over the heads: enough of them to fill the GPU (8 CTAs of 8 warps an
+  // SM), but at least 4 heads to a warp, so that a chunk's angles are used again.
+  const int quads = (p.C + 3) / 4;
+  const int most_heads = t.q_heads > p.H ? t.q_heads : p.H;
+  int64_t warps = ((int64_t)152 * 64 + groups - 1) / groups;  // a group's warps
+  const int64_t cap = (int64_t)quads * ((most_heads + 3) / 4);
+  if (warps > cap) warps = cap;
+  if (warps < quads) warps = quads;
+  int64_t y = (warps + kWarps - 1) / kWarps;
+  if (y > 65535) y = 65535;
+  return ops_launch(append_tile_kernel<T, MAXB>, dim3((unsigned)groups, (unsigned)y),
+                    kAppendThreads, 0, stream, kp);
+}
+
+}  // namespace
+}  // namespace dv
+
+using dv::fail;
+
+extern "C" dv_status dv_rope_init(dv_rope* rope, int32_t rot_dim, int32_t interleaved, double base,
+                                  int32_t scaling, double factor, int32_t original_max) {
+  if (!rope) return fail(DV_ERR_INVALID_ARG, "rope is NULL");
+  if (rot_dim < 2 || rot_dim > DV_MAX_ROT || rot_dim % 2 != 0)
+    return fail(DV_ERR_INVALID_ARG, "rot_dim %d is not an even number in [2,%d]", rot_dim,
+                DV_MAX_ROT);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(DV_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", interleaved);
+  if (!(base > 1.0) || !std::isfinite(base))
+    return fail(DV_ERR_INVALID_ARG, "base must be finite and above 1 (got %g)", base);
+  if (scaling < DV_ROPE_NONE || scaling > DV_ROPE_PARTS)
+    return fail(DV_ERR_INVALID_ARG, "unknown scaling %d", scaling);
+  if (scaling != DV_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(DV_ERR_INVALID_ARG, "factor must be finite and at least 1 (got %g)", factor);
+  if (scaling == DV_ROPE_NTK && rot_dim <= 2)
+    return fail(DV_ERR_INVALID_ARG, "DV_ROPE_NTK needs rot_dim above 2");
+  if (scaling == DV_ROPE_PARTS && original_max <= 0)
+    return fail(DV_ERR_INVALID_ARG, "DV_ROPE_PARTS needs original_max (got %d)", original_max);
+  const double two_pi = 6.283185307179586476925;
+  if (scaling == DV_ROPE_NTK) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  rope->rot_dim = rot_dim;
+  rope->interleaved = interleaved;
+  rope->value_factor = scaling == DV_ROPE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  rope->reserved = 0;
+  for (int i = 0; i < DV_MAX_ROT / 2; ++i) {
+    if (i >= rot_dim / 2) {
+      rope->turn[i] = 0;
+      continue;
+    }
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == DV_ROPE_LINEAR) f /= factor;
+    if (scaling == DV_ROPE_PARTS) {
+      const double g = ((double)original_max * f / two_pi - 1.0) / 31.0;
+      const double w = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      f = w * f + (1.0 - w) * f / factor;
+    }
+    rope->turn[i] = (uint64_t)std::ldexp(f / two_pi, 64);  // f <= 1: below 0.16 of 2^64
+  }
+  return DV_OK;
+}
+
+extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
+                                  const int32_t* seq_end, const dv_new_tokens* tokens,
+                                  dv_stream stream) {
+  dv::Trace trace("dv_kv_append");
+  if (!tokens) return fail(DV_ERR_INVALID_ARG, "tokens is NULL");
+  dv::Plan p;
+  dv_status st = dv::plan_layer(cache, layer, seq_start, seq_end, tokens->dtype, &p);
+  if (st != DV_OK) return st;
+  dv_new_tokens t = *tokens;
+  if (t.q_heads < 0 || (int64_t)t.q_heads * p.D > INT32_MAX / 2)
+    return fail(DV_ERR_INVALID_ARG, "q_heads is %d", t.q_heads);
+  if ((int64_t)p.H * p.D > INT32_MAX / 8)
+    return fail(DV_ERR_UNSUPPORTED, "%d heads of %d elements", p.H, p.D);
+  if (t.rope) {
+    if (t.rope->rot_dim < 2 || t.rope->rot_dim > DV_MAX_ROT || t.rope->rot_dim % 2 != 0 ||
+        t.rope->rot_dim > p.D)
+      return fail(DV_ERR_INVALID_ARG, "rot_dim %d does not fit head_dim %d", t.rope->rot_dim, p.D);
+    if (t.rope->interleaved != 0 && t.rope->interleaved != 1)
+      return fail(DV_ERR_INVALID_ARG, "rope.interleaved is %d", t.rope->interleaved);
+  }
+  if (p.tokens == 0) return DV_OK;
+  if ((st = dv::resolve_cache(cache, &p)) != DV_OK) return st;
+  void* dev = nullptr;
+  size_t nk = 0, nv = 0, nq = 0, no = 0;
+  if ((st = dv::resolve_rows(p, t.k, p.H, t.k_stride, "k", &dev, &nk)) != DV_OK) return st;
+  t.k = dev;
+  if ((st = dv::resolve_rows(p, t.v, p.H, t.v_stride, "v", &dev, &nv)) != DV_OK) return st;
+  t.v = dev;
+  if (t.q_heads > 0) {
+    if ((st = dv::resolve_rows(p, t.q, t.q_heads, t.q_stride, "q", &dev, &nq)) != DV_OK) return st;
+    t.q = dev;
+    if ((st = dv::resolve_rows(p, t.q_out, t.q_heads, t.q_out_stride, "q_out", &dev, &no)) != DV_OK)
+      return st;
+    t.q_out = dev;
+    if (dv::overlap(t.q_out, no, t.q, nq) || dv::overlap(t.q_out, no, t.k, nk) ||
+        dv::overlap(t.q_out, no, t.v, nv))
+      return fail(DV_ERR_INVALID_ARG, "q_out overlaps q, k or v");
+  }
+  if (t.positions && (st = dv::resolve_words(t.positions, (size_t)p.tokens * 4, 4, "positions",
+                                             &dev)) != DV_OK)
+    return st;
+  if (t.positions) t.positions = static_cast<const int32_t*>(dev);
+  cudaError_t err;
+  const bool small = p.B <= dv::kSmallBatch;
+  if (t.dtype == DV_DTYPE_FP16)
+    err = small ? dv::launch_append<__half, dv::kSmallBatch>(p, t, stream)
+                : dv::launch_append<__half, dv::kMaxBatch>(p, t, stream);
+  else
+    err = small ? dv::launch_append<__nv_bfloat16, dv::kSmallBatch>(p, t, stream)
+                : dv::launch_append<__nv_bfloat16, dv::kMaxBatch>(p, t, stream);
+  return err == cudaSuccess ? DV_OK : dv::cuda_fail(err, "append launch");
+}

@@ -110,6 +110,14 @@ dv_status plan_ranges(const dv_cache* c, int32_t l0, int32_t l1, const int32_t* 
 dv_status resolve(const void* ptr, size_t need, bool allow_host, const char* what, void** dev,
                   bool* is_host = nullptr);
 
+// The same for a device array of words of `align` bytes (4 or 8), which need
+// only that alignment.
+dv_status resolve_words(const void* ptr, size_t need, unsigned align, const char* what,
+                        void** dev);
+
+// A driver entry point fetched through the runtime (nullptr if unavailable).
+void* driver_fn(const char* name);
+
 // Resolves the cache's K and V bases (device memory, extent of layers < l1).
 dv_status resolve_cache(const dv_cache* c, Plan* p);
 

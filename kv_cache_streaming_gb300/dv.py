@@ -103,6 +103,38 @@ _delta_streamer_join = _sig("dv_delta_streamer_join", [_P])
 _delta_streamer_wait = _sig("dv_delta_streamer_wait", [_P])
 _delta_streamer_destroy = _sig("dv_delta_streamer_destroy", [_P], None)
 
+DV_DTYPE_FP16, DV_DTYPE_BF16 = 0, 1
+DV_MAX_ROT, DV_MAX_TREE, DV_MAX_GROUP = 256, 64, 128
+DV_ROPE_NONE, DV_ROPE_LINEAR, DV_ROPE_NTK, DV_ROPE_PARTS = range(4)
+
+
+class dv_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", _I32), ("interleaved", _I32), ("value_factor", ctypes.c_float),
+                ("reserved", _I32), ("turn", ctypes.c_uint64 * (DV_MAX_ROT // 2))]
+
+
+class dv_new_tokens(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("q_heads", _I32), ("k", _P), ("k_stride", _I64), ("v", _P),
+                ("v_stride", _I64), ("q", _P), ("q_stride", _I64), ("q_out", _P),
+                ("q_out_stride", _I64), ("positions", _P), ("rope", ctypes.POINTER(dv_rope))]
+
+
+class dv_queries(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("q_heads", _I32), ("q", _P), ("q_stride", _I64), ("out", _P),
+                ("out_stride", _I64), ("scale", ctypes.c_float)]
+
+
+_rope_init = _sig("dv_rope_init", [ctypes.POINTER(dv_rope), _I32, _I32, ctypes.c_double, _I32,
+                                   ctypes.c_double, _I32])
+_append = _sig("dv_kv_append", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_new_tokens), _P])
+_attention_workspace = _sig("dv_attention_workspace", [_CP, _I32P, _I32P, _I32,
+                                                       ctypes.POINTER(_SZ)])
+_prompt_attention = _sig("dv_prompt_attention", [_CP, _I32, _I32P, _I32P,
+                                                 ctypes.POINTER(dv_queries), _P, _SZ, _P])
+_tree_attention = _sig("dv_tree_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
+                                             _P, _P, _SZ, _P])
+_compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _P])
+
 
 class DvError(RuntimeError):
     def __init__(self, status: int, message: str):
@@ -675,3 +707,139 @@ def dv_delta_streamer_wait(ds: DeltaStreamer) -> None:
 
 def dv_delta_streamer_destroy(ds: DeltaStreamer) -> None:
     ds.close()
+
+
+# ---- new tokens, attention and compaction over the cache --------------------------
+
+_ROPE_SCALING = {"none": DV_ROPE_NONE, "linear": DV_ROPE_LINEAR, "ntk": DV_ROPE_NTK,
+                 "parts": DV_ROPE_PARTS}
+_dtypes = {}  # torch dtype -> dv_dtype, filled on first use (torch is imported lazily)
+
+
+def _dtype(t):
+    if not _dtypes:
+        import torch
+        _dtypes[torch.float16], _dtypes[torch.bfloat16] = DV_DTYPE_FP16, DV_DTYPE_BF16
+    d = _dtypes.get(t.dtype)
+    if d is None:
+        raise TypeError(f"fp16 or bf16 tensors are needed (got {t.dtype})")
+    return d
+
+
+def _token_rows(t, name, tokens, heads, head_dim, dtype):
+    """(address, stride) of a [tokens, heads, head_dim] tensor whose tokens may
+    be strided."""
+    if tuple(t.shape) != (tokens, heads, head_dim):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}] (got {tuple(t.shape)})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    s0, s1, s2 = t.stride()
+    if tokens and ((s2 != 1 and head_dim > 1) or (s1 != head_dim and heads > 1)):
+        raise TypeError(f"{name}: a token's heads and elements must be contiguous")
+    return t.data_ptr(), s0 if tokens > 1 else heads * head_dim
+
+
+def _words(t, name, tokens, size):
+    if t.numel() != tokens or t.element_size() != size or t.is_floating_point():
+        raise ValueError(f"{name} must hold {tokens} integers of {size} bytes (got "
+                         f"{tuple(t.shape)} {t.dtype})")
+    if not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def dv_rope_init(rot_dim, interleaved=False, base=10000.0, scaling=DV_ROPE_NONE, factor=1.0,
+                 original_max=0) -> dv_rope:
+    r = dv_rope()
+    _check(_rope_init(ctypes.byref(r), rot_dim, int(interleaved), base, scaling, factor,
+                      original_max))
+    return r
+
+
+class Rope:
+    """A rotation for ``dv_kv_append``: the first ``rot_dim`` elements of a
+    head, in pairs (i, i + rot_dim/2) or, ``interleaved``, (2i, 2i+1).
+    ``scaling``: "none", "linear", "ntk" or "parts", by ``factor``
+    (``original_max``: the trained context, for "parts")."""
+
+    def __init__(self, rot_dim, interleaved=False, base=10000.0, scaling="none", factor=1.0,
+                 original_max=0):
+        if scaling not in _ROPE_SCALING:
+            raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)} (got {scaling!r})")
+        self.c = dv_rope_init(rot_dim, interleaved, base, _ROPE_SCALING[scaling], factor,
+                              original_max)
+
+
+def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=None, rope=None,
+                 positions=None, stream=None):
+    """Rotates ``q`` (into ``q_out``, allocated when None) and ``k`` by
+    ``positions`` (int32, or None: their cache rows) and writes ``k`` and ``v``
+    to rows [seq_start, seq_end) of ``layer``.  k, v: [T, num_heads, head_dim];
+    q: [T, q_heads, head_dim]; T new tokens, packed.  Returns ``q_out``."""
+    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
+    n, H, D = int((e - s).sum()), cache.c.num_heads, cache.c.head_dim
+    t = dv_new_tokens(dtype=_dtype(k))
+    t.k, t.k_stride = _token_rows(k, "k", n, H, D, k.dtype)
+    t.v, t.v_stride = _token_rows(v, "v", n, H, D, k.dtype)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q must be [{n}, q_heads, {D}] (got {tuple(q.shape)})")
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        t.q_heads = q.shape[1]
+        t.q, t.q_stride = _token_rows(q, "q", n, t.q_heads, D, k.dtype)
+        t.q_out, t.q_out_stride = _token_rows(q_out, "q_out", n, t.q_heads, D, k.dtype)
+    if positions is not None:
+        t.positions = _words(positions, "positions", n, 4)
+    if rope is not None:
+        t.rope = ctypes.pointer(rope.c if isinstance(rope, Rope) else rope)
+    _check(_append(cache.ref, layer, sp, ep, ctypes.byref(t), _stream(stream)))
+    return q_out
+
+
+def dv_attention_workspace(cache: Cache, seq_start, seq_end, q_heads) -> int:
+    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
+    out = _SZ(0)
+    _check(_attention_workspace(cache.ref, sp, ep, q_heads, ctypes.byref(out)))
+    return out.value
+
+
+def _queries(cache, s, e, q, out, scale):
+    n, D = int((e - s).sum()), cache.c.head_dim
+    if q.dim() != 3:
+        raise ValueError(f"q must be [{n}, q_heads, {D}] (got {tuple(q.shape)})")
+    a = dv_queries(dtype=_dtype(q), q_heads=q.shape[1], scale=scale)
+    a.q, a.q_stride = _token_rows(q, "q", n, a.q_heads, D, q.dtype)
+    a.out, a.out_stride = _token_rows(out, "out", n, a.q_heads, D, q.dtype)
+    return n, a
+
+
+def dv_prompt_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, workspace=None,
+                        stream=None) -> None:
+    """Causal attention of the new tokens' queries ``q`` [T, q_heads, head_dim]
+    over the cache rows up to their own, into ``out``.  ``workspace``: a device
+    buffer of ``dv_attention_workspace`` bytes (None when that is 0)."""
+    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
+    _, a = _queries(cache, s, e, q, out, scale)
+    w, wn = _buf(workspace)
+    _check(_prompt_attention(cache.ref, layer, sp, ep, ctypes.byref(a), w, wn, _stream(stream)))
+
+
+def dv_tree_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, workspace=None,
+                      tree=None, stream=None) -> None:
+    """Attention of at most DV_MAX_TREE drafted tokens a sequence: all rows
+    before them, and of the new rows those set in ``tree`` (T 64-bit integers;
+    None: a chain, a decode step for one token)."""
+    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
+    n, a = _queries(cache, s, e, q, out, scale)
+    w, wn = _buf(workspace)
+    t = None if tree is None else _words(tree, "tree", n, 8)
+    _check(_tree_attention(cache.ref, layer, sp, ep, ctypes.byref(a), t, w, wn, _stream(stream)))
+
+
+def dv_kv_compact(cache: Cache, l0, l1, seq_start, seq_end, keep, stream=None) -> None:
+    """Row seq_start[b] + i of every sequence gets row keep[...] of it, in
+    place, in layers [l0, l1); ``keep``: int32, packed over the ranges."""
+    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
+    kp = _words(keep, "keep", int((e - s).sum()), 4)
+    _check(_compact(cache.ref, l0, l1, sp, ep, kp, _stream(stream)))
