@@ -133,6 +133,7 @@ _prompt_attention = _sig("dv_prompt_attention", [_CP, _I32, _I32P, _I32P,
                                                  ctypes.POINTER(dv_queries), _P, _SZ, _P])
 _tree_attention = _sig("dv_tree_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
                                              _P, _P, _SZ, _P])
+_attention_check = _sig("dv_attention_check", [_P])
 _compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _P])
 
 
@@ -835,6 +836,12 @@ def dv_tree_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, wo
     w, wn = _buf(workspace)
     t = None if tree is None else _words(tree, "tree", n, 8)
     _check(_tree_attention(cache.ref, layer, sp, ep, ctypes.byref(a), t, w, wn, _stream(stream)))
+
+
+def dv_attention_check(stream=None) -> None:
+    """Waits for the stream; raises DvError (DV_ERR_TIMEOUT) if a wait inside an
+    attention kernel gave up since the last check."""
+    _check(_attention_check(_stream(stream)))
 
 
 def dv_kv_compact(cache: Cache, l0, l1, seq_start, seq_end, keep, stream=None) -> None:

@@ -13,6 +13,12 @@ from tests import operator_refs as R
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _no_wait_gave_up():
+    yield
+    dv.dv_attention_check()
+
+
 def _gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
