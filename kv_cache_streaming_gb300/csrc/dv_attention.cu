@@ -20,21 +20,23 @@
 //          the other, joined at the end: decode steps and small trees, bound
 //          by reading K and V once.
 //
-// Warps: 0-3 and 4-7 the chains' softmax, 8 loads, 9 issues the products.  K
-// goes to shared memory chunk row by chunk row (bulk copies): the cache's
-// [D/8][S][8] is, per tile, exactly the tensor core's unswizzled layout of
-// 8 x 16-byte core matrices, so nothing is transposed.  V goes in by TMA with
-// the 128-byte swizzle and is read with its rows as the contraction.  Only rows
-// up to the last attended one are fetched (V in 32s).
+// Warps: 0-3 and 4-7 the chains' softmax, 8 loads (and walks over the units,
+// publishing each in a ring), 9 issues the products, 10-11 look after V's hidden rows.  K
+// goes to shared memory by TMA in its own layout: the cache's [D/8][S][8] is,
+// per tile, exactly the tensor core's unswizzled layout of 8 x 16-byte core
+// matrices, so nothing is transposed.  V goes in with the 128-byte swizzle and
+// is read with its rows as the contraction.  A sequence's last, partial tile is
+// fetched up to the last attended row (K in bulk copies, V in 32s).
 //
 // The tiles of all units form one line, cut into equal stretches, one for
 // each CTA (one CTA an SM); a unit that a cut divides leaves partial sums in
 // the workspace, which join_kernel adds up.
 //
 // Rows a mask hides must have no effect, but 0 x NaN is NaN in a product: in
-// tiles that hold hidden rows, V's non-finite values are set to zero in shared
-// memory (rows past the last attended one altogether), and should there have been any, the
-// epilogue adds them to the outputs of the rows that do attend them.
+// tiles that hold hidden rows, warps 10-11 set V's non-finite values to zero in
+// shared memory (rows past the last attended one altogether), while the tile's scores
+// are computed, and should there have been any, the epilogue adds them to the
+// outputs of the rows that do attend them.
 //
 // Every wait gives up after kSpinLimit tries: the CTA then drains its copies,
 // frees its tensor memory and returns, and dv_attention_check reports it.
@@ -46,7 +48,7 @@ namespace dv {
 namespace {
 
 constexpr int kTile = 128;        // rows of Q and of K/V in a tile
-constexpr int kThreadsAttn = 320;  // two softmax warpgroups, a load and a product warp
+constexpr int kThreadsAttn = 384;  // two softmax warpgroups, and one of the other warps
 constexpr uint32_t kSpinLimit = 1u << 22;
 constexpr float kLazy = 8.f;       // log2 of the growth that is left to the old maximum
 
@@ -57,8 +59,10 @@ __device__ uint4 g_zero_rows[kTile];
 
 template <int MAXB>
 struct AttnParams {
-  CUtensorMap q_map;  // {D, G, H, T}, 64 x G x 1 x tokens of a tile
-  CUtensorMap v_map;  // {D, S, B * H}, 64 x 32 x 1
+  CUtensorMap q_map;   // {D, G, H, T}, 64 x G x 1 x tokens of a tile
+  CUtensorMap k_map;   // {8 w, S / w, C, B * H}, 8 w x 128 / w x C x 1: w rows of a chunk row in one run
+  CUtensorMap v_map;   // {D, S, B * H}, 64 x 128 x 1
+  CUtensorMap v_part;  // the same, 64 x 32 x 1
   uint16_t* out;
   const uint4* k;
   const uint16_t* v;
@@ -67,6 +71,7 @@ struct AttnParams {
   int64_t out_stride;
   int64_t total;  // tiles of all units
   int32_t H, G, D, C, S;
+  int32_t k_rows;    // w of k_map
   int32_t tile_tok;  // tokens of a row tile: 128 / G
   int32_t unit_tok;  // tokens of a unit
   int32_t is_tree;
@@ -188,12 +193,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* a, uint32_t addr) {
       : DV_R8(a, 0), DV_R8(a, 8), DV_R8(a, 16), DV_R8(a, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* a) {
+__device__ __forceinline__ void tmem_ld16(uint32_t* a, uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      DV_W8(a, 0), DV_W8(a, 8), DV_W8(a, 16), DV_W8(a, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : DV_R8(a, 0), DV_R8(a, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* a) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      DV_W8(a, 0), DV_W8(a, 8)
       : "memory");
 }
 
@@ -213,20 +224,35 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 
 // ---- shared memory -------------------------------------------------------------
 
+// A unit, or the piece of one, that the CTA works on.
+struct Item {
+  int b, h;
+  int tok0;     // the unit's first token in its sequence
+  int row_end;  // rows [0, row_end) are attended by some row of the unit
+  int t0, n;    // the piece's tiles [t0, t0 + n); n = 0: no more items
+  int whole;    // the piece is the whole unit
+  int nt[2];    // tiles of each chain
+  int masked;   // the first tile that hides a row from some query row
+  int start, n_tok, tok_at;  // the sequence's first new row, new tokens, place in packed buffers
+  int bad;      // non-finite values were taken out of V
+};
+constexpr int kItems = 4;
+
 template <int DP>
 struct Smem {
   static constexpr int kQ = kTile * DP * 2;     // bytes of a row tile
   static constexpr int kSlot = kTile * DP * 2;  // bytes of a K or V tile
-  static constexpr int kSlots = DP == 128 ? 5 : 10;
-  static constexpr int kKv = 2 * kQ;
-  static constexpr int kCtl = kKv + kSlots * kSlot;
+  static constexpr int kK = DP == 128 ? 2 : 5;  // K tiles held
+  static constexpr int kV = DP == 128 ? 3 : 5;  // V tiles held (longer: until the softmax is done)
+  static constexpr int kKAt = 2 * kQ, kVAt = kKAt + kK * kSlot;
+  static constexpr int kCtl = kVAt + kV * kSlot;
   struct Ctl {
     uint64_t q_full[2], q_empty[2];
-    uint64_t kv_full[kSlots], kv_empty[kSlots];
+    uint64_t k_full[kK], k_empty[kK], v_full[kV], v_ok[kV], v_empty[kV];
     uint64_t s_full[2], p_ready[2], o_done[2];
-    uint64_t item_done[2], xchg, drained;
+    uint64_t item_full[kItems], item_empty[kItems], o_read[2], xchg, drained;
+    Item item[kItems];
     float2 ml[2][kTile];  // SPLIT: the chains' maxima and sums
-    int bad[2];           // the last item of this parity with non-finite values taken out of V
     volatile int abort;
     uint32_t tmem;
   };
@@ -234,16 +260,21 @@ struct Smem {
   static_assert(kBytes <= 232448, "more shared memory than a CTA has");
 };
 
-// ---- the walk over units ---------------------------------------------------------
-
-struct Item {
-  int b, h;
-  int tok0;         // the unit's first token in its sequence
-  int row_end;      // rows [0, row_end) are attended by some row of the unit
-  int t0, t1, cnt;  // tiles of this piece; of the whole unit
+// A place in a ring of N: its slot, and the parity of its turn.
+template <int N>
+struct Ring {
+  uint32_t slot = 0, turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      turn ^= 1;
+    }
+  }
 };
 
-// K/V tiles of the unit of tokens [tok0, tok0 + unit_tok) of sequence b.
+// ---- the walk over units ---------------------------------------------------------
+
+// Rows attended by some row of the unit of tokens [tok0, tok0 + unit_tok) of sequence b.
 template <typename P>
 __device__ __forceinline__ int unit_rows(const P& p, int b, int tok0) {
   const int n = p.seq.pre[b + 1] - p.seq.pre[b];
@@ -279,8 +310,10 @@ struct Walk {
     t = (int)rem;
   }
 
-  __device__ bool next(Item* it) {
-    if (pos >= end) return false;
+  template <bool PAIR>
+  __device__ void next(Item* it) {
+    it->n = 0;
+    if (pos >= end) return;
     if (!first) {
       tok0 += p.unit_tok;
       if (tok0 >= p.seq.pre[b + 1] - p.seq.pre[b]) {
@@ -293,15 +326,32 @@ struct Walk {
       t = 0;
     }
     first = false;
+    const int start = p.seq.start[b], at = p.seq.pre[b], n_tok = p.seq.pre[b + 1] - at;
+    const int row_end = unit_rows(p, b, tok0), cnt = (row_end + kTile - 1) / kTile;
+    const int n = (int)min((int64_t)(cnt - t), end - pos);
     it->b = b;
     it->h = h;
     it->tok0 = tok0;
-    it->row_end = unit_rows(p, b, tok0);
-    it->cnt = (it->row_end + kTile - 1) / kTile;
+    it->row_end = row_end;
     it->t0 = t;
-    it->t1 = (int)min((int64_t)it->cnt, t + (end - pos));
-    pos += it->t1 - it->t0;
-    return true;
+    it->n = n;
+    it->whole = t == 0 && n == cnt;
+    it->start = start;
+    it->n_tok = n_tok;
+    it->tok_at = at;
+    it->bad = 0;
+    it->masked = (p.is_tree ? start : start + tok0 + 1) / kTile;
+    if (PAIR) {
+      // chain 0's row tile may end earlier, chain 1's may be empty
+      const int tok1 = tok0 + p.tile_tok;
+      const int rows0 = p.is_tree ? row_end : start + min(tok1, n_tok);
+      it->nt[0] = max(0, min(t + n, (rows0 + kTile - 1) / kTile) - t);
+      it->nt[1] = tok1 < n_tok ? n : 0;
+    } else {
+      it->nt[0] = (n + 1) / 2;
+      it->nt[1] = n / 2;
+    }
+    pos += n;
   }
 };
 
@@ -310,32 +360,10 @@ __device__ __forceinline__ int64_t cut(const P& p, int i, int n) {
   return p.total / n * i + min((int64_t)i, p.total % n);
 }
 
-// The tiles of chain i in a piece: how many, and which is the j-th.
-template <bool PAIR, typename P>
-__device__ __forceinline__ int chain_tiles(const P& p, const Item& it, int i) {
-  if (!PAIR) return (it.t1 - it.t0 + 1 - i) / 2;
-  const int n = p.seq.pre[it.b + 1] - p.seq.pre[it.b];
-  const int tok = it.tok0 + i * p.tile_tok;
-  if (tok >= n) return 0;
-  if (p.is_tree) return it.t1 - it.t0;
-  const int rows = p.seq.start[it.b] + min(tok + p.tile_tok, n);
-  return max(0, min(it.t1, (rows + kTile - 1) / kTile) - it.t0);
-}
-// The place of the j-th K and V tile in the order of loads: PAIR K0 V0 K1 V1 ...,
-// SPLIT K0 K1 V0 K2 V1 K3 ... (the order in which the products take them).
-template <bool PAIR>
-__device__ __forceinline__ uint32_t k_place(int j) {
-  return PAIR ? 2 * j : j == 0 ? 0 : 2 * j - 1;
-}
-template <bool PAIR>
-__device__ __forceinline__ uint32_t v_place(int j, int n) {
-  return PAIR ? 2 * j + 1 : j + min(j + 2, n);
-}
-
 // ---- the kernel ------------------------------------------------------------------
 
-// Two 64-column masks of the row's attended columns of the tile at row col0.
-// Bit c of `bits`: new row c; rows before `start` are always attended.
+// 64-column masks of the columns a row attends.
+// Bit c of `bits`: new row c; rows before the new ones are always attended.
 __device__ __forceinline__ uint64_t tree_mask(uint64_t bits, int rel) {  // rel: column 0 - start
   if (rel <= -64) return ~0ull;
   if (rel < 0) return bits << -rel | ((1ull << -rel) - 1);
@@ -347,7 +375,41 @@ __device__ __forceinline__ uint64_t causal_mask(int last) {  // the last attende
 
 template <typename T>
 __device__ __forceinline__ constexpr uint32_t exp_mask() {
-  return sizeof(T) == 2 && std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+  return std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+}
+
+// (a, b) = (a, b) * c + d, and (a, b) += (c, d)
+__device__ __forceinline__ void fma2(float& a, float& b, float c, float d) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n"
+      " mov.b64 z, {%3, %3};\n fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n"
+      " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+// Adds to columns [k, k + 32) of a row's output the non-finite values of V
+// that were taken out of the piece's tiles and that the row attends.  Rare.
+template <typename T, typename P>
+__device__ __noinline__ void add_hidden(const P& p, const Item& it, uint64_t bits, int tok, int k,
+                                        uint32_t* o) {
+  const int64_t head = (int64_t)it.b * p.H + it.h;
+  const int row0 = max(it.masked, it.t0) * kTile;
+  const int row1 = min(it.row_end, (it.t0 + it.n) * kTile);
+  for (int row = row0; row < row1; ++row) {
+    if (row >= it.start && !(p.is_tree ? (bits >> (row - it.start) & 1) != 0 : row <= it.start + tok))
+      continue;
+    const uint16_t* v = p.v + (head * p.S + row) * p.D + k;
+    for (int e = 0; e < 32 && k + e < p.D; e += 2) {
+      const float2 f = Pack2<T>::unpack(*reinterpret_cast<const uint32_t*>(v + e));
+      if (!isfinite(f.x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f.x);
+      if (!isfinite(f.y)) o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) + f.y);
+    }
+  }
 }
 
 template <typename T, int DP, bool PAIR, int MAXB>
@@ -362,36 +424,42 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   }
   typename SM::Ctl& ctl = *reinterpret_cast<typename SM::Ctl*>(sm + SM::kCtl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const auto q_full = [&](int i) { return smem_u32(&ctl.q_full[i]); };
-  const auto q_empty = [&](int i) { return smem_u32(&ctl.q_empty[i]); };
-  const auto kv_full = [&](uint32_t n) { return smem_u32(&ctl.kv_full[n % SM::kSlots]); };
-  const auto kv_empty = [&](uint32_t n) { return smem_u32(&ctl.kv_empty[n % SM::kSlots]); };
-  const auto kv_addr = [&](uint32_t n) { return base + SM::kKv + (n % SM::kSlots) * SM::kSlot; };
-  const auto kv_parity = [&](uint32_t n) { return (n / SM::kSlots) & 1u; };
+  // a barrier's shared-memory address
+  const auto at = [&](const uint64_t& bar) {
+    return base + (uint32_t)(reinterpret_cast<const uint8_t*>(&bar) - sm);
+  };
   volatile int* const abort = &ctl.abort;
 
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&ctl.tmem)),
+                     base + (uint32_t)(reinterpret_cast<uint8_t*>(&ctl.tmem) - sm)),
                  "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      bar_init(q_full(i), 1);
-      bar_init(q_empty(i), 1);
-      bar_init(smem_u32(&ctl.s_full[i]), 1);
-      bar_init(smem_u32(&ctl.p_ready[i]), kTile);
-      bar_init(smem_u32(&ctl.o_done[i]), 1);
-      bar_init(smem_u32(&ctl.item_done[i]), 2 * kTile);
-      ctl.bad[i] = -1;
+      bar_init(at(ctl.q_full[i]), 1);
+      bar_init(at(ctl.q_empty[i]), 1);
+      bar_init(at(ctl.s_full[i]), 1);
+      bar_init(at(ctl.p_ready[i]), kTile);
+      bar_init(at(ctl.o_done[i]), 1);
+      bar_init(at(ctl.o_read[i]), 2 * kTile);
     }
-    for (int i = 0; i < SM::kSlots; ++i) {
-      bar_init(kv_full(i), 1);
-      bar_init(kv_empty(i), 1);
+    for (int i = 0; i < SM::kK; ++i) {
+      bar_init(at(ctl.k_full[i]), 1);
+      bar_init(at(ctl.k_empty[i]), 1);
     }
-    bar_init(smem_u32(&ctl.xchg), 2 * kTile);
-    bar_init(smem_u32(&ctl.drained), 1);
+    for (int i = 0; i < SM::kV; ++i) {
+      bar_init(at(ctl.v_full[i]), 1);
+      bar_init(at(ctl.v_ok[i]), 2);  // the two warps that look at hidden rows
+      bar_init(at(ctl.v_empty[i]), 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      bar_init(at(ctl.item_full[i]), 1);
+      bar_init(at(ctl.item_empty[i]), 11);  // 8 softmax warps, the products, warps 10 and 11
+    }
+    bar_init(at(ctl.xchg), 2 * kTile);
+    bar_init(at(ctl.drained), 1);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -400,295 +468,379 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   __syncthreads();
   fence_after();
   const uint32_t tmem = ctl.tmem;
-  Walk<AttnParams<MAXB>> walk(p, cut(p, blockIdx.x, gridDim.x), cut(p, blockIdx.x + 1, gridDim.x));
-  Item it;
   ops_pdl_enter();
 
-  if (warp == 8) {
-    // ---- loads ----
-    uint32_t n_loads = 0, n_q = 0, base_n = 0;
-    uint32_t q_used[2] = {0, 0};
-    bool ok = true;
-    while (ok && walk.next(&it)) {
-      const int n = it.t1 - it.t0;
-      const int64_t head = (int64_t)it.b * p.H + it.h;
-      for (int i = 0; i < (PAIR ? 2 : 1) && ok; ++i) {
-        if (PAIR && chain_tiles<PAIR>(p, it, i) == 0) continue;
-        const int qb = PAIR ? i : (int)(n_q & 1);
-        if (q_used[qb] > 0) ok = bar_wait(q_empty(qb), (q_used[qb] - 1) & 1, abort);
-        if (!ok) break;
-        ++q_used[qb];
-        ++n_q;
-        if (lane == 0) bar_expect(q_full(qb), (DP / 64) * 128 * p.G * p.tile_tok);
-        __syncwarp();
-        if (lane < DP / 64)
-          tma_load4(base + qb * SM::kQ + lane * (kTile * 128), &p.q_map, lane * 64, 0, it.h,
-                    p.seq.pre[it.b] + it.tok0 + i * p.tile_tok, q_full(qb));
-      }
-      for (int m = 0; m < 2 * n && ok; ++m) {
-        // the m-th load of the piece: K or V of which tile
-        int j;
-        bool is_k;
-        if (PAIR) {
-          j = m >> 1;
-          is_k = (m & 1) == 0;
-        } else {
-          is_k = m == 0 || (m & 1) != 0;
-          j = m == 0 ? 0 : is_k ? (m + 1) / 2 : m / 2 - 1;
-          if (m >= 2 && is_k && j >= n) {  // past the last K: the last V tile
-            is_k = false;
-            j = n - 1;
-          }
-          if (n == 1 && m == 1) {
-            is_k = false;
-            j = 0;
-          }
-        }
-        const uint32_t ld = base_n + m, bar = kv_full(ld), dst = kv_addr(ld);
-        if (ld >= SM::kSlots) ok = bar_wait(kv_empty(ld), kv_parity(ld) ^ 1, abort);
-        if (!ok) break;
-        n_loads = ld + 1;
-        const int row = (it.t0 + j) * kTile, rows = min(kTile, it.row_end - row);
-        if (is_k) {
-          const int chunks = p.C + (p.C & 1);
-          if (lane == 0) bar_expect(bar, p.C * rows * 16 + (p.C & 1) * (kTile * 16));
-          __syncwarp();
-          if (lane < p.C)
-            bulk_load(dst + lane * (kTile * 16), p.k + (head * p.C + lane) * p.S + row, rows * 16,
-                      bar);
-          else if (lane < chunks)
-            bulk_load(dst + lane * (kTile * 16), g_zero_rows, kTile * 16, bar);
-        } else {
+  // The k-th item, from the ring.
+  const auto get_item = [&](uint32_t k, Item* it) {
+    if (!bar_wait(at(ctl.item_full[k % kItems]), k / kItems & 1, abort)) return false;
+    *it = ctl.item[k % kItems];
+    return it->n > 0;
+  };
+
+  if (warp >= 8) {
+    if (warp == 8) {
+      // ---- the walk, and loads ----
+      if (lane == 0) {
+        Walk<AttnParams<MAXB>> walk(p, cut(p, blockIdx.x, gridDim.x),
+                                    cut(p, blockIdx.x + 1, gridDim.x));
+        Item it, after;
+        Ring<SM::kK> kr;
+        Ring<SM::kV> vr;
+        uint32_t nk = 0, nv = 0, q_used[2] = {0, 0}, n_items = 0;
+        bool ok = true;
+        const auto publish = [&](const Item& x) {
+          if (n_items >= kItems)
+            ok = bar_wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1, abort);
+          if (!ok) return;
+          ctl.item[n_items % kItems] = x;
+          bar_arrive(at(ctl.item_full[n_items % kItems]));
+          ++n_items;
+        };
+        const auto load_v = [&](int head, int row, int rows) {
+          const uint32_t bar = at(ctl.v_full[vr.slot]), dst = base + SM::kVAt + vr.slot * SM::kSlot;
+          if (nv >= SM::kV) ok = bar_wait(at(ctl.v_empty[vr.slot]), vr.turn ^ 1, abort);
+          if (!ok) return;
           const int boxes = (rows + 31) / 32;
-          if (lane == 0) bar_expect(bar, boxes * (DP / 64) * 4096);
-          __syncwarp();
-          const int half = lane & (DP / 64 - 1), box = lane / (DP / 64);
-          if (box < boxes)
-            tma_load3(dst + half * (kTile * 128) + box * 4096, &p.v_map, half * 64, row + box * 32,
-                      (int)head, bar);
-        }
-      }
-      base_n += 2 * n;
-    }
-    // A CTA that gave up leaves no copy in flight.
-    if (!ok) {
-      int never = 0;
-      for (uint32_t ld = n_loads > SM::kSlots ? n_loads - SM::kSlots : 0; ld < n_loads; ++ld)
-        bar_wait(kv_full(ld), kv_parity(ld), &never);
-      for (int i = 0; i < 2; ++i)
-        if (q_used[i] > 0) bar_wait(q_full(i), (q_used[i] - 1) & 1, &never);
-    }
-  } else if (warp == 9) {
-    // ---- products ----
-    if (lane == 0) {
-      constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
-      constexpr uint32_t kIdesc = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(kTile >> 4) << 24;
-      constexpr uint32_t kIdescS = kIdesc | (uint32_t)(kTile >> 3) << 17;
-      constexpr uint32_t kIdescO = kIdesc | 1u << 16 | (uint32_t)(DP >> 3) << 17;
-      const int steps = (p.C + 1) / 2;
-      uint32_t base_n = 0, n_q = 0, q_used[2] = {0, 0}, p_count[2] = {0, 0};
-      bool ok = true;
-      while (ok && walk.next(&it)) {
-        const int n = it.t1 - it.t0;
-        const int nt[2] = {chain_tiles<PAIR>(p, it, 0), chain_tiles<PAIR>(p, it, 1)};
-        const int qb_split = (int)(n_q & 1);
-        if (PAIR) {
-          for (int i = 0; i < 2; ++i)
-            if (nt[i] > 0) ++q_used[i];
-        } else {
-          ++q_used[qb_split];
-          ++n_q;
-        }
-        const int longest = max(nt[0], nt[1]);
-        // S_i = Q K_j^T into the chain's S columns
-        const auto qk = [&](int i, int j) {
-          const int tile = PAIR ? j : 2 * j + i;
-          const uint32_t ld = base_n + k_place<PAIR>(tile);
-          const int qb = PAIR ? i : qb_split;
-          if (j == 0 && !bar_wait(q_full(qb), (q_used[qb] - 1) & 1, abort)) return false;
-          if (!bar_wait(kv_full(ld), kv_parity(ld), abort)) return false;
-          fence_after();
-          const uint32_t qa = base + qb * SM::kQ, ka = kv_addr(ld);
-          for (int s = 0; s < steps; ++s)
-            mma_ss(tmem + i * kTile,
-                   smem_desc(qa + (s >> 2) * (kTile * 128) + (s & 3) * 32, 0, 1024, 2),
-                   smem_desc(ka + s * (2 * kTile * 16), kTile * 16, 128, 0), kIdescS, s > 0);
-          mma_commit(smem_u32(&ctl.s_full[i]));
-          if (!PAIR || i == 1 || j >= nt[1]) mma_commit(kv_empty(ld));
-          // the row tile's last use
-          if (j == nt[i] - 1 && (PAIR || tile == n - 1)) mma_commit(q_empty(qb));
-          return true;
-        };
-        const auto pv = [&](int i, int j) {
-          const int tile = PAIR ? j : 2 * j + i;
-          const uint32_t ld = base_n + v_place<PAIR>(tile, n);
-          if (!bar_wait(kv_full(ld), kv_parity(ld), abort)) return false;
-          if (!bar_wait(smem_u32(&ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
-          ++p_count[i];
-          fence_after();
-          const uint32_t va = kv_addr(ld);
-          const int rows = min(kTile, it.row_end - (it.t0 + tile) * kTile);
-          for (int s = 0; s * 16 < rows; ++s)
-            mma_ts(tmem + 2 * kTile + i * kTile, tmem + i * kTile + s * 8,
-                   smem_desc(va + s * 2048, kTile * 128, 1024, 2), kIdescO, j > 0 || s > 0);
-          if (!PAIR || i == 1 || j >= nt[1]) mma_commit(kv_empty(ld));
-          if (j == nt[i] - 1) mma_commit(smem_u32(&ctl.o_done[i]));
-          return true;
-        };
-        for (int i = 0; i < 2 && ok; ++i)
-          if (nt[i] > 0) ok = qk(i, 0);
-        for (int j = 0; j < longest && ok; ++j)
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j < nt[i]) ok = pv(i, j);
-            if (ok && j + 1 < nt[i]) ok = qk(i, j + 1);
+          bar_expect(bar, boxes * (DP / 64) * 4096);
+          for (int half = 0; half < DP / 64; ++half) {
+            if (boxes == 4)
+              tma_load3(dst + half * (kTile * 128), &p.v_map, half * 64, row, head, bar);
+            else
+              for (int x = 0; x < boxes; ++x)
+                tma_load3(dst + half * (kTile * 128) + x * 4096, &p.v_part, half * 64,
+                          row + x * 32, head, bar);
           }
-        base_n += 2 * n;
+          vr.next();
+          ++nv;
+        };
+        const auto load_k = [&](int head, int row, int rows) {
+          const uint32_t bar = at(ctl.k_full[kr.slot]), dst = base + SM::kKAt + kr.slot * SM::kSlot;
+          if (nk >= SM::kK) ok = bar_wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1, abort);
+          if (!ok) return;
+          const int pad = p.C & 1;  // zeros for the other half of the last contraction step
+          if (rows == kTile) {
+            bar_expect(bar, (p.C + pad) * (kTile * 16));
+            tma_load4(dst, &p.k_map, 0, row / p.k_rows, 0, head, bar);
+          } else {
+            bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16));
+            const uint4* src = p.k + (int64_t)head * p.C * p.S + row;
+            for (int c = 0; c < p.C; ++c)
+              bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar);
+          }
+          if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar);
+          kr.next();
+          ++nk;
+        };
+        walk.template next<PAIR>(&it);
+        publish(it);
+        uint32_t n_q = 0;
+        int v_head = 0, v_row = 0, v_rows = 0;  // the V tile that is due (none: v_rows 0)
+        while (ok && it.n > 0) {
+          walk.template next<PAIR>(&after);
+          publish(after);
+          if (ok && v_rows > 0) load_v(v_head, v_row, v_rows);
+          v_rows = 0;
+          for (int i = 0; i < (PAIR ? 2 : 1) && ok; ++i) {
+            if (it.nt[i] == 0) continue;
+            const int qb = PAIR ? i : (int)(n_q & 1);
+            if (q_used[qb] > 0) ok = bar_wait(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1, abort);
+            if (!ok) break;
+            ++q_used[qb];
+            ++n_q;
+            const uint32_t bar = at(ctl.q_full[qb]);
+            bar_expect(bar, (DP / 64) * 128 * p.G * p.tile_tok);
+            for (int half = 0; half < DP / 64; ++half)
+              tma_load4(base + qb * SM::kQ + half * (kTile * 128), &p.q_map, half * 64, 0, it.h,
+                        it.tok_at + it.tok0 + i * p.tile_tok, bar);
+          }
+          const int head = it.b * p.H + it.h;
+          for (int j = 0; j < it.n && ok; ++j) {
+            const int row = (it.t0 + j) * kTile, rows = min(kTile, it.row_end - row);
+            load_k(head, row, rows);
+            if (ok && v_rows > 0) load_v(v_head, v_row, v_rows);
+            v_head = head;
+            v_row = row;
+            v_rows = rows;
+          }
+          it = after;
+        }
+        if (ok && v_rows > 0) load_v(v_head, v_row, v_rows);
+        // A CTA that gave up leaves no copy in flight.
+        if (!ok) {
+          int never = 0;
+          for (uint32_t i = 0; i < SM::kK; ++i, kr.next())
+            if (nk > i) bar_wait(at(ctl.k_full[kr.slot]), nk >= SM::kK ? kr.turn ^ 1 : 0, &never);
+          for (uint32_t i = 0; i < SM::kV; ++i, vr.next())
+            if (nv > i) bar_wait(at(ctl.v_full[vr.slot]), nv >= SM::kV ? vr.turn ^ 1 : 0, &never);
+          for (int i = 0; i < 2; ++i)
+            if (q_used[i] > 0) bar_wait(at(ctl.q_full[i]), (q_used[i] - 1) & 1, &never);
+        }
       }
-      // the products that are in flight end before tensor memory is given back
-      int never = 0;
-      mma_commit(smem_u32(&ctl.drained));
-      bar_wait(smem_u32(&ctl.drained), 0, &never);
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---- products ----
+      if (lane == 0) {
+        constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
+        constexpr uint32_t kIdesc =
+            1u << 4 | kType << 7 | kType << 10 | (uint32_t)(kTile >> 4) << 24;
+        constexpr uint32_t kIdescS = kIdesc | (uint32_t)(kTile >> 3) << 17;
+        constexpr uint32_t kIdescO = kIdesc | 1u << 16 | (uint32_t)(DP >> 3) << 17;
+        const int steps = (p.C + 1) / 2;
+        Ring<SM::kK> kr, kr1;  // the next K and V tile; PAIR: chain 0's and chain 1's places
+        Ring<SM::kV> vr, vr1;
+        uint32_t n_items = 0, n_q = 0, q_used[2] = {0, 0}, p_count[2] = {0, 0};
+        bool ok = true;
+        Item it;
+        while (ok && get_item(n_items, &it)) {
+          const int qb_split = (int)(n_q & 1);
+          if (PAIR) {
+            for (int i = 0; i < 2; ++i)
+              if (it.nt[i] > 0) ++q_used[i];
+          } else {
+            ++q_used[qb_split];
+            ++n_q;
+          }
+          if (PAIR) {
+            kr1 = kr;
+            vr1 = vr;
+          }
+          // S_i = Q K_j^T into the chain's S columns
+          const auto qk = [&](int i, int j) {
+            const int qb = PAIR ? i : qb_split;
+            if (j == 0 && !bar_wait(at(ctl.q_full[qb]), (q_used[qb] - 1) & 1, abort)) return false;
+            Ring<SM::kK>& r = PAIR && i == 1 ? kr1 : kr;
+            if (!bar_wait(at(ctl.k_full[r.slot]), r.turn, abort)) return false;
+            fence_after();
+            const uint64_t qd = smem_desc(base + qb * SM::kQ, 0, 1024, 2);
+            const uint64_t kd =
+                smem_desc(base + SM::kKAt + r.slot * SM::kSlot, kTile * 16, 128, 0);
+            if (steps == DP / 16) {
+#pragma unroll
+              for (int s = 0; s < DP / 16; ++s)
+                mma_ss(tmem + i * kTile, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2,
+                       kd + s * (2 * kTile), kIdescS, s > 0);
+            } else {
+              for (int s = 0; s < steps; ++s)
+                mma_ss(tmem + i * kTile, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2,
+                       kd + s * (2 * kTile), kIdescS, s > 0);
+            }
+            mma_commit(at(ctl.s_full[i]));
+            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.k_empty[r.slot]));
+            // the row tile's last use
+            if (j == it.nt[i] - 1 && (PAIR || 2 * j + i == it.n - 1)) mma_commit(at(ctl.q_empty[qb]));
+            r.next();
+            return true;
+          };
+          const auto pv = [&](int i, int j) {
+            const int tile = it.t0 + (PAIR ? j : 2 * j + i);
+            Ring<SM::kV>& r = PAIR && i == 1 ? vr1 : vr;
+            if (!bar_wait(at(ctl.v_full[r.slot]), r.turn, abort)) return false;
+            if (!bar_wait(at(ctl.v_ok[r.slot]), r.turn, abort)) return false;
+            if (!bar_wait(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
+            ++p_count[i];
+            fence_after();
+            const uint64_t vd =
+                smem_desc(base + SM::kVAt + r.slot * SM::kSlot, kTile * 128, 1024, 2);
+            const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
+            const int rows = min(kTile, it.row_end - tile * kTile);
+            if (rows > kTile - 16) {
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0);
+            } else {
+              for (int s = 0; s * 16 < rows; ++s)
+                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0);
+            }
+            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.v_empty[r.slot]));
+            if (j == it.nt[i] - 1) mma_commit(at(ctl.o_done[i]));
+            r.next();
+            return true;
+          };
+          if (it.nt[0] > 0) ok = qk(0, 0);
+          if (ok && it.nt[1] > 0) ok = qk(1, 0);
+          const int longest = max(it.nt[0], it.nt[1]);
+          for (int j = 0; j < longest && ok; ++j) {
+            if (j < it.nt[0]) {
+              ok = pv(0, j);
+              if (ok && j + 1 < it.nt[0]) ok = qk(0, j + 1);
+            }
+            if (ok && j < it.nt[1]) {
+              ok = pv(1, j);
+              if (ok && j + 1 < it.nt[1]) ok = qk(1, j + 1);
+            }
+          }
+          if (PAIR && it.nt[1] == it.n) {  // chain 1 has gone through every tile
+            kr = kr1;
+            vr = vr1;
+          }
+          bar_arrive(at(ctl.item_empty[n_items % kItems]));
+          ++n_items;
+        }
+        // the products in flight end before tensor memory is given back
+        int never = 0;
+        mma_commit(at(ctl.drained));
+        bar_wait(at(ctl.drained), 0, &never);
+      }
+      __syncwarp();
+    } else {
+      // ---- V's hidden rows: zero past the last attended one, finite elsewhere ----
+      Ring<SM::kV> vr;
+      Item it;
+      bool ok = true;
+      for (uint32_t k = 0; ok && get_item(k, &it); ++k) {
+        for (int j = 0; j < it.n; ++j, vr.next()) {
+          if (!(ok = bar_wait(at(ctl.v_full[vr.slot]), vr.turn, abort))) break;
+          const int row0 = (it.t0 + j) * kTile;
+          if (it.t0 + j >= it.masked) {
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              const int r = x * 64 + (warp - 10) * 32 + lane;
+              uint4* const vrow = reinterpret_cast<uint4*>(sm + SM::kVAt + vr.slot * SM::kSlot + r * 128);
+              if (row0 + r >= it.row_end) {
+#pragma unroll
+                for (int c = 0; c < DP / 8; ++c)
+                  vrow[(c >> 3) * (kTile * 8) + ((c + r) & 7)] = make_uint4(0, 0, 0, 0);
+              } else {
+                constexpr uint32_t M = exp_mask<T>();
+                uint32_t bad = 0;
+#pragma unroll
+                for (int c = 0; c < DP / 8; ++c) {
+                  const uint4 u = vrow[(c >> 3) * (kTile * 8) + ((c + r) & 7)];
+                  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {  // a zero half-word of y: all exponent bits set
+                    const uint32_t y = (w[e] & M) ^ M;
+                    bad |= (y - 0x00010001u) & ~y & 0x80008000u;
+                  }
+                }
+                if (bad) {
+                  ctl.item[k % kItems].bad = 1;
+                  uint16_t* const e = reinterpret_cast<uint16_t*>(vrow);
+                  for (int c = 0; c < DP; ++c) {
+                    uint16_t& y = e[(c >> 6) * (kTile * 64) + (c & 63)];
+                    if ((y & (M & 0xffff)) == (M & 0xffff)) y = 0;
+                  }
+                }
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(at(ctl.v_ok[vr.slot]));
+        }
+        if (lane == 0) bar_arrive(at(ctl.item_empty[k % kItems]));
+      }
     }
-    __syncwarp();
   } else {
     // ---- softmax: a chain's warpgroup, a thread per row ----
     const int i = warp >> 2, r = threadIdx.x & (kTile - 1);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
     const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + 2 * kTile;
     const int tr = r / p.G, g = r - tr * p.G;
-    uint32_t base_n = 0, s_count = 0, o_count = 0, x_count = 0, item = 0;
+    uint32_t s_count = 0, o_count = 0, item = 0;
     bool ok = true;
-    for (; ok && walk.next(&it); ++item) {
-      const int n = it.t1 - it.t0;
-      const int nt[2] = {chain_tiles<PAIR>(p, it, 0), chain_tiles<PAIR>(p, it, 1)};
+    Item it;
+    for (; ok && get_item(item, &it); ++item) {
       const int tile_tok0 = it.tok0 + (PAIR ? i * p.tile_tok : 0);
-      const int start = p.seq.start[it.b], n_tok = p.seq.pre[it.b + 1] - p.seq.pre[it.b];
-      const int tok = tile_tok0 + tr;
-      const bool valid = tr < p.tile_tok && tok < n_tok;
+      const int tok = tile_tok0 + tr, nt = it.nt[i];
+      const bool valid = tr < p.tile_tok && tok < it.n_tok;
       const bool any_valid = __any_sync(~0u, valid);
       uint64_t bits = 0;
       if (p.is_tree && valid) {
-        bits = p.tree ? __ldg(p.tree + p.seq.pre[it.b] + tok) : causal_mask(tok);
-        if (n_tok < 64) bits &= (1ull << n_tok) - 1;
+        bits = p.tree ? __ldg(p.tree + it.tok_at + tok) : causal_mask(tok);
+        if (it.n_tok < 64) bits &= (1ull << it.n_tok) - 1;
       }
-      // the other chain may be an item behind, not more (PAIR: bad[]; SPLIT: O)
-      if (PAIR ? item >= 2 : item >= 1) {
-        const uint32_t w = item - (PAIR ? 2 : 1);
-        ok = bar_wait(smem_u32(&ctl.item_done[w & 1]), (w >> 1) & 1, abort);
-        if (!ok) break;
-      }
+      // the first tile that hides a column from some row of the chain's tile
+      const int masked = p.is_tree ? it.masked : (it.start + tile_tok0 + 1) / kTile;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < nt[i]; ++j) {
-        const int tile = PAIR ? j : 2 * j + i;
-        const int col0 = (it.t0 + tile) * kTile;
-        // whether some row of the tile does not attend every column
-        const bool masked = p.is_tree ? col0 + kTile > start : col0 + kTile > start + tile_tok0 + 1;
-        if (!(ok = bar_wait(smem_u32(&ctl.s_full[i]), s_count & 1, abort))) break;
+      for (int j = 0; j < nt; ++j) {
+        const int tile = it.t0 + (PAIR ? j : 2 * j + i);
+        if (!(ok = bar_wait(at(ctl.s_full[i]), s_count & 1, abort))) break;
         ++s_count;
         fence_after();
-        if (masked && (!PAIR || i == 0 || j >= nt[0])) {
-          // V's hidden rows: zero past the last attended one, finite elsewhere.  (The wait
-          // comes after S's: the products have then taken the slot's previous load, and the
-          // barrier is not two phases back.)
-          const uint32_t ld = base_n + v_place<PAIR>(tile, n);
-          if (!(ok = bar_wait(kv_full(ld), kv_parity(ld), abort))) break;
-          uint4* const vrow = reinterpret_cast<uint4*>(sm + (kv_addr(ld) - base) + r * 128);
-          if (col0 + r >= it.row_end) {
-#pragma unroll
-            for (int k = 0; k < DP / 8; ++k)
-              vrow[(k >> 3) * (kTile * 8) + ((k + r) & 7)] = make_uint4(0, 0, 0, 0);
-          } else {
-            constexpr uint32_t M = exp_mask<T>();
-            uint32_t bad = 0;
-#pragma unroll
-            for (int k = 0; k < DP / 8; ++k) {
-              const uint4 u = vrow[(k >> 3) * (kTile * 8) + ((k + r) & 7)];
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {  // a zero half-word of x: all exponent bits set
-                const uint32_t x = (w[e] & M) ^ M;
-                bad |= (x - 0x00010001u) & ~x & 0x80008000u;
-              }
-            }
-            if (bad) {
-              ctl.bad[item & 1] = (int)item;
-              uint16_t* const e = reinterpret_cast<uint16_t*>(vrow);
-              for (int k = 0; k < DP; ++k) {
-                uint16_t& x = e[(k >> 6) * (kTile * 64) + (k & 63)];
-                if ((x & (M & 0xffff)) == (M & 0xffff)) x = 0;
-              }
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         if (any_valid) {
           uint32_t x[kTile];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32(x + 32 * k, ts + 32 * k);
           tmem_wait_ld();
-          if (masked) {
-            const uint64_t lo = p.is_tree ? tree_mask(bits, col0 - start)
-                                          : causal_mask(start + tok - col0);
-            const uint64_t hi = p.is_tree ? tree_mask(bits, col0 + 64 - start)
-                                          : causal_mask(start + tok - col0 - 64);
+          if (tile >= masked) {
+            const int col0 = tile * kTile;
+            const uint64_t lo = p.is_tree ? tree_mask(bits, col0 - it.start)
+                                          : causal_mask(it.start + tok - col0);
+            const uint64_t hi = p.is_tree ? tree_mask(bits, col0 + 64 - it.start)
+                                          : causal_mask(it.start + tok - col0 - 64);
+            const uint32_t w[4] = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
+                                   (uint32_t)(hi >> 32)};
 #pragma unroll
             for (int k = 0; k < kTile; ++k)
-              if (!((k < 64 ? lo : hi) >> (k & 63) & 1)) x[k] = 0xff800000u;  // -inf
+              if (!(w[k >> 5] & (1u << (k & 31)))) x[k] = 0xff800000u;  // -inf
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[4] = {m, m, m, m};
 #pragma unroll
-          for (int k = 0; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[k]));
-          const float m_new = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+          for (int k = 0; k < kTile; k += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[k + 2 * e])), __uint_as_float(x[k + 2 * e + 1]));
+          const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           if (__any_sync(~0u, valid && (m_new - m) * p.c > kLazy)) {
             const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * p.c);
             m = m_new;
             l *= f;
             if (j > 0) {
-#pragma unroll
-              for (int k = 0; k < DP / 32; ++k) {
-                uint32_t o[32];
-                tmem_ld32(o, to + i * kTile + 32 * k);
+#pragma unroll 1
+              for (int k = 0; k < DP; k += 16) {
+                uint32_t o[16];
+                tmem_ld16(o, to + i * kTile + k);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(to + i * kTile + 32 * k, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(to + i * kTile + k, o);
               }
             }
           }
-          const float mb = m == -INFINITY ? 0.f : m * p.c;
+          const float mb = m == -INFINITY ? 0.f : -m * p.c;
           float sum[4] = {};
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t w[32];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float a = ex2(fmaf(__uint_as_float(x[64 * k + 2 * e]), p.c, -mb));
-              const float b = ex2(fmaf(__uint_as_float(x[64 * k + 2 * e + 1]), p.c, -mb));
-              sum[e & 3] += a + b;
+            for (int e = 0; e < 16; ++e) {
+              float a = __uint_as_float(x[32 * k + 2 * e]), b = __uint_as_float(x[32 * k + 2 * e + 1]);
+              fma2(a, b, p.c, mb);
+              a = ex2(a);
+              b = ex2(b);
+              add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], a, b);
               w[e] = Pack2<T>::pack(a, b);
             }
-            tmem_st32(ts + 32 * k, w);
+            tmem_st16(ts + 16 * k, w);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
+        // SPLIT: the other chain has read this chain's last O
+        if (!PAIR && j == 0 && item > 0) {
+          const uint32_t w = item - 1;
+          if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
+        }
         fence_before();
-        bar_arrive(smem_u32(&ctl.p_ready[i]));
+        bar_arrive(at(ctl.p_ready[i]));
       }
       if (!ok) break;
-      if (nt[i] > 0) {
-        if (!(ok = bar_wait(smem_u32(&ctl.o_done[i]), o_count & 1, abort))) break;
+      if (nt > 0) {
+        if (!(ok = bar_wait(at(ctl.o_done[i]), o_count & 1, abort))) break;
         ++o_count;
         fence_after();
       }
       float w0 = 1.f, w1 = 0.f;  // SPLIT: the chains' weights
       if (!PAIR) {
+        if (nt == 0 && item > 0) {  // (not waited for above)
+          const uint32_t w = item - 1;
+          if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
+        }
         ctl.ml[i][r] = make_float2(m, l);
         fence_before();
-        bar_arrive(smem_u32(&ctl.xchg));
-        if (!(ok = bar_wait(smem_u32(&ctl.xchg), x_count & 1, abort))) break;
-        ++x_count;
+        bar_arrive(at(ctl.xchg));
+        if (!(ok = bar_wait(at(ctl.xchg), item & 1, abort))) break;
         fence_after();  // the other chain's O has been waited for by its own threads
         const float2 a = ctl.ml[0][r], b = ctl.ml[1][r];
         m = fmaxf(a.x, b.x);
@@ -698,91 +850,73 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       }
       // ---- the piece's output: SPLIT each chain half of the columns ----
       if (any_valid) {
-        const bool whole = it.t0 == 0 && it.t1 == it.cnt;
-        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        const bool patch = ctl.bad[item & 1] == (int)item;
+        const bool whole = it.whole != 0;
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const bool patch = ctl.item[item % kItems].bad != 0;
         constexpr int kCols = PAIR ? DP : DP / 2;
         const int c0 = PAIR ? 0 : i * kCols;
-        const int hq = it.h * p.G + g;
-        uint16_t* const out =
-            p.out + (int64_t)(p.seq.pre[it.b] + tok) * p.out_stride + (int64_t)hq * p.D;
         // slot 0: the CTA's first piece, 1: its last
         constexpr int kRows = PAIR ? 2 * kTile : kTile;
-        float* const part = p.part + (int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kRows *
-                                         (p.D + 2);
+        float* const part =
+            p.part + (int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kRows * (p.D + 2);
         const int prow = (PAIR ? i * kTile : 0) + r;
+        uint16_t* const out = p.out + (int64_t)(it.tok_at + tok) * p.out_stride +
+                              (int64_t)(it.h * p.G + g) * p.D;
         if (!whole && valid && (PAIR || i == 0))
           reinterpret_cast<float2*>(part + kRows * p.D)[prow] = make_float2(m * p.c, l);
 #pragma unroll 1
-        for (int k = 0; k < kCols; k += 32) {
+        for (int k = c0; k < c0 + kCols; k += 32) {
+          if (k >= p.D) break;
           uint32_t o[32];
-          if (nt[PAIR ? i : 0] > 0) {
-            tmem_ld32(o, to + (PAIR ? i * kTile : 0) + c0 + k);
+          if (it.nt[PAIR ? i : 0] > 0) {
+            tmem_ld32(o, to + (PAIR ? i * kTile : 0) + k);
             tmem_wait_ld();
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0;
           }
           if (!PAIR) {
-            if (w0 != 1.f || w1 != 0.f) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                o[e] = __float_as_uint(w0 == 0.f ? 0.f : __uint_as_float(o[e]) * w0);
-            }
-            if (nt[1] > 0) {
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(w0 == 0.f ? 0.f : __uint_as_float(o[e]) * w0);
+            if (it.nt[1] > 0) {
               uint32_t o1[32];
-              tmem_ld32(o1, to + kTile + c0 + k);
+              tmem_ld32(o1, to + kTile + k);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (w1 != 0.f)
-                  o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+                o[e] = __float_as_uint(
+                    w1 == 0.f ? __uint_as_float(o[e])
+                              : fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
             }
           }
           if (valid) {
-            if (patch) {
-              // the non-finite values that the row does attend, from the cache
-              const int first = (p.is_tree ? start : start + it.tok0 + 1) / kTile * kTile;
-              const int64_t head = (int64_t)it.b * p.H + it.h;
-              for (int row = max(first, it.t0 * kTile); row < min(it.row_end, it.t1 * kTile); ++row) {
-                if (row >= start &&
-                    !(p.is_tree ? (bits >> (row - start) & 1) != 0 : row <= start + tok))
-                  continue;
-                const uint16_t* vr = p.v + (head * p.S + row) * p.D + c0 + k;
-                for (int e = 0; e < 32; e += 2) {
-                  if (c0 + k + e >= p.D) break;
-                  const float2 f = Pack2<T>::unpack(*reinterpret_cast<const uint32_t*>(vr + e));
+            if (patch) add_hidden<T>(p, it, bits, tok, k, o);
+            if (whole) {
+              uint32_t w[16];
 #pragma unroll
-                  for (int q = 0; q < 32; q += 2)
-                    if (q == e) {
-                      if (!isfinite(f.x)) o[q] = __float_as_uint(__uint_as_float(o[q]) + f.x);
-                      if (!isfinite(f.y)) o[q + 1] = __float_as_uint(__uint_as_float(o[q + 1]) + f.y);
-                    }
-                }
-              }
-            }
+              for (int e = 0; e < 16; ++e)
+                w[e] = Pack2<T>::pack(__uint_as_float(o[2 * e]) * inv,
+                                      __uint_as_float(o[2 * e + 1]) * inv);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              if (c0 + k + e >= p.D) break;
-              if (whole) {
-                uint32_t w[4];
+              for (int e = 0; e < 16; e += 4)
+                if (k + 2 * e < p.D)
+                  *reinterpret_cast<uint4*>(out + k + 2 * e) =
+                      make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            } else {
+              float* const d = part + (int64_t)prow * p.D + k;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  w[q] = Pack2<T>::pack(__uint_as_float(o[e + 2 * q]) * inv,
-                                        __uint_as_float(o[e + 2 * q + 1]) * inv);
-                *reinterpret_cast<uint4*>(out + c0 + k + e) = make_uint4(w[0], w[1], w[2], w[3]);
-              } else {
-                float* const d = part + (int64_t)prow * p.D + c0 + k + e;
-                *reinterpret_cast<uint4*>(d) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                *reinterpret_cast<uint4*>(d + 4) = make_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
-              }
+              for (int e = 0; e < 32; e += 4)
+                if (k + e < p.D)
+                  *reinterpret_cast<uint4*>(d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
         }
       }
       fence_before();
-      bar_arrive(smem_u32(&ctl.item_done[item & 1]));
-      base_n += 2 * n;
+      if (!PAIR) bar_arrive(at(ctl.o_read[item & 1]));
+      __syncwarp();
+      if (lane == 0) bar_arrive(at(ctl.item_empty[item % kItems]));
     }
   }
   fence_before();
@@ -908,12 +1042,13 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 bool encode(CUtensorMap* map, bool fp16, int rank, const void* base, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box) {
+            const cuuint64_t* strides, const cuuint32_t* box, bool swizzle) {
   static const EncodeFn fn = reinterpret_cast<EncodeFn>(driver_fn("cuTensorMapEncodeTiled"));
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   return fn && fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                   (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -943,8 +1078,21 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
   const cuuint32_t qb[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)s.tile_tok};
   const cuuint64_t vd[3] = {D, (cuuint64_t)p.S, (cuuint64_t)p.B * p.H};
   const cuuint64_t vs[2] = {D * 2, D * 2 * p.S};
-  const cuuint32_t vb[3] = {64, 32, 1};
-  if (!encode(&kp.q_map, fp16, 4, q.q, qd, qs, qb) || !encode(&kp.v_map, fp16, 3, v, vd, vs, vb))
+  const cuuint32_t vb[3] = {64, kTile, 1}, vp[3] = {64, 32, 1};
+  // A chunk row's S rows of 16 bytes are one run, so the copy's innermost run may be several
+  // rows: as many as divide S, up to the 256 elements a box may have.  (Rows one by one, for an
+  // odd S, make 8 times as many 16-byte pieces of a tile.)
+  int w = 32;
+  while (p.S % w != 0) w /= 2;
+  kp.k_rows = w;
+  const cuuint64_t kd[4] = {8 * (cuuint64_t)w, (cuuint64_t)p.S / w, (cuuint64_t)p.C,
+                            (cuuint64_t)p.B * p.H};
+  const cuuint64_t ks[3] = {16 * (cuuint64_t)w, 16 * (cuuint64_t)p.S, 16 * (cuuint64_t)p.S * p.C};
+  const cuuint32_t kb[4] = {8 * (cuuint32_t)w, (cuuint32_t)(kTile / w), (cuuint32_t)p.C, 1};
+  if (!encode(&kp.q_map, fp16, 4, q.q, qd, qs, qb, true) ||
+      !encode(&kp.k_map, fp16, 4, k, kd, ks, kb, false) ||
+      !encode(&kp.v_map, fp16, 3, v, vd, vs, vb, true) ||
+      !encode(&kp.v_part, fp16, 3, v, vd, vs, vp, true))
     return fail(DV_ERR_CUDA, "cuTensorMapEncodeTiled refused the queries or the cache");
   kp.out = static_cast<uint16_t*>(q.out);
   kp.k = static_cast<const uint4*>(k);
