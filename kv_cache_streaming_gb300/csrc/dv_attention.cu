@@ -88,10 +88,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
 }
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -121,49 +117,70 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   return bar_wait_long(bar, parity, abort);
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+// The load and the product warp run their loops as whole warps on uniform
+// values, and one elected lane (`on`) issues: descriptors and addresses then
+// stay in uniform registers, from where these instructions take them.
+__device__ __forceinline__ bool elect() {
+  uint32_t on;
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(on));
+  return on != 0;
+}
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(~0u, bar_wait(bar, parity, abort));
+}
+#define DV_ON(n) "{\n .reg .pred q;\n setp.ne.b32 q, %" #n ", 0;\n @q "
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes, bool on) {
+  asm volatile(DV_ON(2) "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
+               "r"(bytes), "r"((uint32_t)on)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar, bool on) {
+  asm volatile(DV_ON(4)
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}" ::
+          "r"(dst), "l"(src), "r"(bytes), "r"(bar), "r"((uint32_t)on)
       : "memory");
 }
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                          uint32_t bar) {
-  asm volatile(
+                                          uint32_t bar, bool on) {
+  asm volatile(DV_ON(6)
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "[%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar),
+      "r"((uint32_t)on)
       : "memory");
 }
 __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                          int w, uint32_t bar) {
-  asm volatile(
+                                          int w, uint32_t bar, bool on) {
+  asm volatile(DV_ON(7)
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w),
-      "r"(bar)
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];\n}" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w),
+      "r"(bar), "r"((uint32_t)on)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc,
+                                       bool on) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
-      "r"(idesc), "r"((uint32_t)acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
+      "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)on)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc,
+                                       bool on) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b),
-      "r"(idesc), "r"((uint32_t)acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b),
+      "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)on)
       : "memory");
 }
 // Arrives on `bar` once every product issued so far has finished.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+__device__ __forceinline__ void mma_commit(uint32_t bar, bool on) {
+  asm volatile(DV_ON(1)
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"((uint32_t)on)
       : "memory");
 }
 __device__ __forceinline__ void fence_before() {
@@ -392,26 +409,6 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
       : "f"(c), "f"(d));
 }
 
-// Adds to columns [k, k + 32) of a row's output the non-finite values of V
-// that were taken out of the piece's tiles and that the row attends.  Rare.
-template <typename T, typename P>
-__device__ __noinline__ void add_hidden(const P& p, const Item& it, uint64_t bits, int tok, int k,
-                                        uint32_t* o) {
-  const int64_t head = (int64_t)it.b * p.H + it.h;
-  const int row0 = max(it.masked, it.t0) * kTile;
-  const int row1 = min(it.row_end, (it.t0 + it.n) * kTile);
-  for (int row = row0; row < row1; ++row) {
-    if (row >= it.start && !(p.is_tree ? (bits >> (row - it.start) & 1) != 0 : row <= it.start + tok))
-      continue;
-    const uint16_t* v = p.v + (head * p.S + row) * p.D + k;
-    for (int e = 0; e < 32 && k + e < p.D; e += 2) {
-      const float2 f = Pack2<T>::unpack(*reinterpret_cast<const uint32_t*>(v + e));
-      if (!isfinite(f.x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f.x);
-      if (!isfinite(f.y)) o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) + f.y);
-    }
-  }
-}
-
 template <typename T, int DP, bool PAIR, int MAXB>
 __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     const __grid_constant__ AttnParams<MAXB> p) {
@@ -423,7 +420,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     return;
   }
   typename SM::Ctl& ctl = *reinterpret_cast<typename SM::Ctl*>(sm + SM::kCtl);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // a barrier's shared-memory address
   const auto at = [&](const uint64_t& bar) {
     return base + (uint32_t)(reinterpret_cast<const uint8_t*>(&bar) - sm);
@@ -467,7 +464,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = __shfl_sync(~0u, ctl.tmem, 0);
   ops_pdl_enter();
 
   // The k-th item, from the ring.
@@ -480,7 +477,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   if (warp >= 8) {
     if (warp == 8) {
       // ---- the walk, and loads ----
-      if (lane == 0) {
+      {
+        const bool on = elect();
         Walk<AttnParams<MAXB>> walk(p, cut(p, blockIdx.x, gridDim.x),
                                     cut(p, blockIdx.x + 1, gridDim.x));
         Item it, after;
@@ -490,44 +488,47 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         bool ok = true;
         const auto publish = [&](const Item& x) {
           if (n_items >= kItems)
-            ok = bar_wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1, abort);
+            ok = bar_wait_warp(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1,
+                               abort);
           if (!ok) return;
-          ctl.item[n_items % kItems] = x;
-          bar_arrive(at(ctl.item_full[n_items % kItems]));
+          if (on) {
+            ctl.item[n_items % kItems] = x;
+            bar_arrive(at(ctl.item_full[n_items % kItems]));
+          }
           ++n_items;
         };
         const auto load_v = [&](int head, int row, int rows) {
           const uint32_t bar = at(ctl.v_full[vr.slot]), dst = base + SM::kVAt + vr.slot * SM::kSlot;
-          if (nv >= SM::kV) ok = bar_wait(at(ctl.v_empty[vr.slot]), vr.turn ^ 1, abort);
+          if (nv >= SM::kV) ok = bar_wait_warp(at(ctl.v_empty[vr.slot]), vr.turn ^ 1, abort);
           if (!ok) return;
           const int boxes = (rows + 31) / 32;
-          bar_expect(bar, boxes * (DP / 64) * 4096);
+          bar_expect(bar, boxes * (DP / 64) * 4096, on);
           for (int half = 0; half < DP / 64; ++half) {
             if (boxes == 4)
-              tma_load3(dst + half * (kTile * 128), &p.v_map, half * 64, row, head, bar);
+              tma_load3(dst + half * (kTile * 128), &p.v_map, half * 64, row, head, bar, on);
             else
               for (int x = 0; x < boxes; ++x)
                 tma_load3(dst + half * (kTile * 128) + x * 4096, &p.v_part, half * 64,
-                          row + x * 32, head, bar);
+                          row + x * 32, head, bar, on);
           }
           vr.next();
           ++nv;
         };
         const auto load_k = [&](int head, int row, int rows) {
           const uint32_t bar = at(ctl.k_full[kr.slot]), dst = base + SM::kKAt + kr.slot * SM::kSlot;
-          if (nk >= SM::kK) ok = bar_wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1, abort);
+          if (nk >= SM::kK) ok = bar_wait_warp(at(ctl.k_empty[kr.slot]), kr.turn ^ 1, abort);
           if (!ok) return;
           const int pad = p.C & 1;  // zeros for the other half of the last contraction step
           if (rows == kTile) {
-            bar_expect(bar, (p.C + pad) * (kTile * 16));
-            tma_load4(dst, &p.k_map, 0, row / p.k_rows, 0, head, bar);
+            bar_expect(bar, (p.C + pad) * (kTile * 16), on);
+            tma_load4(dst, &p.k_map, 0, row / p.k_rows, 0, head, bar, on);
           } else {
-            bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16));
+            bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
             const uint4* src = p.k + (int64_t)head * p.C * p.S + row;
             for (int c = 0; c < p.C; ++c)
-              bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar);
+              bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar, on);
           }
-          if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar);
+          if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar, on);
           kr.next();
           ++nk;
         };
@@ -543,15 +544,15 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           for (int i = 0; i < (PAIR ? 2 : 1) && ok; ++i) {
             if (it.nt[i] == 0) continue;
             const int qb = PAIR ? i : (int)(n_q & 1);
-            if (q_used[qb] > 0) ok = bar_wait(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1, abort);
+            if (q_used[qb] > 0) ok = bar_wait_warp(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1, abort);
             if (!ok) break;
             ++q_used[qb];
             ++n_q;
             const uint32_t bar = at(ctl.q_full[qb]);
-            bar_expect(bar, (DP / 64) * 128 * p.G * p.tile_tok);
+            bar_expect(bar, (DP / 64) * 128 * p.G * p.tile_tok, on);
             for (int half = 0; half < DP / 64; ++half)
               tma_load4(base + qb * SM::kQ + half * (kTile * 128), &p.q_map, half * 64, 0, it.h,
-                        it.tok_at + it.tok0 + i * p.tile_tok, bar);
+                        it.tok_at + it.tok0 + i * p.tile_tok, bar, on);
           }
           const int head = it.b * p.H + it.h;
           for (int j = 0; j < it.n && ok; ++j) {
@@ -568,10 +569,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         // A CTA that gave up leaves no copy in flight.
         if (!ok) {
           int never = 0;
-          for (uint32_t i = 0; i < SM::kK; ++i, kr.next())
-            if (nk > i) bar_wait(at(ctl.k_full[kr.slot]), nk >= SM::kK ? kr.turn ^ 1 : 0, &never);
-          for (uint32_t i = 0; i < SM::kV; ++i, vr.next())
-            if (nv > i) bar_wait(at(ctl.v_full[vr.slot]), nv >= SM::kV ? vr.turn ^ 1 : 0, &never);
+          for (uint32_t i = 0; i < SM::kK && i < nk; ++i)  // a slot's last use
+            bar_wait(at(ctl.k_full[i]), (nk - i - 1) / SM::kK & 1, &never);
+          for (uint32_t i = 0; i < SM::kV && i < nv; ++i)
+            bar_wait(at(ctl.v_full[i]), (nv - i - 1) / SM::kV & 1, &never);
           for (int i = 0; i < 2; ++i)
             if (q_used[i] > 0) bar_wait(at(ctl.q_full[i]), (q_used[i] - 1) & 1, &never);
         }
@@ -579,7 +580,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       __syncwarp();
     } else if (warp == 9) {
       // ---- products ----
-      if (lane == 0) {
+      {
+        const bool on = elect();
         constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
         constexpr uint32_t kIdesc =
             1u << 4 | kType << 7 | kType << 10 | (uint32_t)(kTile >> 4) << 24;
@@ -591,7 +593,12 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         uint32_t n_items = 0, n_q = 0, q_used[2] = {0, 0}, p_count[2] = {0, 0};
         bool ok = true;
         Item it;
-        while (ok && get_item(n_items, &it)) {
+        while (ok && __all_sync(~0u, get_item(n_items, &it))) {
+          it.n = __shfl_sync(~0u, it.n, 0);
+          it.t0 = __shfl_sync(~0u, it.t0, 0);
+          it.nt[0] = __shfl_sync(~0u, it.nt[0], 0);
+          it.nt[1] = __shfl_sync(~0u, it.nt[1], 0);
+          it.row_end = __shfl_sync(~0u, it.row_end, 0);
           const int qb_split = (int)(n_q & 1);
           if (PAIR) {
             for (int i = 0; i < 2; ++i)
@@ -607,9 +614,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           // S_i = Q K_j^T into the chain's S columns
           const auto qk = [&](int i, int j) {
             const int qb = PAIR ? i : qb_split;
-            if (j == 0 && !bar_wait(at(ctl.q_full[qb]), (q_used[qb] - 1) & 1, abort)) return false;
+            if (j == 0 && !bar_wait_warp(at(ctl.q_full[qb]), (q_used[qb] - 1) & 1, abort)) return false;
             Ring<SM::kK>& r = PAIR && i == 1 ? kr1 : kr;
-            if (!bar_wait(at(ctl.k_full[r.slot]), r.turn, abort)) return false;
+            if (!bar_wait_warp(at(ctl.k_full[r.slot]), r.turn, abort)) return false;
             fence_after();
             const uint64_t qd = smem_desc(base + qb * SM::kQ, 0, 1024, 2);
             const uint64_t kd =
@@ -618,25 +625,25 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll
               for (int s = 0; s < DP / 16; ++s)
                 mma_ss(tmem + i * kTile, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2,
-                       kd + s * (2 * kTile), kIdescS, s > 0);
+                       kd + s * (2 * kTile), kIdescS, s > 0, on);
             } else {
               for (int s = 0; s < steps; ++s)
                 mma_ss(tmem + i * kTile, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2,
-                       kd + s * (2 * kTile), kIdescS, s > 0);
+                       kd + s * (2 * kTile), kIdescS, s > 0, on);
             }
-            mma_commit(at(ctl.s_full[i]));
-            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.k_empty[r.slot]));
+            mma_commit(at(ctl.s_full[i]), on);
+            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.k_empty[r.slot]), on);
             // the row tile's last use
-            if (j == it.nt[i] - 1 && (PAIR || 2 * j + i == it.n - 1)) mma_commit(at(ctl.q_empty[qb]));
+            if (j == it.nt[i] - 1 && (PAIR || 2 * j + i == it.n - 1)) mma_commit(at(ctl.q_empty[qb]), on);
             r.next();
             return true;
           };
           const auto pv = [&](int i, int j) {
             const int tile = it.t0 + (PAIR ? j : 2 * j + i);
             Ring<SM::kV>& r = PAIR && i == 1 ? vr1 : vr;
-            if (!bar_wait(at(ctl.v_full[r.slot]), r.turn, abort)) return false;
-            if (!bar_wait(at(ctl.v_ok[r.slot]), r.turn, abort)) return false;
-            if (!bar_wait(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
+            if (!bar_wait_warp(at(ctl.v_full[r.slot]), r.turn, abort)) return false;
+            if (!bar_wait_warp(at(ctl.v_ok[r.slot]), r.turn, abort)) return false;
+            if (!bar_wait_warp(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
             ++p_count[i];
             fence_after();
             const uint64_t vd =
@@ -646,13 +653,13 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             if (rows > kTile - 16) {
 #pragma unroll
               for (int s = 0; s < kTile / 16; ++s)
-                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0);
+                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0, on);
             } else {
               for (int s = 0; s * 16 < rows; ++s)
-                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0);
+                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0, on);
             }
-            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.v_empty[r.slot]));
-            if (j == it.nt[i] - 1) mma_commit(at(ctl.o_done[i]));
+            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.v_empty[r.slot]), on);
+            if (j == it.nt[i] - 1) mma_commit(at(ctl.o_done[i]), on);
             r.next();
             return true;
           };
@@ -673,12 +680,12 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             kr = kr1;
             vr = vr1;
           }
-          bar_arrive(at(ctl.item_empty[n_items % kItems]));
+          if (on) bar_arrive(at(ctl.item_empty[n_items % kItems]));
           ++n_items;
         }
         // the products in flight end before tensor memory is given back
         int never = 0;
-        mma_commit(at(ctl.drained));
+        mma_commit(at(ctl.drained), on);
         bar_wait(at(ctl.drained), 0, &never);
       }
       __syncwarp();
@@ -891,7 +898,26 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             }
           }
           if (valid) {
-            if (patch) add_hidden<T>(p, it, bits, tok, k, o);
+            if (patch) {
+              // the non-finite values taken out of V that the row does attend
+              const uint16_t* const v =
+                  p.v + ((int64_t)it.b * p.H + it.h) * p.S * (int64_t)p.D + k;
+              const int row1 = min(it.row_end, (it.t0 + it.n) * kTile);
+#pragma unroll 1
+              for (int row = max(it.masked, it.t0) * kTile; row < row1; ++row) {
+                if (row >= it.start && !(p.is_tree ? (bits >> (row - it.start) & 1) != 0
+                                                   : row <= it.start + tok))
+                  continue;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                  if (k + e < p.D) {
+                    const float2 f = Pack2<T>::unpack(
+                        *reinterpret_cast<const uint32_t*>(v + (int64_t)row * p.D + e));
+                    if (!isfinite(f.x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f.x);
+                    if (!isfinite(f.y)) o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) + f.y);
+                  }
+              }
+            }
             if (whole) {
               uint32_t w[16];
 #pragma unroll
