@@ -681,7 +681,7 @@ dv_status dv_attention_workspace(const dv_cache* cache, const int32_t* seq_start
  * are rounded to `dtype` before they multiply v, the output once.  Rows that
  * a token does not attend have no effect on it, whatever they hold (NaN and
  * infinities included).  head_dim a multiple of 8 up to 128, elem_bytes 2
- * (else DV_ERR_UNSUPPORTED).  `workspace`: device memory, 16-byte aligned,
+ * (else DV_ERR_UNSUPPORTED).  `workspace`: device memory, 32-byte aligned,
  * of dv_attention_workspace bytes (NULL when that is 0), for this call alone
  * until the stream has passed it; it needs no initial value. */
 dv_status dv_prompt_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,

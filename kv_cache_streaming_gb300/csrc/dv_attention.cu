@@ -28,7 +28,7 @@
 // is read with its rows as the contraction.  A sequence's last, partial tile is
 // fetched up to the last attended row (K in bulk copies, V in 32s).
 //
-// The tiles of all units form one line, cut into equal stretches, one for
+// The units form one line, each as long as its cost, cut into equal stretches, one for
 // each CTA (one CTA an SM); a unit that a cut divides leaves partial sums in
 // the workspace, which join_kernel adds up.
 //
@@ -69,12 +69,14 @@ struct AttnParams {
   const uint64_t* tree;
   float* part;
   int64_t out_stride;
-  int64_t total;  // tiles of all units
+  int64_t total;  // cost of all units
   int32_t H, G, D, C, S;
   int32_t k_rows;    // w of k_map
   int32_t tile_tok;  // tokens of a row tile: 128 / G
   int32_t unit_tok;  // tokens of a unit
+  int32_t unit_cost;  // in tiles, on top of a unit's tiles
   int32_t is_tree;
+  int32_t wide;  // every output row of a head is 32-byte aligned, of whole 32-byte sectors
   float c;  // scale * log2(e)
   SeqTable<MAXB> seq;
   int64_t tile_pre[MAXB + 1];
@@ -102,6 +104,8 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// The rest of a wait, out of line: inlined at each of its thirty places (and
+// with a vote of the warp) it made the kernel 1.1 to 1.5 times slower, by the size of the code.
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort) {
   for (uint32_t i = 0; i < kSpinLimit; ++i) {
     if (bar_try(bar, parity)) return true;
@@ -116,7 +120,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   if (bar_try(bar, parity)) return true;
   return bar_wait_long(bar, parity, abort);
 }
-
 // The load and the product warp run their loops as whole warps on uniform
 // values, and one elected lane (`on`) issues: descriptors and addresses then
 // stay in uniform registers, from where these instructions take them.
@@ -126,9 +129,6 @@ __device__ __forceinline__ bool elect() {
       "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(on));
   return on != 0;
-}
-__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(~0u, bar_wait(bar, parity, abort));
 }
 #define DV_ON(n) "{\n .reg .pred q;\n setp.ne.b32 q, %" #n ", 0;\n @q "
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes, bool on) {
@@ -225,6 +225,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* a) {
       : "memory");
 }
 
+// 32 bytes to a 32-byte aligned place.
+__device__ __forceinline__ void st32(void* dst, const uint32_t* a) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), DV_W8(a, 0)
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -266,7 +272,7 @@ struct Smem {
   struct Ctl {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kK], k_empty[kK], v_full[kV], v_ok[kV], v_empty[kV];
-    uint64_t s_full[2], p_ready[2], o_done[2];
+    uint64_t s_full[2], p_half[2], p_ready[2], o_done[2];
     uint64_t item_full[kItems], item_empty[kItems], o_read[2], xchg, drained;
     Item item[kItems];
     float2 ml[2][kTile];  // SPLIT: the chains' maxima and sums
@@ -301,11 +307,10 @@ __device__ __forceinline__ int unit_rows(const P& p, int b, int tok0) {
 template <typename P>
 struct Walk {
   const P& p;
-  int64_t pos, end;
+  int64_t pos, end;   // where the unit starts on the line of costs; where the CTA's stretch ends
   int b, h, tok0, t;  // the next piece: its unit and first tile
-  bool first;
 
-  __device__ Walk(const P& p_, int64_t lo, int64_t hi) : p(p_), pos(lo), end(hi), first(true) {
+  __device__ Walk(const P& p_, int64_t lo, int64_t hi) : p(p_), pos(lo), end(hi) {
     b = h = tok0 = t = 0;
     if (lo >= hi) return;
     int x = 0, y = p.seq.batch;
@@ -319,33 +324,24 @@ struct Walk {
     h = (int)(rem / head);
     rem -= h * head;
     for (;;) {
-      const int cnt = (unit_rows(p, b, tok0) + kTile - 1) / kTile;
-      if (rem < cnt) break;
-      rem -= cnt;
+      const int cost = p.unit_cost + (unit_rows(p, b, tok0) + kTile - 1) / kTile;
+      if (rem < cost) break;
+      rem -= cost;
       tok0 += p.unit_tok;
     }
-    t = (int)rem;
+    pos = lo - rem;
+    t = max(0, (int)rem - p.unit_cost);
   }
 
   template <bool PAIR>
   __device__ void next(Item* it) {
     it->n = 0;
     if (pos >= end) return;
-    if (!first) {
-      tok0 += p.unit_tok;
-      if (tok0 >= p.seq.pre[b + 1] - p.seq.pre[b]) {
-        tok0 = 0;
-        if (++h == p.H) {
-          h = 0;
-          do ++b; while (p.seq.pre[b + 1] == p.seq.pre[b]);
-        }
-      }
-      t = 0;
-    }
-    first = false;
     const int start = p.seq.start[b], at = p.seq.pre[b], n_tok = p.seq.pre[b + 1] - at;
     const int row_end = unit_rows(p, b, tok0), cnt = (row_end + kTile - 1) / kTile;
-    const int n = (int)min((int64_t)(cnt - t), end - pos);
+    const int64_t left = end - pos - p.unit_cost;  // tiles of the unit before the end
+    const int n = (int)min((int64_t)cnt, left) - t;
+    if (n <= 0) return;
     it->b = b;
     it->h = h;
     it->tok0 = tok0;
@@ -368,7 +364,16 @@ struct Walk {
       it->nt[0] = (n + 1) / 2;
       it->nt[1] = n / 2;
     }
-    pos += n;
+    pos += p.unit_cost + cnt;
+    t = 0;
+    tok0 += p.unit_tok;
+    if (tok0 >= n_tok) {
+      tok0 = 0;
+      if (++h == p.H) {
+        h = 0;
+        if (pos < end) do ++b; while (p.seq.pre[b + 1] == p.seq.pre[b]);
+      }
+    }
   }
 };
 
@@ -438,6 +443,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       bar_init(at(ctl.q_full[i]), 1);
       bar_init(at(ctl.q_empty[i]), 1);
       bar_init(at(ctl.s_full[i]), 1);
+      bar_init(at(ctl.p_half[i]), kTile);
       bar_init(at(ctl.p_ready[i]), kTile);
       bar_init(at(ctl.o_done[i]), 1);
       bar_init(at(ctl.o_read[i]), 2 * kTile);
@@ -471,7 +477,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   const auto get_item = [&](uint32_t k, Item* it) {
     if (!bar_wait(at(ctl.item_full[k % kItems]), k / kItems & 1, abort)) return false;
     *it = ctl.item[k % kItems];
-    return it->n > 0;
+    return __all_sync(~0u, it->n > 0) != 0;
   };
 
   if (warp >= 8) {
@@ -488,7 +494,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         bool ok = true;
         const auto publish = [&](const Item& x) {
           if (n_items >= kItems)
-            ok = bar_wait_warp(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1,
+            ok = bar_wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1,
                                abort);
           if (!ok) return;
           if (on) {
@@ -499,7 +505,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         };
         const auto load_v = [&](int head, int row, int rows) {
           const uint32_t bar = at(ctl.v_full[vr.slot]), dst = base + SM::kVAt + vr.slot * SM::kSlot;
-          if (nv >= SM::kV) ok = bar_wait_warp(at(ctl.v_empty[vr.slot]), vr.turn ^ 1, abort);
+          if (nv >= SM::kV) ok = bar_wait(at(ctl.v_empty[vr.slot]), vr.turn ^ 1, abort);
           if (!ok) return;
           const int boxes = (rows + 31) / 32;
           bar_expect(bar, boxes * (DP / 64) * 4096, on);
@@ -516,7 +522,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         };
         const auto load_k = [&](int head, int row, int rows) {
           const uint32_t bar = at(ctl.k_full[kr.slot]), dst = base + SM::kKAt + kr.slot * SM::kSlot;
-          if (nk >= SM::kK) ok = bar_wait_warp(at(ctl.k_empty[kr.slot]), kr.turn ^ 1, abort);
+          if (nk >= SM::kK) ok = bar_wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1, abort);
           if (!ok) return;
           const int pad = p.C & 1;  // zeros for the other half of the last contraction step
           if (rows == kTile) {
@@ -532,27 +538,29 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           kr.next();
           ++nk;
         };
+        uint32_t n_q = 0;
+        const auto load_q = [&](const Item& x, int i) {
+          const int qb = PAIR ? i : (int)(n_q & 1);
+          if (q_used[qb] > 0) ok = bar_wait(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1, abort);
+          if (!ok) return;
+          ++q_used[qb];
+          ++n_q;
+          const uint32_t bar = at(ctl.q_full[qb]);
+          bar_expect(bar, (DP / 64) * 128 * p.G * p.tile_tok, on);
+          for (int half = 0; half < DP / 64; ++half)
+            tma_load4(base + qb * SM::kQ + half * (kTile * 128), &p.q_map, half * 64, 0, x.h,
+                      x.tok_at + x.tok0 + i * p.tile_tok, bar, on);
+        };
         walk.template next<PAIR>(&it);
         publish(it);
-        uint32_t n_q = 0;
+        if (!PAIR && it.n > 0) load_q(it, 0);
         int v_head = 0, v_row = 0, v_rows = 0;  // the V tile that is due (none: v_rows 0)
         while (ok && it.n > 0) {
-          walk.template next<PAIR>(&after);
-          publish(after);
-          if (ok && v_rows > 0) load_v(v_head, v_row, v_rows);
-          v_rows = 0;
-          for (int i = 0; i < (PAIR ? 2 : 1) && ok; ++i) {
-            if (it.nt[i] == 0) continue;
-            const int qb = PAIR ? i : (int)(n_q & 1);
-            if (q_used[qb] > 0) ok = bar_wait_warp(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1, abort);
-            if (!ok) break;
-            ++q_used[qb];
-            ++n_q;
-            const uint32_t bar = at(ctl.q_full[qb]);
-            bar_expect(bar, (DP / 64) * 128 * p.G * p.tile_tok, on);
-            for (int half = 0; half < DP / 64; ++half)
-              tma_load4(base + qb * SM::kQ + half * (kTile * 128), &p.q_map, half * 64, 0, it.h,
-                        it.tok_at + it.tok0 + i * p.tile_tok, bar, on);
+          if (PAIR) {  // the row tiles' buffers are free once the unit before has used them up,
+            if (v_rows > 0) load_v(v_head, v_row, v_rows);  // which takes its last V
+            v_rows = 0;
+            for (int i = 0; i < 2 && ok; ++i)
+              if (it.nt[i] > 0) load_q(it, i);
           }
           const int head = it.b * p.H + it.h;
           for (int j = 0; j < it.n && ok; ++j) {
@@ -562,6 +570,11 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             v_head = head;
             v_row = row;
             v_rows = rows;
+            if (j == 0 && ok) {  // ahead of need: the next unit, SPLIT its queries
+              walk.template next<PAIR>(&after);
+              publish(after);
+              if (!PAIR && ok && after.n > 0) load_q(after, 0);
+            }
           }
           it = after;
         }
@@ -593,7 +606,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         uint32_t n_items = 0, n_q = 0, q_used[2] = {0, 0}, p_count[2] = {0, 0};
         bool ok = true;
         Item it;
-        while (ok && __all_sync(~0u, get_item(n_items, &it))) {
+        while (ok && get_item(n_items, &it)) {
           it.n = __shfl_sync(~0u, it.n, 0);
           it.t0 = __shfl_sync(~0u, it.t0, 0);
           it.nt[0] = __shfl_sync(~0u, it.nt[0], 0);
@@ -614,9 +627,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           // S_i = Q K_j^T into the chain's S columns
           const auto qk = [&](int i, int j) {
             const int qb = PAIR ? i : qb_split;
-            if (j == 0 && !bar_wait_warp(at(ctl.q_full[qb]), (q_used[qb] - 1) & 1, abort)) return false;
+            if (j == 0 && !bar_wait(at(ctl.q_full[qb]), (q_used[qb] - 1) & 1, abort)) return false;
             Ring<SM::kK>& r = PAIR && i == 1 ? kr1 : kr;
-            if (!bar_wait_warp(at(ctl.k_full[r.slot]), r.turn, abort)) return false;
+            if (!bar_wait(at(ctl.k_full[r.slot]), r.turn, abort)) return false;
             fence_after();
             const uint64_t qd = smem_desc(base + qb * SM::kQ, 0, 1024, 2);
             const uint64_t kd =
@@ -641,23 +654,30 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           const auto pv = [&](int i, int j) {
             const int tile = it.t0 + (PAIR ? j : 2 * j + i);
             Ring<SM::kV>& r = PAIR && i == 1 ? vr1 : vr;
-            if (!bar_wait_warp(at(ctl.v_full[r.slot]), r.turn, abort)) return false;
-            if (!bar_wait_warp(at(ctl.v_ok[r.slot]), r.turn, abort)) return false;
-            if (!bar_wait_warp(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
-            ++p_count[i];
-            fence_after();
+            if (!bar_wait(at(ctl.v_full[r.slot]), r.turn, abort)) return false;
+            if (!bar_wait(at(ctl.v_ok[r.slot]), r.turn, abort)) return false;
             const uint64_t vd =
                 smem_desc(base + SM::kVAt + r.slot * SM::kSlot, kTile * 128, 1024, 2);
             const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
             const int rows = min(kTile, it.row_end - tile * kTile);
+            if (!bar_wait(at(ctl.p_half[i]), p_count[i] & 1, abort)) return false;
+            fence_after();
             if (rows > kTile - 16) {
 #pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
+              for (int s = 0; s < kTile / 32; ++s)
                 mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0, on);
+              if (!bar_wait(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
+              fence_after();
+#pragma unroll
+              for (int s = kTile / 32; s < kTile / 16; ++s)
+                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, true, on);
             } else {
+              if (!bar_wait(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
+              fence_after();
               for (int s = 0; s * 16 < rows; ++s)
                 mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0, on);
             }
+            ++p_count[i];
             if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.v_empty[r.slot]), on);
             if (j == it.nt[i] - 1) mma_commit(at(ctl.o_done[i]), on);
             r.next();
@@ -782,14 +802,19 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             for (int k = 0; k < kTile; ++k)
               if (!(w[k >> 5] & (1u << (k & 31)))) x[k] = 0xff800000u;  // -inf
           }
-          float mx[4] = {m, m, m, m};
+          const auto row_max = [&]() {
+            float mx[4] = {m, m, m, m};
 #pragma unroll
-          for (int k = 0; k < kTile; k += 8)
+            for (int k = 0; k < kTile; k += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[k + 2 * e])), __uint_as_float(x[k + 2 * e + 1]));
-          const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (__any_sync(~0u, valid && (m_new - m) * p.c > kLazy)) {
+              for (int e = 0; e < 4; ++e)
+                mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[k + 2 * e])),
+                              __uint_as_float(x[k + 2 * e + 1]));
+            return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          };
+          // Takes m_new as the reference where some row of the warp has grown past it by 2^kLazy.
+          const auto move_max = [&](float m_new) {
+            if (!__any_sync(~0u, valid && (m_new - m) * p.c > kLazy)) return;
             const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * p.c);
             m = m_new;
             l *= f;
@@ -804,33 +829,51 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 tmem_st16(to + i * kTile + k, o);
               }
             }
-          }
-          const float mb = m == -INFINITY ? 0.f : -m * p.c;
-          float sum[4] = {};
+          };
+          // Half of the row: p = exp2(c (s - m)), to tensor memory; gives its sum.
+          const auto half_row = [&](int half) {
+            const float mb = m == -INFINITY ? 0.f : -m * p.c;
+            float sum[4] = {};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[16];
+            for (int k = 2 * half; k < 2 * half + 2; ++k) {
+              uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float a = __uint_as_float(x[32 * k + 2 * e]), b = __uint_as_float(x[32 * k + 2 * e + 1]);
-              fma2(a, b, p.c, mb);
-              a = ex2(a);
-              b = ex2(b);
-              add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], a, b);
-              w[e] = Pack2<T>::pack(a, b);
+              for (int e = 0; e < 16; ++e) {
+                float a = __uint_as_float(x[32 * k + 2 * e]);
+                float b = __uint_as_float(x[32 * k + 2 * e + 1]);
+                fma2(a, b, p.c, mb);
+                a = ex2(a);
+                b = ex2(b);
+                add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], a, b);
+                w[e] = Pack2<T>::pack(a, b);
+              }
+              tmem_st16(ts + 16 * k, w);
             }
-            tmem_st16(ts + 16 * k, w);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          };
+          move_max(row_max());
+          l += half_row(0);
           tmem_wait_st();
+          // SPLIT: the other chain has read this chain's last O
+          if (!PAIR && j == 0 && item > 0) {
+            const uint32_t w = item - 1;
+            if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
+          }
+          fence_before();
+          bar_arrive(at(ctl.p_half[i]));
+          l += half_row(1);
+          tmem_wait_st();
+          fence_before();
+          bar_arrive(at(ctl.p_ready[i]));
+        } else {
+          if (!PAIR && j == 0 && item > 0) {
+            const uint32_t w = item - 1;
+            if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
+          }
+          fence_before();
+          bar_arrive(at(ctl.p_half[i]));
+          bar_arrive(at(ctl.p_ready[i]));
         }
-        // SPLIT: the other chain has read this chain's last O
-        if (!PAIR && j == 0 && item > 0) {
-          const uint32_t w = item - 1;
-          if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
-        }
-        fence_before();
-        bar_arrive(at(ctl.p_ready[i]));
       }
       if (!ok) break;
       if (nt > 0) {
@@ -924,17 +967,22 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
               for (int e = 0; e < 16; ++e)
                 w[e] = Pack2<T>::pack(__uint_as_float(o[2 * e]) * inv,
                                       __uint_as_float(o[2 * e + 1]) * inv);
+              if (p.wide) {  // rows of whole, aligned 32-byte sectors: half the store requests
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                if (k + 2 * e < p.D)
-                  *reinterpret_cast<uint4*>(out + k + 2 * e) =
-                      make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                for (int e = 0; e < 16; e += 8)
+                  if (k + 2 * e < p.D) st32(out + k + 2 * e, w + e);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                  if (k + 2 * e < p.D)
+                    *reinterpret_cast<uint4*>(out + k + 2 * e) =
+                        make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+              }
             } else {
               float* const d = part + (int64_t)prow * p.D + k;
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                if (k + e < p.D)
-                  *reinterpret_cast<uint4*>(d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 32; e += 8)
+                if (k + e < p.D) st32(d + e, o + e);
             }
           }
         }
@@ -963,12 +1011,12 @@ __global__ __launch_bounds__(256) void join_kernel(const __grid_constant__ AttnP
   ops_pdl_enter();
   const int i0 = blockIdx.x;
   const int64_t at = cut(p, i0 + 1, ctas);
-  const Walk<AttnParams<MAXB>> walk(p, at, at + 1);  // the unit that holds tile `at`
+  const Walk<AttnParams<MAXB>> walk(p, at, at + 1);  // the unit that holds place `at`
   if (walk.t == 0) return;                           // no unit is divided here
-  const int64_t lo = at - walk.t, from = cut(p, i0, ctas);
-  if (from > lo) return;  // an earlier cut divides it too
+  const int64_t lo = walk.pos, from = cut(p, i0, ctas);
+  if (from > lo + p.unit_cost) return;  // an earlier cut divides it too
   const int rows_end = unit_rows(p, walk.b, walk.tok0);
-  const int64_t hi = lo + (rows_end + kTile - 1) / kTile;
+  const int64_t hi = lo + p.unit_cost + (rows_end + kTile - 1) / kTile;
   int i1 = i0 + 1;  // the last CTA with a piece
   while (cut(p, i1 + 1, ctas) < hi) ++i1;
   const int n_tok = min(p.seq.pre[walk.b + 1] - p.seq.pre[walk.b] - walk.tok0, p.unit_tok);
@@ -1016,7 +1064,8 @@ __global__ __launch_bounds__(256) void join_kernel(const __grid_constant__ AttnP
 struct Schedule {
   bool pair;
   int tile_tok, unit_tok;
-  int64_t total;  // tiles
+  int64_t total;  // cost: tiles, and unit_cost for each unit
+  int unit_cost;
   int64_t units;
   int ctas;
   size_t bytes;  // of workspace
@@ -1032,14 +1081,23 @@ int sm_count() {
   return n;
 }
 
+#ifndef DV_UCP
+#define DV_UCP 2
+#define DV_UCS 3
+#endif
 constexpr int kMinTiles = 4;  // a CTA's share is not cut below this many tiles
+// What a unit costs besides its tiles (fetching its queries, filling and
+// draining the two chains, its output), in tiles.
+constexpr int kUnitCostPair = DV_UCP, kUnitCostSplit = DV_UCS;
 
 Schedule schedule(const Plan& p, int group, bool is_tree, int64_t* tile_pre) {
   Schedule s;
   s.tile_tok = kTile / group;
   s.pair = p.max_len > s.tile_tok;
   s.unit_tok = s.tile_tok * (s.pair ? 2 : 1);
+  s.unit_cost = s.pair ? kUnitCostPair : kUnitCostSplit;
   s.total = s.units = 0;
+  int64_t all_tiles = 0;
   for (int b = 0; b < p.B; ++b) {
     if (tile_pre) tile_pre[b] = s.total;
     const int n = p.seq_len[b], first = p.seq_start[b];
@@ -1047,13 +1105,15 @@ Schedule schedule(const Plan& p, int group, bool is_tree, int64_t* tile_pre) {
     for (int64_t u = 0; u < n; u += s.unit_tok) {
       const int64_t rows = first + (is_tree || u + s.unit_tok > n ? n : u + s.unit_tok);
       tiles += (rows + kTile - 1) / kTile;
+      s.total += (int64_t)s.unit_cost * p.H;
       s.units += p.H;
     }
     s.total += tiles * p.H;
+    all_tiles += tiles * p.H;
   }
   if (tile_pre) tile_pre[p.B] = s.total;
   const int64_t sms = sm_count();
-  int64_t ctas = s.total / kMinTiles;
+  int64_t ctas = all_tiles / kMinTiles;
   if (ctas < s.units) ctas = s.units;
   if (ctas > sms) ctas = sms;
   if (ctas < 1) ctas = 1;
@@ -1134,7 +1194,9 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
   kp.S = p.S;
   kp.tile_tok = s.tile_tok;
   kp.unit_tok = s.unit_tok;
+  kp.unit_cost = s.unit_cost;
   kp.is_tree = is_tree ? 1 : 0;
+  kp.wide = p.D % 16 == 0 && q.out_stride % 16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 32 == 0;
   kp.c = q.scale * 1.4426950408889634f;
   fill_table(p, &kp.seq);
   cudaError_t err;
@@ -1202,6 +1264,8 @@ dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, cons
   if (need > 0) {
     if ((st = resolve(workspace, need, false, "workspace", &dev)) != DV_OK) return st;
     part = static_cast<float*>(dev);
+    if (reinterpret_cast<uintptr_t>(part) % 32 != 0)
+      return fail(DV_ERR_MISALIGNED, "workspace %p is not 32-byte aligned", workspace);
     if (overlap(part, need, q.q, nq) || overlap(part, need, q.out, no))
       return fail(DV_ERR_INVALID_ARG, "workspace overlaps q or out");
   }
