@@ -21,7 +21,7 @@
 //          by reading K and V once.
 //
 // Warps: 0-3 and 4-7 the chains' softmax, 8 loads (and walks over the units,
-// publishing each in a ring), 9 issues the products, 10-11 look after V's hidden rows.  K
+// publishing each in a ring), 9 and 10 issue the chains' products, 11 looks after V's hidden rows.  K
 // goes to shared memory by TMA in its own layout: the cache's [D/8][S][8] is,
 // per tile, exactly the tensor core's unswizzled layout of 8 x 16-byte core
 // matrices, so nothing is transposed.  V goes in with the 128-byte swizzle and
@@ -33,7 +33,7 @@
 // the workspace, which join_kernel adds up.
 //
 // Rows a mask hides must have no effect, but 0 x NaN is NaN in a product: in
-// tiles that hold hidden rows, warps 10-11 set V's non-finite values to zero in
+// tiles that hold hidden rows, warp 11 sets V's non-finite values to zero in
 // shared memory (rows past the last attended one altogether), while the tile's scores
 // are computed, and should there have been any, the epilogue adds them to the
 // outputs of the rows that do attend them.
@@ -209,6 +209,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* a, uint32_t addr) {
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : DV_R8(a, 0), DV_R8(a, 8), DV_R8(a, 16), DV_R8(a, 24)
       : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* a) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      DV_W8(a, 0), DV_W8(a, 8), DV_W8(a, 16), DV_W8(a, 24)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t* a, uint32_t addr) {
   asm volatile(
@@ -395,11 +403,6 @@ __device__ __forceinline__ uint64_t causal_mask(int last) {  // the last attende
   return last >= 63 ? ~0ull : last < 0 ? 0ull : (2ull << last) - 1;
 }
 
-template <typename T>
-__device__ __forceinline__ constexpr uint32_t exp_mask() {
-  return std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
-}
-
 // (a, b) = (a, b) * c + d, and (a, b) += (c, d)
 __device__ __forceinline__ void fma2(float& a, float& b, float c, float d) {
   asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n"
@@ -441,7 +444,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(at(ctl.q_full[i]), 1);
-      bar_init(at(ctl.q_empty[i]), 1);
+      bar_init(at(ctl.q_empty[i]), PAIR ? 1 : 2);  // the chains that use it
       bar_init(at(ctl.s_full[i]), 1);
       bar_init(at(ctl.p_half[i]), kTile);
       bar_init(at(ctl.p_ready[i]), kTile);
@@ -450,19 +453,19 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     }
     for (int i = 0; i < SM::kK; ++i) {
       bar_init(at(ctl.k_full[i]), 1);
-      bar_init(at(ctl.k_empty[i]), 1);
+      bar_init(at(ctl.k_empty[i]), 2);  // both chains
     }
     for (int i = 0; i < SM::kV; ++i) {
       bar_init(at(ctl.v_full[i]), 1);
-      bar_init(at(ctl.v_ok[i]), 2);  // the two warps that look at hidden rows
-      bar_init(at(ctl.v_empty[i]), 1);
+      bar_init(at(ctl.v_ok[i]), 1);
+      bar_init(at(ctl.v_empty[i]), 3);  // both chains, and the look at hidden rows
     }
     for (int i = 0; i < kItems; ++i) {
       bar_init(at(ctl.item_full[i]), 1);
-      bar_init(at(ctl.item_empty[i]), 11);  // 8 softmax warps, the products, warps 10 and 11
+      bar_init(at(ctl.item_empty[i]), 11);  // all warps but the loads'
     }
     bar_init(at(ctl.xchg), 2 * kTile);
-    bar_init(at(ctl.drained), 1);
+    bar_init(at(ctl.drained), 2);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -591,7 +594,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         }
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp < 11) {
       // ---- products ----
       {
         const bool on = elect();
@@ -600,105 +603,110 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             1u << 4 | kType << 7 | kType << 10 | (uint32_t)(kTile >> 4) << 24;
         constexpr uint32_t kIdescS = kIdesc | (uint32_t)(kTile >> 3) << 17;
         constexpr uint32_t kIdescO = kIdesc | 1u << 16 | (uint32_t)(DP >> 3) << 17;
-        const int steps = (p.C + 1) / 2;
-        Ring<SM::kK> kr, kr1;  // the next K and V tile; PAIR: chain 0's and chain 1's places
-        Ring<SM::kV> vr, vr1;
-        uint32_t n_items = 0, n_q = 0, q_used[2] = {0, 0}, p_count[2] = {0, 0};
+        const int i = warp - 9, steps = (p.C + 1) / 2;
+        Ring<SM::kK> kr;
+        Ring<SM::kV> vr;
+        uint32_t n_items = 0, n_q = 0, p_count = 0;
         bool ok = true;
         Item it;
         while (ok && get_item(n_items, &it)) {
-          it.n = __shfl_sync(~0u, it.n, 0);
-          it.t0 = __shfl_sync(~0u, it.t0, 0);
-          it.nt[0] = __shfl_sync(~0u, it.nt[0], 0);
-          it.nt[1] = __shfl_sync(~0u, it.nt[1], 0);
-          it.row_end = __shfl_sync(~0u, it.row_end, 0);
-          const int qb_split = (int)(n_q & 1);
-          if (PAIR) {
-            for (int i = 0; i < 2; ++i)
-              if (it.nt[i] > 0) ++q_used[i];
-          } else {
-            ++q_used[qb_split];
-            ++n_q;
+          const int n = __shfl_sync(~0u, it.n, 0), t0 = __shfl_sync(~0u, it.t0, 0);
+          const int nt = __shfl_sync(~0u, it.nt[i], 0), row_end = __shfl_sync(~0u, it.row_end, 0);
+          const int masked = __shfl_sync(~0u, it.masked, 0);
+          const int qb = PAIR ? i : (int)(n_items & 1);
+          const uint32_t q_parity = (PAIR ? n_q : n_items >> 1) & 1;
+          if (nt > 0) ++n_q;
+          if (!PAIR && nt == 0) {  // (once the buffer's last turn is over for both chains)
+            if (!(ok = bar_wait(at(ctl.q_full[qb]), q_parity, abort))) break;
+            if (on) bar_arrive(at(ctl.q_empty[qb]));
           }
-          if (PAIR) {
-            kr1 = kr;
-            vr1 = vr;
-          }
-          // S_i = Q K_j^T into the chain's S columns
-          const auto qk = [&](int i, int j) {
-            const int qb = PAIR ? i : qb_split;
-            if (j == 0 && !bar_wait(at(ctl.q_full[qb]), (q_used[qb] - 1) & 1, abort)) return false;
-            Ring<SM::kK>& r = PAIR && i == 1 ? kr1 : kr;
-            if (!bar_wait(at(ctl.k_full[r.slot]), r.turn, abort)) return false;
-            fence_after();
-            const uint64_t qd = smem_desc(base + qb * SM::kQ, 0, 1024, 2);
-            const uint64_t kd =
-                smem_desc(base + SM::kKAt + r.slot * SM::kSlot, kTile * 16, 128, 0);
-            if (steps == DP / 16) {
+          const auto mine = [&](int j) { return PAIR ? j < nt : (j & 1) == i; };
+          int jk = 0, jv = 0, k_mine = 0, v_mine = 0;
+          // Both chains go through every K and V tile in order; one that is not the chain's is
+          // let go.  Neither ring is followed past the other (V_j is loaded after K_j+1 and not
+          // before K_j-1, V_j-1 are let go).
+          // Up to the chain's next K tile: S = Q K^T into the chain's S columns.
+          const auto next_k = [&]() {
+            while (jk < n) {
+              const bool own = mine(jk);
+              if (!own && jk > jv + 1) break;
+              if (!bar_wait(at(ctl.k_full[kr.slot]), kr.turn, abort)) return false;
+              if (own) {
+                if (k_mine == 0 && !bar_wait(at(ctl.q_full[qb]), q_parity, abort)) return false;
+                fence_after();
+                const uint64_t qd = smem_desc(base + qb * SM::kQ, 0, 1024, 2);
+                const uint64_t kd =
+                    smem_desc(base + SM::kKAt + kr.slot * SM::kSlot, kTile * 16, 128, 0);
+                const uint32_t s0 = tmem + i * kTile;
+                if (steps == DP / 16) {
 #pragma unroll
-              for (int s = 0; s < DP / 16; ++s)
-                mma_ss(tmem + i * kTile, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2,
-                       kd + s * (2 * kTile), kIdescS, s > 0, on);
-            } else {
-              for (int s = 0; s < steps; ++s)
-                mma_ss(tmem + i * kTile, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2,
-                       kd + s * (2 * kTile), kIdescS, s > 0, on);
+                  for (int s = 0; s < DP / 16; ++s)
+                    mma_ss(s0, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kd + s * (2 * kTile),
+                           kIdescS, s > 0, on);
+                } else {
+                  for (int s = 0; s < steps; ++s)
+                    mma_ss(s0, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kd + s * (2 * kTile),
+                           kIdescS, s > 0, on);
+                }
+                mma_commit(at(ctl.s_full[i]), on);
+                mma_commit(at(ctl.k_empty[kr.slot]), on);
+                if (++k_mine == nt) mma_commit(at(ctl.q_empty[qb]), on);
+              } else if (on) {
+                bar_arrive(at(ctl.k_empty[kr.slot]));
+              }
+              kr.next();
+              ++jk;
+              if (own) break;
             }
-            mma_commit(at(ctl.s_full[i]), on);
-            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.k_empty[r.slot]), on);
-            // the row tile's last use
-            if (j == it.nt[i] - 1 && (PAIR || 2 * j + i == it.n - 1)) mma_commit(at(ctl.q_empty[qb]), on);
-            r.next();
             return true;
           };
-          const auto pv = [&](int i, int j) {
-            const int tile = it.t0 + (PAIR ? j : 2 * j + i);
-            Ring<SM::kV>& r = PAIR && i == 1 ? vr1 : vr;
-            if (!bar_wait(at(ctl.v_full[r.slot]), r.turn, abort)) return false;
-            if (!bar_wait(at(ctl.v_ok[r.slot]), r.turn, abort)) return false;
-            const uint64_t vd =
-                smem_desc(base + SM::kVAt + r.slot * SM::kSlot, kTile * 128, 1024, 2);
-            const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
-            const int rows = min(kTile, it.row_end - tile * kTile);
-            if (!bar_wait(at(ctl.p_half[i]), p_count[i] & 1, abort)) return false;
-            fence_after();
-            if (rows > kTile - 16) {
+          // Up to the chain's next V tile: O += P V.
+          const auto next_v = [&]() {
+            while (jv < jk) {
+              const bool own = mine(jv);
+              // (hidden rows have been looked at where the tile has any)
+              if (!bar_wait(at(own && t0 + jv >= masked ? ctl.v_ok[vr.slot] : ctl.v_full[vr.slot]),
+                            vr.turn, abort))
+                return false;
+              if (own) {
+                const uint64_t vd =
+                    smem_desc(base + SM::kVAt + vr.slot * SM::kSlot, kTile * 128, 1024, 2);
+                const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
+                const int rows = min(kTile, row_end - (t0 + jv) * kTile);
+                const bool more = v_mine > 0;
+                if (!bar_wait(at(ctl.p_half[i]), p_count & 1, abort)) return false;
+                fence_after();
+                if (rows > kTile - 16) {
 #pragma unroll
-              for (int s = 0; s < kTile / 32; ++s)
-                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0, on);
-              if (!bar_wait(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
-              fence_after();
+                  for (int s = 0; s < kTile / 32; ++s)
+                    mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, more || s > 0, on);
+                  if (!bar_wait(at(ctl.p_ready[i]), p_count & 1, abort)) return false;
+                  fence_after();
 #pragma unroll
-              for (int s = kTile / 32; s < kTile / 16; ++s)
-                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, true, on);
-            } else {
-              if (!bar_wait(at(ctl.p_ready[i]), p_count[i] & 1, abort)) return false;
-              fence_after();
-              for (int s = 0; s * 16 < rows; ++s)
-                mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, j > 0 || s > 0, on);
+                  for (int s = kTile / 32; s < kTile / 16; ++s)
+                    mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, true, on);
+                } else {
+                  if (!bar_wait(at(ctl.p_ready[i]), p_count & 1, abort)) return false;
+                  fence_after();
+                  for (int s = 0; s * 16 < rows; ++s)
+                    mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, more || s > 0, on);
+                }
+                ++p_count;
+                mma_commit(at(ctl.v_empty[vr.slot]), on);
+                if (++v_mine == nt) mma_commit(at(ctl.o_done[i]), on);
+              } else if (on) {
+                bar_arrive(at(ctl.v_empty[vr.slot]));
+              }
+              vr.next();
+              ++jv;
+              if (own) break;
             }
-            ++p_count[i];
-            if (!PAIR || i == 1 || j >= it.nt[1]) mma_commit(at(ctl.v_empty[r.slot]), on);
-            if (j == it.nt[i] - 1) mma_commit(at(ctl.o_done[i]), on);
-            r.next();
             return true;
           };
-          if (it.nt[0] > 0) ok = qk(0, 0);
-          if (ok && it.nt[1] > 0) ok = qk(1, 0);
-          const int longest = max(it.nt[0], it.nt[1]);
-          for (int j = 0; j < longest && ok; ++j) {
-            if (j < it.nt[0]) {
-              ok = pv(0, j);
-              if (ok && j + 1 < it.nt[0]) ok = qk(0, j + 1);
-            }
-            if (ok && j < it.nt[1]) {
-              ok = pv(1, j);
-              if (ok && j + 1 < it.nt[1]) ok = qk(1, j + 1);
-            }
-          }
-          if (PAIR && it.nt[1] == it.n) {  // chain 1 has gone through every tile
-            kr = kr1;
-            vr = vr1;
+          ok = next_k();
+          while (ok && jv < n) {
+            ok = next_v();
+            if (ok) ok = next_k();
           }
           if (on) bar_arrive(at(ctl.item_empty[n_items % kItems]));
           ++n_items;
@@ -720,32 +728,28 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           const int row0 = (it.t0 + j) * kTile;
           if (it.t0 + j >= it.masked) {
 #pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-              const int r = x * 64 + (warp - 10) * 32 + lane;
+            for (int r = lane; r < kTile; r += 32) {
               uint4* const vrow = reinterpret_cast<uint4*>(sm + SM::kVAt + vr.slot * SM::kSlot + r * 128);
               if (row0 + r >= it.row_end) {
 #pragma unroll
                 for (int c = 0; c < DP / 8; ++c)
                   vrow[(c >> 3) * (kTile * 8) + ((c + r) & 7)] = make_uint4(0, 0, 0, 0);
               } else {
-                constexpr uint32_t M = exp_mask<T>();
+                // adding one to the exponent carries to the sign bit where it is all ones
+                constexpr uint32_t one = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
                 uint32_t bad = 0;
 #pragma unroll
                 for (int c = 0; c < DP / 8; ++c) {
                   const uint4 u = vrow[(c >> 3) * (kTile * 8) + ((c + r) & 7)];
-                  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {  // a zero half-word of y: all exponent bits set
-                    const uint32_t y = (w[e] & M) ^ M;
-                    bad |= (y - 0x00010001u) & ~y & 0x80008000u;
-                  }
+                  bad |= ((u.x & 0x7fff7fffu) + one) | ((u.y & 0x7fff7fffu) + one) |
+                         ((u.z & 0x7fff7fffu) + one) | ((u.w & 0x7fff7fffu) + one);
                 }
-                if (bad) {
+                if (bad & 0x80008000u) {
                   ctl.item[k % kItems].bad = 1;
                   uint16_t* const e = reinterpret_cast<uint16_t*>(vrow);
                   for (int c = 0; c < DP; ++c) {
                     uint16_t& y = e[(c >> 6) * (kTile * 64) + (c & 63)];
-                    if ((y & (M & 0xffff)) == (M & 0xffff)) y = 0;
+                    if (((y & 0x7fffu) + (one & 0xffffu)) & 0x8000u) y = 0;
                   }
                 }
               }
@@ -753,7 +757,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(at(ctl.v_ok[vr.slot]));
+          if (lane == 0) {
+            bar_arrive(at(ctl.v_ok[vr.slot]));
+            bar_arrive(at(ctl.v_empty[vr.slot]));
+          }
         }
         if (lane == 0) bar_arrive(at(ctl.item_empty[k % kItems]));
       }
@@ -786,22 +793,29 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         ++s_count;
         fence_after();
         if (any_valid) {
+          // Hidden columns are set to -inf in tensor memory, 32 at a time and only where the
+          // warp has some: a small loop beside the tile's long straight code.
+          if (tile >= masked) {
+#pragma unroll 1
+            for (int k = 0; k < kTile; k += 32) {
+              const int col = tile * kTile + k;
+              const uint32_t w = (uint32_t)(p.is_tree ? tree_mask(bits, col - it.start)
+                                                      : causal_mask(it.start + tok - col));
+              if (__all_sync(~0u, w == ~0u)) continue;
+              uint32_t y[32];
+              tmem_ld32(y, ts + k);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(w & (1u << e))) y[e] = 0xff800000u;
+              tmem_st32(ts + k, y);
+            }
+            tmem_wait_st();
+          }
           uint32_t x[kTile];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32(x + 32 * k, ts + 32 * k);
           tmem_wait_ld();
-          if (tile >= masked) {
-            const int col0 = tile * kTile;
-            const uint64_t lo = p.is_tree ? tree_mask(bits, col0 - it.start)
-                                          : causal_mask(it.start + tok - col0);
-            const uint64_t hi = p.is_tree ? tree_mask(bits, col0 + 64 - it.start)
-                                          : causal_mask(it.start + tok - col0 - 64);
-            const uint32_t w[4] = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
-                                   (uint32_t)(hi >> 32)};
-#pragma unroll
-            for (int k = 0; k < kTile; ++k)
-              if (!(w[k >> 5] & (1u << (k & 31)))) x[k] = 0xff800000u;  // -inf
-          }
           const auto row_max = [&]() {
             float mx[4] = {m, m, m, m};
 #pragma unroll

@@ -129,6 +129,10 @@ PROMPTS = [
     (36, 2, 1, 64, 70, (0, 10), (0, 60)),
     (1, 2, 1, 128, 2048, (0, 0), (2048, 2048)),
     (1, 1, 2, 64, 5000, (4500, 4500), (300, 300)),
+    # more units than the GPU has SMs, some of one row tile with many K/V tiles
+    (4, 64, 1, 128, 1500, (600, 900), (40, 600)),
+    (6, 50, 1, 64, 1300, (0, 900), (1, 390)),
+    (3, 60, 3, 128, 700, (0, 500), (20, 90)),
 ]
 
 
@@ -164,6 +168,9 @@ TREES = [
     (40, 1, 2, 64, 100, (0, 90), (0, 10)),
     (1, 1, 1, 128, 20000, (19900, 19900), (1, 1)),
     (1, 2, 4, 128, 9000, (8900, 8900), (31, 31)),
+    (5, 70, 1, 128, 1200, (0, 1130), (1, 20)),   # more units than the GPU has SMs
+    (4, 64, 2, 64, 900, (0, 830), (0, 64)),
+    (3, 60, 4, 128, 800, (300, 730), (20, 64)),
 ]
 
 
