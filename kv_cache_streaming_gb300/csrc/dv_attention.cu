@@ -69,7 +69,7 @@ struct AttnParams {
   const uint64_t* tree;
   float* part;
   int64_t out_stride;
-  int64_t total;  // cost of all units
+  int32_t share, extra;  // a CTA's part of the units' cost; the first `extra` have one more
   int32_t H, G, D, C, S;
   int32_t k_rows;    // w of k_map
   int32_t tile_tok;  // tokens of a row tile: 128 / G
@@ -79,7 +79,7 @@ struct AttnParams {
   int32_t wide;  // every output row of a head is 32-byte aligned, of whole 32-byte sectors
   float c;  // scale * log2(e)
   SeqTable<MAXB> seq;
-  int64_t tile_pre[MAXB + 1];
+  int32_t cost_pre[MAXB + 1];  // cost of the sequences before
 };
 
 // ---- instructions --------------------------------------------------------------
@@ -104,22 +104,21 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The rest of a wait, out of line: inlined at each of its thirty places (and
-// with a vote of the warp) it made the kernel 1.1 to 1.5 times slower, by the size of the code.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t i = 0; i < kSpinLimit; ++i) {
-    if (bar_try(bar, parity)) return true;
-    if ((i & 31) == 31 && *abort) return false;
-  }
-  *abort = 1;
+// Waits for the phase of `parity` to complete; false when it gave up.  Kept
+// short: it stands at some thirty places, and the kernel's speed hangs on its
+// size (an instruction cache miss in every loop made ragged prompts twice as slow).
+__device__ __noinline__ bool gave_up() {
   atomicExch(&g_attention_timeout, 1u);
   return false;
 }
-// Waits for the phase of `parity` to complete; false when it gave up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (bar_try(bar, parity)) return true;
-  return bar_wait_long(bar, parity, abort);
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  uint32_t left = kSpinLimit;
+#pragma unroll 1
+  while (!bar_try(bar, parity))
+    if (--left == 0) return gave_up();
+  return true;
 }
+
 // The load and the product warp run their loops as whole warps on uniform
 // values, and one elected lane (`on`) issues: descriptors and addresses then
 // stay in uniform registers, from where these instructions take them.
@@ -284,7 +283,6 @@ struct Smem {
     uint64_t item_full[kItems], item_empty[kItems], o_read[2], xchg, drained;
     Item item[kItems];
     float2 ml[2][kTile];  // SPLIT: the chains' maxima and sums
-    volatile int abort;
     uint32_t tmem;
   };
   static constexpr int kBytes = kCtl + (int)sizeof(Ctl);
@@ -315,22 +313,24 @@ __device__ __forceinline__ int unit_rows(const P& p, int b, int tok0) {
 template <typename P>
 struct Walk {
   const P& p;
-  int64_t pos, end;   // where the unit starts on the line of costs; where the CTA's stretch ends
+  int pos, end;       // where the unit starts on the line of costs; where the CTA's stretch ends
   int b, h, tok0, t;  // the next piece: its unit and first tile
 
-  __device__ Walk(const P& p_, int64_t lo, int64_t hi) : p(p_), pos(lo), end(hi) {
+  __device__ Walk(const P& p_, int lo, int hi) : p(p_), pos(lo), end(hi) {
     b = h = tok0 = t = 0;
     if (lo >= hi) return;
     int x = 0, y = p.seq.batch;
+#pragma unroll 1
     while (y - x > 1) {
       const int m = (x + y) >> 1;
-      if (p.tile_pre[m] <= lo) x = m; else y = m;
+      if (p.cost_pre[m] <= lo) x = m; else y = m;
     }
     b = x;
-    int64_t rem = lo - p.tile_pre[b];
-    const int64_t head = (p.tile_pre[b + 1] - p.tile_pre[b]) / p.H;
-    h = (int)(rem / head);
+    int rem = lo - p.cost_pre[b];
+    const int head = (p.cost_pre[b + 1] - p.cost_pre[b]) / p.H;
+    h = rem / head;
     rem -= h * head;
+#pragma unroll 1
     for (;;) {
       const int cost = p.unit_cost + (unit_rows(p, b, tok0) + kTile - 1) / kTile;
       if (rem < cost) break;
@@ -338,7 +338,7 @@ struct Walk {
       tok0 += p.unit_tok;
     }
     pos = lo - rem;
-    t = max(0, (int)rem - p.unit_cost);
+    t = max(0, rem - p.unit_cost);
   }
 
   template <bool PAIR>
@@ -347,8 +347,7 @@ struct Walk {
     if (pos >= end) return;
     const int start = p.seq.start[b], at = p.seq.pre[b], n_tok = p.seq.pre[b + 1] - at;
     const int row_end = unit_rows(p, b, tok0), cnt = (row_end + kTile - 1) / kTile;
-    const int64_t left = end - pos - p.unit_cost;  // tiles of the unit before the end
-    const int n = (int)min((int64_t)cnt, left) - t;
+    const int n = min(cnt, end - pos - p.unit_cost) - t;
     if (n <= 0) return;
     it->b = b;
     it->h = h;
@@ -385,9 +384,10 @@ struct Walk {
   }
 };
 
+// Where CTA i's stretch of the line starts.
 template <typename P>
-__device__ __forceinline__ int64_t cut(const P& p, int i, int n) {
-  return p.total / n * i + min((int64_t)i, p.total % n);
+__device__ __forceinline__ int cut(const P& p, int i) {
+  return p.share * i + min(i, p.extra);
 }
 
 // ---- the kernel ------------------------------------------------------------------
@@ -433,7 +433,6 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   const auto at = [&](const uint64_t& bar) {
     return base + (uint32_t)(reinterpret_cast<const uint8_t*>(&bar) - sm);
   };
-  volatile int* const abort = &ctl.abort;
 
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -466,7 +465,6 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     }
     bar_init(at(ctl.xchg), 2 * kTile);
     bar_init(at(ctl.drained), 2);
-    ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -478,7 +476,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 
   // The k-th item, from the ring.
   const auto get_item = [&](uint32_t k, Item* it) {
-    if (!bar_wait(at(ctl.item_full[k % kItems]), k / kItems & 1, abort)) return false;
+    if (!bar_wait(at(ctl.item_full[k % kItems]), k / kItems & 1)) return false;
     *it = ctl.item[k % kItems];
     return __all_sync(~0u, it->n > 0) != 0;
   };
@@ -488,17 +486,16 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       // ---- the walk, and loads ----
       {
         const bool on = elect();
-        Walk<AttnParams<MAXB>> walk(p, cut(p, blockIdx.x, gridDim.x),
-                                    cut(p, blockIdx.x + 1, gridDim.x));
+        Walk<AttnParams<MAXB>> walk(p, cut(p, blockIdx.x),
+                                    cut(p, blockIdx.x + 1));
         Item it, after;
         Ring<SM::kK> kr;
         Ring<SM::kV> vr;
-        uint32_t nk = 0, nv = 0, q_used[2] = {0, 0}, n_items = 0;
+        uint32_t nk = 0, nv = 0, q_used[2] = {0, 0}, n_items = 0, n_q = 0;
         bool ok = true;
         const auto publish = [&](const Item& x) {
           if (n_items >= kItems)
-            ok = bar_wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1,
-                               abort);
+            ok = bar_wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1);
           if (!ok) return;
           if (on) {
             ctl.item[n_items % kItems] = x;
@@ -506,45 +503,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           }
           ++n_items;
         };
-        const auto load_v = [&](int head, int row, int rows) {
-          const uint32_t bar = at(ctl.v_full[vr.slot]), dst = base + SM::kVAt + vr.slot * SM::kSlot;
-          if (nv >= SM::kV) ok = bar_wait(at(ctl.v_empty[vr.slot]), vr.turn ^ 1, abort);
-          if (!ok) return;
-          const int boxes = (rows + 31) / 32;
-          bar_expect(bar, boxes * (DP / 64) * 4096, on);
-          for (int half = 0; half < DP / 64; ++half) {
-            if (boxes == 4)
-              tma_load3(dst + half * (kTile * 128), &p.v_map, half * 64, row, head, bar, on);
-            else
-              for (int x = 0; x < boxes; ++x)
-                tma_load3(dst + half * (kTile * 128) + x * 4096, &p.v_part, half * 64,
-                          row + x * 32, head, bar, on);
-          }
-          vr.next();
-          ++nv;
-        };
-        const auto load_k = [&](int head, int row, int rows) {
-          const uint32_t bar = at(ctl.k_full[kr.slot]), dst = base + SM::kKAt + kr.slot * SM::kSlot;
-          if (nk >= SM::kK) ok = bar_wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1, abort);
-          if (!ok) return;
-          const int pad = p.C & 1;  // zeros for the other half of the last contraction step
-          if (rows == kTile) {
-            bar_expect(bar, (p.C + pad) * (kTile * 16), on);
-            tma_load4(dst, &p.k_map, 0, row / p.k_rows, 0, head, bar, on);
-          } else {
-            bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
-            const uint4* src = p.k + (int64_t)head * p.C * p.S + row;
-            for (int c = 0; c < p.C; ++c)
-              bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar, on);
-          }
-          if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar, on);
-          kr.next();
-          ++nk;
-        };
-        uint32_t n_q = 0;
         const auto load_q = [&](const Item& x, int i) {
           const int qb = PAIR ? i : (int)(n_q & 1);
-          if (q_used[qb] > 0) ok = bar_wait(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1, abort);
+          if (q_used[qb] > 0) ok = bar_wait(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1);
           if (!ok) return;
           ++q_used[qb];
           ++n_q;
@@ -554,43 +515,83 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             tma_load4(base + qb * SM::kQ + half * (kTile * 128), &p.q_map, half * 64, 0, x.h,
                       x.tok_at + x.tok0 + i * p.tile_tok, bar, on);
         };
-        walk.template next<PAIR>(&it);
-        publish(it);
-        if (!PAIR && it.n > 0) load_q(it, 0);
-        int v_head = 0, v_row = 0, v_rows = 0;  // the V tile that is due (none: v_rows 0)
-        while (ok && it.n > 0) {
-          if (PAIR) {  // the row tiles' buffers are free once the unit before has used them up,
-            if (v_rows > 0) load_v(v_head, v_row, v_rows);  // which takes its last V
+        // In the order K0 V0 K1 V1 ...; a unit's queries before its first K.
+        int j = 0, head = 0, v_row = 0, v_rows = 0;  // the V tile that is due (none: v_rows 0)
+        bool first = true;
+#pragma unroll 1
+        while (ok) {
+          if (v_rows > 0) {
+            if (nv >= SM::kV) ok = bar_wait(at(ctl.v_empty[vr.slot]), vr.turn ^ 1);
+            if (!ok) break;
+            // a whole tile in one copy a half, else in boxes of 32 rows
+            const uint32_t bar = at(ctl.v_full[vr.slot]);
+            const uint32_t dst = base + SM::kVAt + vr.slot * SM::kSlot;
+            const int boxes = (v_rows + 31) / 32, copies = boxes == 4 ? 1 : boxes;
+            const CUtensorMap* const map = boxes == 4 ? &p.v_map : &p.v_part;
+            bar_expect(bar, boxes * (DP / 64) * 4096, on);
+#pragma unroll 1
+            for (int x = 0; x < copies; ++x)
+              for (int half = 0; half < DP / 64; ++half)
+                tma_load3(dst + half * (kTile * 128) + x * 4096, map, half * 64, v_row + x * 32,
+                          head, bar, on);
+            vr.next();
+            ++nv;
             v_rows = 0;
-            for (int i = 0; i < 2 && ok; ++i)
-              if (it.nt[i] > 0) load_q(it, i);
           }
-          const int head = it.b * p.H + it.h;
-          for (int j = 0; j < it.n && ok; ++j) {
-            const int row = (it.t0 + j) * kTile, rows = min(kTile, it.row_end - row);
-            load_k(head, row, rows);
-            if (ok && v_rows > 0) load_v(v_head, v_row, v_rows);
-            v_head = head;
-            v_row = row;
-            v_rows = rows;
-            if (j == 0 && ok) {  // ahead of need: the next unit, SPLIT its queries
-              walk.template next<PAIR>(&after);
-              publish(after);
-              if (!PAIR && ok && after.n > 0) load_q(after, 0);
+          if (j == 0) {
+            if (!first && it.n == 0) break;
+            // ahead of need: the next unit, SPLIT its queries
+            walk.template next<PAIR>(&after);
+            publish(after);
+            if (!PAIR && ok && after.n > 0) load_q(after, 0);
+            if (first) {
+              first = false;
+              it = after;
+              continue;
             }
+            // (the row tiles' buffers are free once the unit before has used them up)
+            if (PAIR)
+#pragma unroll 1
+              for (int i = 0; i < 2 && ok; ++i)
+                if (it.nt[i] > 0) load_q(it, i);
+            head = it.b * p.H + it.h;
           }
-          it = after;
+          if (!ok) break;
+          const int row = (it.t0 + j) * kTile, rows = min(kTile, it.row_end - row);
+          if (nk >= SM::kK) ok = bar_wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1);
+          if (!ok) break;
+          const uint32_t bar = at(ctl.k_full[kr.slot]);
+          const uint32_t dst = base + SM::kKAt + kr.slot * SM::kSlot;
+          const int pad = p.C & 1;  // zeros for the other half of the last contraction step
+          bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
+          if (rows == kTile) {
+            tma_load4(dst, &p.k_map, 0, row / p.k_rows, 0, head, bar, on);
+          } else {
+            const uint4* src = p.k + (int64_t)head * p.C * p.S + row;
+#pragma unroll 1
+            for (int c = 0; c < p.C; ++c)
+              bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar, on);
+          }
+          if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar, on);
+          kr.next();
+          ++nk;
+          v_row = row;
+          v_rows = rows;
+          if (++j == it.n) {
+            it = after;
+            j = 0;
+          }
         }
-        if (ok && v_rows > 0) load_v(v_head, v_row, v_rows);
         // A CTA that gave up leaves no copy in flight.
         if (!ok) {
-          int never = 0;
+#pragma unroll 1
           for (uint32_t i = 0; i < SM::kK && i < nk; ++i)  // a slot's last use
-            bar_wait(at(ctl.k_full[i]), (nk - i - 1) / SM::kK & 1, &never);
+            bar_wait(at(ctl.k_full[i]), (nk - i - 1) / SM::kK & 1);
+#pragma unroll 1
           for (uint32_t i = 0; i < SM::kV && i < nv; ++i)
-            bar_wait(at(ctl.v_full[i]), (nv - i - 1) / SM::kV & 1, &never);
+            bar_wait(at(ctl.v_full[i]), (nv - i - 1) / SM::kV & 1);
           for (int i = 0; i < 2; ++i)
-            if (q_used[i] > 0) bar_wait(at(ctl.q_full[i]), (q_used[i] - 1) & 1, &never);
+            if (q_used[i] > 0) bar_wait(at(ctl.q_full[i]), (q_used[i] - 1) & 1);
         }
       }
       __syncwarp();
@@ -617,7 +618,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           const uint32_t q_parity = (PAIR ? n_q : n_items >> 1) & 1;
           if (nt > 0) ++n_q;
           if (!PAIR && nt == 0) {  // (once the buffer's last turn is over for both chains)
-            if (!(ok = bar_wait(at(ctl.q_full[qb]), q_parity, abort))) break;
+            if (!(ok = bar_wait(at(ctl.q_full[qb]), q_parity))) break;
             if (on) bar_arrive(at(ctl.q_empty[qb]));
           }
           const auto mine = [&](int j) { return PAIR ? j < nt : (j & 1) == i; };
@@ -627,27 +628,22 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           // before K_j-1, V_j-1 are let go).
           // Up to the chain's next K tile: S = Q K^T into the chain's S columns.
           const auto next_k = [&]() {
+#pragma unroll 1
             while (jk < n) {
               const bool own = mine(jk);
               if (!own && jk > jv + 1) break;
-              if (!bar_wait(at(ctl.k_full[kr.slot]), kr.turn, abort)) return false;
+              if (!bar_wait(at(ctl.k_full[kr.slot]), kr.turn)) return false;
               if (own) {
-                if (k_mine == 0 && !bar_wait(at(ctl.q_full[qb]), q_parity, abort)) return false;
+                if (k_mine == 0 && !bar_wait(at(ctl.q_full[qb]), q_parity)) return false;
                 fence_after();
                 const uint64_t qd = smem_desc(base + qb * SM::kQ, 0, 1024, 2);
                 const uint64_t kd =
                     smem_desc(base + SM::kKAt + kr.slot * SM::kSlot, kTile * 16, 128, 0);
                 const uint32_t s0 = tmem + i * kTile;
-                if (steps == DP / 16) {
 #pragma unroll
-                  for (int s = 0; s < DP / 16; ++s)
-                    mma_ss(s0, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kd + s * (2 * kTile),
-                           kIdescS, s > 0, on);
-                } else {
-                  for (int s = 0; s < steps; ++s)
-                    mma_ss(s0, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kd + s * (2 * kTile),
-                           kIdescS, s > 0, on);
-                }
+                for (int s = 0; s < DP / 16; ++s)
+                  mma_ss(s0, qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kd + s * (2 * kTile),
+                         kIdescS, s > 0, on && s < steps);
                 mma_commit(at(ctl.s_full[i]), on);
                 mma_commit(at(ctl.k_empty[kr.slot]), on);
                 if (++k_mine == nt) mma_commit(at(ctl.q_empty[qb]), on);
@@ -662,11 +658,12 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           };
           // Up to the chain's next V tile: O += P V.
           const auto next_v = [&]() {
+#pragma unroll 1
             while (jv < jk) {
               const bool own = mine(jv);
               // (hidden rows have been looked at where the tile has any)
               if (!bar_wait(at(own && t0 + jv >= masked ? ctl.v_ok[vr.slot] : ctl.v_full[vr.slot]),
-                            vr.turn, abort))
+                            vr.turn))
                 return false;
               if (own) {
                 const uint64_t vd =
@@ -674,23 +671,16 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
                 const int rows = min(kTile, row_end - (t0 + jv) * kTile);
                 const bool more = v_mine > 0;
-                if (!bar_wait(at(ctl.p_half[i]), p_count & 1, abort)) return false;
+                if (!bar_wait(at(ctl.p_half[i]), p_count & 1)) return false;
                 fence_after();
-                if (rows > kTile - 16) {
 #pragma unroll
-                  for (int s = 0; s < kTile / 32; ++s)
-                    mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, more || s > 0, on);
-                  if (!bar_wait(at(ctl.p_ready[i]), p_count & 1, abort)) return false;
-                  fence_after();
+                for (int s = 0; s < kTile / 32; ++s)
+                  mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, more || s > 0, on && s * 16 < rows);
+                if (!bar_wait(at(ctl.p_ready[i]), p_count & 1)) return false;
+                fence_after();
 #pragma unroll
-                  for (int s = kTile / 32; s < kTile / 16; ++s)
-                    mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, true, on);
-                } else {
-                  if (!bar_wait(at(ctl.p_ready[i]), p_count & 1, abort)) return false;
-                  fence_after();
-                  for (int s = 0; s * 16 < rows; ++s)
-                    mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, more || s > 0, on);
-                }
+                for (int s = kTile / 32; s < kTile / 16; ++s)
+                  mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, true, on && s * 16 < rows);
                 ++p_count;
                 mma_commit(at(ctl.v_empty[vr.slot]), on);
                 if (++v_mine == nt) mma_commit(at(ctl.o_done[i]), on);
@@ -703,18 +693,17 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             }
             return true;
           };
-          ok = next_k();
-          while (ok && jv < n) {
-            ok = next_v();
-            if (ok) ok = next_k();
+#pragma unroll 1
+          for (;;) {
+            if (!(ok = next_k()) || jv == n) break;
+            if (!(ok = next_v())) break;
           }
           if (on) bar_arrive(at(ctl.item_empty[n_items % kItems]));
           ++n_items;
         }
         // the products in flight end before tensor memory is given back
-        int never = 0;
         mma_commit(at(ctl.drained), on);
-        bar_wait(at(ctl.drained), 0, &never);
+        bar_wait(at(ctl.drained), 0);
       }
       __syncwarp();
     } else {
@@ -723,8 +712,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       Item it;
       bool ok = true;
       for (uint32_t k = 0; ok && get_item(k, &it); ++k) {
+#pragma unroll 1
         for (int j = 0; j < it.n; ++j, vr.next()) {
-          if (!(ok = bar_wait(at(ctl.v_full[vr.slot]), vr.turn, abort))) break;
+          if (!(ok = bar_wait(at(ctl.v_full[vr.slot]), vr.turn))) break;
           const int row0 = (it.t0 + j) * kTile;
           if (it.t0 + j >= it.masked) {
 #pragma unroll 1
@@ -747,6 +737,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 if (bad & 0x80008000u) {
                   ctl.item[k % kItems].bad = 1;
                   uint16_t* const e = reinterpret_cast<uint16_t*>(vrow);
+#pragma unroll 1
                   for (int c = 0; c < DP; ++c) {
                     uint16_t& y = e[(c >> 6) * (kTile * 64) + (c & 63)];
                     if (((y & 0x7fffu) + (one & 0xffffu)) & 0x8000u) y = 0;
@@ -786,12 +777,39 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       }
       // the first tile that hides a column from some row of the chain's tile
       const int masked = p.is_tree ? it.masked : (it.start + tile_tok0 + 1) / kTile;
+      if (!PAIR && item > 0) {  // the other chain has read this chain's last O
+        const uint32_t w = item - 1;
+        if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1))) break;
+      }
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < nt; ++j) {
         const int tile = it.t0 + (PAIR ? j : 2 * j + i);
-        if (!(ok = bar_wait(at(ctl.s_full[i]), s_count & 1, abort))) break;
+        if (!(ok = bar_wait(at(ctl.s_full[i]), s_count & 1))) break;
         ++s_count;
         fence_after();
+        uint32_t x[kTile];
+        // Half of the row: p = exp2(c (s - m)), to tensor memory; gives its sum.
+        const auto half_row = [&](int half) {
+          const float mb = m == -INFINITY ? 0.f : -m * p.c;
+          float sum[4] = {};
+#pragma unroll
+          for (int k = 2 * half; k < 2 * half + 2; ++k) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a = __uint_as_float(x[32 * k + 2 * e]);
+              float b = __uint_as_float(x[32 * k + 2 * e + 1]);
+              fma2(a, b, p.c, mb);
+              a = ex2(a);
+              b = ex2(b);
+              add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], a, b);
+              w[e] = Pack2<T>::pack(a, b);
+            }
+            tmem_st16(ts + 16 * k, w);
+          }
+          return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        };
         if (any_valid) {
           // Hidden columns are set to -inf in tensor memory, 32 at a time and only where the
           // warp has some: a small loop beside the tile's long straight code.
@@ -812,7 +830,6 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             }
             tmem_wait_st();
           }
-          uint32_t x[kTile];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32(x + 32 * k, ts + 32 * k);
           tmem_wait_ld();
@@ -844,67 +861,31 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
               }
             }
           };
-          // Half of the row: p = exp2(c (s - m)), to tensor memory; gives its sum.
-          const auto half_row = [&](int half) {
-            const float mb = m == -INFINITY ? 0.f : -m * p.c;
-            float sum[4] = {};
-#pragma unroll
-            for (int k = 2 * half; k < 2 * half + 2; ++k) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float a = __uint_as_float(x[32 * k + 2 * e]);
-                float b = __uint_as_float(x[32 * k + 2 * e + 1]);
-                fma2(a, b, p.c, mb);
-                a = ex2(a);
-                b = ex2(b);
-                add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], a, b);
-                w[e] = Pack2<T>::pack(a, b);
-              }
-              tmem_st16(ts + 16 * k, w);
-            }
-            return (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          };
           move_max(row_max());
           l += half_row(0);
           tmem_wait_st();
-          // SPLIT: the other chain has read this chain's last O
-          if (!PAIR && j == 0 && item > 0) {
-            const uint32_t w = item - 1;
-            if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
-          }
-          fence_before();
-          bar_arrive(at(ctl.p_half[i]));
+        }
+        fence_before();
+        bar_arrive(at(ctl.p_half[i]));
+        if (any_valid) {
           l += half_row(1);
           tmem_wait_st();
-          fence_before();
-          bar_arrive(at(ctl.p_ready[i]));
-        } else {
-          if (!PAIR && j == 0 && item > 0) {
-            const uint32_t w = item - 1;
-            if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
-          }
-          fence_before();
-          bar_arrive(at(ctl.p_half[i]));
-          bar_arrive(at(ctl.p_ready[i]));
         }
+        fence_before();
+        bar_arrive(at(ctl.p_ready[i]));
       }
       if (!ok) break;
       if (nt > 0) {
-        if (!(ok = bar_wait(at(ctl.o_done[i]), o_count & 1, abort))) break;
+        if (!(ok = bar_wait(at(ctl.o_done[i]), o_count & 1))) break;
         ++o_count;
         fence_after();
       }
       float w0 = 1.f, w1 = 0.f;  // SPLIT: the chains' weights
       if (!PAIR) {
-        if (nt == 0 && item > 0) {  // (not waited for above)
-          const uint32_t w = item - 1;
-          if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1, abort))) break;
-        }
         ctl.ml[i][r] = make_float2(m, l);
         fence_before();
         bar_arrive(at(ctl.xchg));
-        if (!(ok = bar_wait(at(ctl.xchg), item & 1, abort))) break;
+        if (!(ok = bar_wait(at(ctl.xchg), item & 1))) break;
         fence_after();  // the other chain's O has been waited for by its own threads
         const float2 a = ctl.ml[0][r], b = ctl.ml[1][r];
         m = fmaxf(a.x, b.x);
@@ -916,7 +897,6 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       if (any_valid) {
         const bool whole = it.whole != 0;
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        const bool patch = ctl.item[item % kItems].bad != 0;
         constexpr int kCols = PAIR ? DP : DP / 2;
         const int c0 = PAIR ? 0 : i * kCols;
         // slot 0: the CTA's first piece, 1: its last
@@ -955,26 +935,6 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             }
           }
           if (valid) {
-            if (patch) {
-              // the non-finite values taken out of V that the row does attend
-              const uint16_t* const v =
-                  p.v + ((int64_t)it.b * p.H + it.h) * p.S * (int64_t)p.D + k;
-              const int row1 = min(it.row_end, (it.t0 + it.n) * kTile);
-#pragma unroll 1
-              for (int row = max(it.masked, it.t0) * kTile; row < row1; ++row) {
-                if (row >= it.start && !(p.is_tree ? (bits >> (row - it.start) & 1) != 0
-                                                   : row <= it.start + tok))
-                  continue;
-#pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                  if (k + e < p.D) {
-                    const float2 f = Pack2<T>::unpack(
-                        *reinterpret_cast<const uint32_t*>(v + (int64_t)row * p.D + e));
-                    if (!isfinite(f.x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f.x);
-                    if (!isfinite(f.y)) o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) + f.y);
-                  }
-              }
-            }
             if (whole) {
               uint32_t w[16];
 #pragma unroll
@@ -1003,6 +963,41 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       }
       fence_before();
       if (!PAIR) bar_arrive(at(ctl.o_read[item & 1]));
+      if (valid && ctl.item[item % kItems].bad != 0) {
+        // Rare: the non-finite values taken out of V that the row does attend are added to
+        // what it has just written.
+        constexpr int kCols = PAIR ? DP : DP / 2;
+        const int c0 = PAIR ? 0 : i * kCols, c1 = min(p.D, c0 + kCols);
+        const uint16_t* const v = p.v + ((int64_t)it.b * p.H + it.h) * p.S * (int64_t)p.D;
+        uint32_t* const out = reinterpret_cast<uint32_t*>(
+            p.out + (int64_t)(it.tok_at + tok) * p.out_stride + (int64_t)(it.h * p.G + g) * p.D);
+        constexpr int kRows = PAIR ? 2 * kTile : kTile;
+        float* const part =
+            p.part + (int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kRows * (p.D + 2) +
+            (int64_t)((PAIR ? i * kTile : 0) + r) * p.D;
+        const int row1 = min(it.row_end, (it.t0 + it.n) * kTile);
+#pragma unroll 1
+        for (int row = max(it.masked, it.t0) * kTile; row < row1; ++row) {
+          if (row >= it.start &&
+              !(p.is_tree ? (bits >> (row - it.start) & 1) != 0 : row <= it.start + tok))
+            continue;
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 2) {
+            float2 f = Pack2<T>::unpack(
+                *reinterpret_cast<const uint32_t*>(v + (int64_t)row * p.D + c));
+            if (isfinite(f.x) && isfinite(f.y)) continue;
+            f.x = isfinite(f.x) ? 0.f : f.x;
+            f.y = isfinite(f.y) ? 0.f : f.y;
+            if (it.whole) {
+              const float2 o = Pack2<T>::unpack(out[c / 2]);
+              out[c / 2] = Pack2<T>::pack(o.x + f.x, o.y + f.y);
+            } else {
+              part[c] += f.x;
+              part[c + 1] += f.y;
+            }
+          }
+        }
+      }
       __syncwarp();
       if (lane == 0) bar_arrive(at(ctl.item_empty[item % kItems]));
     }
@@ -1021,18 +1016,18 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 //   out = sum_i f_i O_i / sum_i f_i l_i,  f_i = exp2(m_i - max m).
 template <typename T, int MAXB>
 __global__ __launch_bounds__(256) void join_kernel(const __grid_constant__ AttnParams<MAXB> p,
-                                                   int ctas, int rows_per_unit) {
+                                                   int rows_per_unit) {
   ops_pdl_enter();
   const int i0 = blockIdx.x;
-  const int64_t at = cut(p, i0 + 1, ctas);
+  const int at = cut(p, i0 + 1);
   const Walk<AttnParams<MAXB>> walk(p, at, at + 1);  // the unit that holds place `at`
   if (walk.t == 0) return;                           // no unit is divided here
-  const int64_t lo = walk.pos, from = cut(p, i0, ctas);
+  const int lo = walk.pos, from = cut(p, i0);
   if (from > lo + p.unit_cost) return;  // an earlier cut divides it too
   const int rows_end = unit_rows(p, walk.b, walk.tok0);
-  const int64_t hi = lo + p.unit_cost + (rows_end + kTile - 1) / kTile;
+  const int hi = lo + p.unit_cost + (rows_end + kTile - 1) / kTile;
   int i1 = i0 + 1;  // the last CTA with a piece
-  while (cut(p, i1 + 1, ctas) < hi) ++i1;
+  while (cut(p, i1 + 1) < hi) ++i1;
   const int n_tok = min(p.seq.pre[walk.b + 1] - p.seq.pre[walk.b] - walk.tok0, p.unit_tok);
   const int lane = threadIdx.x & 31;
   const int64_t slot = (int64_t)rows_per_unit * (p.D + 2);
@@ -1104,7 +1099,7 @@ constexpr int kMinTiles = 4;  // a CTA's share is not cut below this many tiles
 // draining the two chains, its output), in tiles.
 constexpr int kUnitCostPair = DV_UCP, kUnitCostSplit = DV_UCS;
 
-Schedule schedule(const Plan& p, int group, bool is_tree, int64_t* tile_pre) {
+Schedule schedule(const Plan& p, int group, bool is_tree, int32_t* cost_pre) {
   Schedule s;
   s.tile_tok = kTile / group;
   s.pair = p.max_len > s.tile_tok;
@@ -1113,7 +1108,7 @@ Schedule schedule(const Plan& p, int group, bool is_tree, int64_t* tile_pre) {
   s.total = s.units = 0;
   int64_t all_tiles = 0;
   for (int b = 0; b < p.B; ++b) {
-    if (tile_pre) tile_pre[b] = s.total;
+    if (cost_pre) cost_pre[b] = (int32_t)s.total;
     const int n = p.seq_len[b], first = p.seq_start[b];
     int64_t tiles = 0;
     for (int64_t u = 0; u < n; u += s.unit_tok) {
@@ -1125,7 +1120,7 @@ Schedule schedule(const Plan& p, int group, bool is_tree, int64_t* tile_pre) {
     s.total += tiles * p.H;
     all_tiles += tiles * p.H;
   }
-  if (tile_pre) tile_pre[p.B] = s.total;
+  if (cost_pre) cost_pre[p.B] = (int32_t)s.total;
   const int64_t sms = sm_count();
   int64_t ctas = all_tiles / kMinTiles;
   if (ctas < s.units) ctas = s.units;
@@ -1167,7 +1162,7 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
                            float* part, size_t part_bytes, cudaStream_t stream) {
   AttnParams<MAXB> kp;
   const int group = q.q_heads / p.H;
-  const Schedule s = schedule(p, group, is_tree, kp.tile_pre);
+  const Schedule s = schedule(p, group, is_tree, kp.cost_pre);
   const bool fp16 = q.dtype == DV_DTYPE_FP16;
   const void* k = static_cast<const uint4*>(p.k) + p.l0 * p.layer_chunks;
   const void* v = static_cast<const uint4*>(p.v) + p.l0 * p.layer_chunks;
@@ -1200,7 +1195,8 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
   kp.tree = tree;
   kp.part = part;
   kp.out_stride = q.out_stride;
-  kp.total = s.total;
+  kp.share = (int32_t)(s.total / s.ctas);
+  kp.extra = (int32_t)(s.total % s.ctas);
   kp.H = p.H;
   kp.G = group;
   kp.D = p.D;
@@ -1222,8 +1218,8 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
                  : launch_kernel<T, 128, false, MAXB>(kp, s.ctas, stream);
   if (err != cudaSuccess) return cuda_fail(err, "attention launch");
   if (s.ctas > 1) {
-    void (*const join)(AttnParams<MAXB>, int, int) = join_kernel<T, MAXB>;
-    err = ops_launch(join, dim3((unsigned)s.ctas - 1, 8), 256, 0, stream, kp, (int)s.ctas,
+    void (*const join)(AttnParams<MAXB>, int) = join_kernel<T, MAXB>;
+    err = ops_launch(join, dim3((unsigned)s.ctas - 1, 8), 256, 0, stream, kp,
                      (s.pair ? 2 : 1) * kTile);
     if (err != cudaSuccess) return cuda_fail(err, "attention join launch");
   }
@@ -1258,7 +1254,10 @@ dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, cons
     return fail(DV_ERR_UNSUPPORTED, "%d drafted tokens of a sequence, more than %d", p.max_len,
                 DV_MAX_TREE);
   if (p.tokens == 0) return DV_OK;
-  const size_t need = schedule(p, q.q_heads / p.H, is_tree, nullptr).bytes;
+  const Schedule sch = schedule(p, q.q_heads / p.H, is_tree, nullptr);
+  const size_t need = sch.bytes;
+  if (sch.total > INT32_MAX)
+    return fail(DV_ERR_UNSUPPORTED, "%lld tiles of attention in one call", (long long)sch.total);
   if (workspace_bytes < need)
     return fail(DV_ERR_BUFFER_TOO_SMALL, "attention needs %zu workspace bytes (got %zu)", need,
                 workspace_bytes);
