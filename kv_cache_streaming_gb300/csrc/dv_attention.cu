@@ -108,7 +108,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // Waits for the phase of `parity` to complete; false when it gave up.  Kept
 // short: it stands at some thirty places, and the kernel's speed hangs on its
 // size (an instruction cache miss in every loop made ragged prompts twice as slow).
-__device__ __noinline__ bool gave_up() {
+__device__ __forceinline__ bool gave_up() {
   atomicExch(&g_attention_timeout, 1u);
   return false;
 }
@@ -262,7 +262,7 @@ struct Item {
   int row_end;  // rows [0, row_end) are attended by some row of the unit
   int t0, n;    // the piece's tiles [t0, t0 + n); n = 0: no more items
   int whole;    // the piece is the whole unit
-  int nt[2];    // tiles of each chain
+  int nt0, nt1;  // tiles of each chain
   int masked;   // the first tile that hides a row from some query row
   int start, n_tok, tok_at;  // the sequence's first new row, new tokens, place in packed buffers
   int bad;      // non-finite values were taken out of V
@@ -367,11 +367,11 @@ struct Walk {
       // chain 0's row tile may end earlier, chain 1's may be empty
       const int tok1 = tok0 + p.tile_tok;
       const int rows0 = p.is_tree ? row_end : start + min(tok1, n_tok);
-      it->nt[0] = max(0, min(t + n, (rows0 + kTile - 1) / kTile) - t);
-      it->nt[1] = tok1 < n_tok ? n : 0;
+      it->nt0 = max(0, min(t + n, (rows0 + kTile - 1) / kTile) - t);
+      it->nt1 = tok1 < n_tok ? n : 0;
     } else {
-      it->nt[0] = (n + 1) / 2;
-      it->nt[1] = n / 2;
+      it->nt0 = (n + 1) / 2;
+      it->nt1 = n / 2;
     }
     pos += p.unit_cost + cnt;
     t = 0;
@@ -485,6 +485,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   };
 
   if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 8) {
       // ---- the walk, and loads ----
       {
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         Item it, after;
         Ring<SM::kK> kr;
         Ring<SM::kV> vr;
-        uint32_t nk = 0, nv = 0, q_used[2] = {0, 0}, n_items = 0, n_q = 0;
+        uint32_t nk = 0, nv = 0, q0 = 0, q1 = 0, n_items = 0, n_q = 0;
         bool ok = true;
         const auto publish = [&](const Item& x) {
           if (n_items >= kItems)
@@ -508,9 +509,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         };
         const auto load_q = [&](const Item& x, int i) {
           const int qb = PAIR ? i : (int)(n_q & 1);
-          if (q_used[qb] > 0) ok = bar_wait(at(ctl.q_empty[qb]), (q_used[qb] - 1) & 1);
+          const uint32_t used = qb ? q1 : q0;  // the buffer's loads so far
+          if (used > 0) ok = bar_wait(at(ctl.q_empty[qb]), (used - 1) & 1);
           if (!ok) return;
-          ++q_used[qb];
+          if (qb) ++q1; else ++q0;
           ++n_q;
           const uint32_t bar = at(ctl.q_full[qb]);
           bar_expect(bar, (DP / 64) * 128 * p.G * p.tile_tok, on);
@@ -556,7 +558,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             if (PAIR)
 #pragma unroll 1
               for (int i = 0; i < 2 && ok; ++i)
-                if (it.nt[i] > 0) load_q(it, i);
+                if ((i ? it.nt1 : it.nt0) > 0) load_q(it, i);
             head = it.b * p.H + it.h;
           }
           if (!ok) break;
@@ -593,8 +595,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll 1
           for (uint32_t i = 0; i < SM::kV && i < nv; ++i)
             bar_wait(at(ctl.v_full[i]), (nv - i - 1) / SM::kV & 1);
-          for (int i = 0; i < 2; ++i)
-            if (q_used[i] > 0) bar_wait(at(ctl.q_full[i]), (q_used[i] - 1) & 1);
+          if (q0 > 0) bar_wait(at(ctl.q_full[0]), (q0 - 1) & 1);
+          if (q1 > 0) bar_wait(at(ctl.q_full[1]), (q1 - 1) & 1);
         }
       }
       __syncwarp();
@@ -616,9 +618,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         Item it;
         while (ok && get_item(n_items, &it)) {
           const int n = __shfl_sync(~0u, it.n, 0), t0 = __shfl_sync(~0u, it.t0, 0);
-          const int nt = __shfl_sync(~0u, it.nt[i], 0), row_end = __shfl_sync(~0u, it.row_end, 0);
+          const int nt = __shfl_sync(~0u, i ? it.nt1 : it.nt0, 0), row_end = __shfl_sync(~0u, it.row_end, 0);
           const int masked = __shfl_sync(~0u, it.masked, 0);
-          const int nt_other = __shfl_sync(~0u, it.nt[i ^ 1], 0);
+          const int nt_other = __shfl_sync(~0u, i ? it.nt0 : it.nt1, 0);
           const int qb = PAIR ? i : (int)(n_items & 1);
           const uint32_t q_parity = (PAIR ? n_q : n_items >> 1) & 1;
           if (nt > 0) ++n_q;
@@ -774,6 +776,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax: a chain's warpgroup, a thread per row ----
     const int i = warp >> 2, r = threadIdx.x & (kTile - 1);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
@@ -784,7 +787,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     Item it;
     for (; ok && get_item(item, &it); ++item) {
       const int tile_tok0 = it.tok0 + (PAIR ? i * p.tile_tok : 0);
-      const int tok = tile_tok0 + tr, nt = it.nt[i];
+      const int tok = tile_tok0 + tr, nt = i ? it.nt1 : it.nt0;
       const bool valid = tr < p.tile_tok && tok < it.n_tok;
       const bool any_valid = __any_sync(~0u, valid);
       uint64_t bits = 0;
@@ -930,7 +933,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         for (int k = c0; k < c0 + kCols; k += 32) {
           if (k >= p.D) break;
           uint32_t o[32];
-          if (it.nt[PAIR ? i : 0] > 0) {
+          if ((PAIR ? nt : it.nt0) > 0) {
             tmem_ld32(o, to + (PAIR ? i * kTile : 0) + k);
             tmem_wait_ld();
           } else {
@@ -941,7 +944,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               o[e] = __float_as_uint(w0 == 0.f ? 0.f : __uint_as_float(o[e]) * w0);
-            if (it.nt[1] > 0) {
+            if (it.nt1 > 0) {
               uint32_t o1[32];
               tmem_ld32(o1, to + kTile + k);
               tmem_wait_ld();
