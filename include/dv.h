@@ -633,6 +633,7 @@ dv_status dv_rope_init(dv_rope* rope, int32_t rot_dim, int32_t interleaved, doub
 typedef struct {
   int32_t dtype;   /* dv_dtype, of every buffer here and of the cache */
   int32_t q_heads; /* 0: keys and values only */
+  int64_t tokens;  /* T: what the buffers hold, and the ranges' sum (else DV_ERR_INVALID_ARG) */
   const void* k;   /* [T][num_heads][head_dim] */
   int64_t k_stride;
   const void* v; /* [T][num_heads][head_dim] */
@@ -661,6 +662,7 @@ typedef struct {
   int32_t dtype;   /* dv_dtype of q, out and the cache */
   int32_t q_heads; /* a multiple of num_heads, at most DV_MAX_GROUP times it; query head h
                       reads key head h / (q_heads / num_heads) */
+  int64_t tokens;  /* T: what q and out hold, and the ranges' sum (else DV_ERR_INVALID_ARG) */
   const void* q;   /* [T][q_heads][head_dim] */
   int64_t q_stride; /* elements from one token to the next, a multiple of 8 */
   void* out;        /* the same shape; does not overlap q */

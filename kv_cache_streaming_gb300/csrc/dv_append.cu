@@ -341,6 +341,9 @@ extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const in
     if (t.rope->interleaved != 0 && t.rope->interleaved != 1)
       return fail(DV_ERR_INVALID_ARG, "rope.interleaved is %d", t.rope->interleaved);
   }
+  if (t.tokens != p.tokens)
+    return fail(DV_ERR_INVALID_ARG, "the buffers hold %lld tokens, the ranges %lld",
+                (long long)t.tokens, (long long)p.tokens);
   if (p.tokens == 0) return DV_OK;
   if ((st = dv::resolve_cache(cache, &p)) != DV_OK) return st;
   void* dev = nullptr;

@@ -114,13 +114,14 @@ class dv_rope(ctypes.Structure):
 
 
 class dv_new_tokens(ctypes.Structure):
-    _fields_ = [("dtype", _I32), ("q_heads", _I32), ("k", _P), ("k_stride", _I64), ("v", _P),
+    _fields_ = [("dtype", _I32), ("q_heads", _I32), ("tokens", _I64), ("k", _P), ("k_stride", _I64), ("v", _P),
                 ("v_stride", _I64), ("q", _P), ("q_stride", _I64), ("q_out", _P),
-                ("q_out_stride", _I64), ("positions", _P), ("rope", ctypes.POINTER(dv_rope))]
+                ("q_out_stride", _I64), ("positions", _P), ("rope", _P)]
 
 
 class dv_queries(ctypes.Structure):
-    _fields_ = [("dtype", _I32), ("q_heads", _I32), ("q", _P), ("q_stride", _I64), ("out", _P),
+    _fields_ = [("dtype", _I32), ("q_heads", _I32), ("tokens", _I64), ("q", _P),
+                ("q_stride", _I64), ("out", _P),
                 ("out_stride", _I64), ("scale", ctypes.c_float)]
 
 
@@ -170,10 +171,28 @@ def _buf(x, nbytes=None):
     raise TypeError(f"cannot use {type(x).__name__} as a buffer")
 
 
+_current_raw_stream = None
+
+
+def _current_stream():
+    """torch's current stream as a raw handle, by the short way where torch has
+    it (building a Stream object costs microseconds)."""
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.current_stream()  # sets CUDA up
+        if raw is None or device is None:
+            _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _current_raw_stream = lambda: raw(device())  # noqa: E731
+    return _current_raw_stream()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -727,17 +746,18 @@ def _dtype(t):
     return d
 
 
-def _token_rows(t, name, tokens, heads, head_dim, dtype):
-    """(address, stride) of a [tokens, heads, head_dim] tensor whose tokens may
-    be strided."""
-    if tuple(t.shape) != (tokens, heads, head_dim):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}] (got {tuple(t.shape)})")
+def _token_rows(t, name, shape, dtype):
+    """(address, stride) of a tensor of ``shape`` (tokens, heads, head_dim) whose
+    tokens may be strided."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    n, heads, dim = shape
     s0, s1, s2 = t.stride()
-    if tokens and ((s2 != 1 and head_dim > 1) or (s1 != head_dim and heads > 1)):
+    if n and (s2 != 1 or (s1 != dim and heads > 1)):
         raise TypeError(f"{name}: a token's heads and elements must be contiguous")
-    return t.data_ptr(), s0 if tokens > 1 else heads * head_dim
+    return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
 def _words(t, name, tokens, size):
@@ -777,23 +797,25 @@ def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=No
     ``positions`` (int32, or None: their cache rows) and writes ``k`` and ``v``
     to rows [seq_start, seq_end) of ``layer``.  k, v: [T, num_heads, head_dim];
     q: [T, q_heads, head_dim]; T new tokens, packed.  Returns ``q_out``."""
-    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
-    n, H, D = int((e - s).sum()), cache.c.num_heads, cache.c.head_dim
-    t = dv_new_tokens(dtype=_dtype(k))
-    t.k, t.k_stride = _token_rows(k, "k", n, H, D, k.dtype)
-    t.v, t.v_stride = _token_rows(v, "v", n, H, D, k.dtype)
+    c = cache.c
+    s, e, sp, ep = _ranges(seq_start, seq_end, c.batch)
+    n, D, dtype = k.shape[0], c.head_dim, k.dtype
+    shape = (n, c.num_heads, D)
+    kp, ks = _token_rows(k, "k", shape, dtype)
+    vp, vs = _token_rows(v, "v", shape, dtype)
+    heads, qp, qs, op, os_ = 0, None, 0, None, 0
     if q is not None:
         if q.dim() != 3:
-            raise ValueError(f"q must be [{n}, q_heads, {D}] (got {tuple(q.shape)})")
+            raise ValueError(f"q must be [{n}, q_heads, {D}] (got {list(q.shape)})")
         if q_out is None:
             q_out = q.new_empty(q.shape)
-        t.q_heads = q.shape[1]
-        t.q, t.q_stride = _token_rows(q, "q", n, t.q_heads, D, k.dtype)
-        t.q_out, t.q_out_stride = _token_rows(q_out, "q_out", n, t.q_heads, D, k.dtype)
-    if positions is not None:
-        t.positions = _words(positions, "positions", n, 4)
-    if rope is not None:
-        t.rope = ctypes.pointer(rope.c if isinstance(rope, Rope) else rope)
+        heads = q.shape[1]
+        shape = (n, heads, D)
+        qp, qs = _token_rows(q, "q", shape, dtype)
+        op, os_ = _token_rows(q_out, "q_out", shape, dtype)
+    pos = None if positions is None else _words(positions, "positions", n, 4)
+    rp = None if rope is None else ctypes.addressof(rope.c if isinstance(rope, Rope) else rope)
+    t = dv_new_tokens(_dtype(k), heads, n, kp, ks, vp, vs, qp, qs, op, os_, pos, rp)
     _check(_append(cache.ref, layer, sp, ep, ctypes.byref(t), _stream(stream)))
     return q_out
 
@@ -805,14 +827,14 @@ def dv_attention_workspace(cache: Cache, seq_start, seq_end, q_heads) -> int:
     return out.value
 
 
-def _queries(cache, s, e, q, out, scale):
-    n, D = int((e - s).sum()), cache.c.head_dim
+def _queries(cache, q, out, scale):
     if q.dim() != 3:
-        raise ValueError(f"q must be [{n}, q_heads, {D}] (got {tuple(q.shape)})")
-    a = dv_queries(dtype=_dtype(q), q_heads=q.shape[1], scale=scale)
-    a.q, a.q_stride = _token_rows(q, "q", n, a.q_heads, D, q.dtype)
-    a.out, a.out_stride = _token_rows(out, "out", n, a.q_heads, D, q.dtype)
-    return n, a
+        raise ValueError(f"q must be [tokens, q_heads, {cache.c.head_dim}] (got {list(q.shape)})")
+    n, heads, _ = q.shape
+    shape, dtype = (n, heads, cache.c.head_dim), q.dtype
+    qp, qs = _token_rows(q, "q", shape, dtype)
+    op, os_ = _token_rows(out, "out", shape, dtype)
+    return n, dv_queries(_dtype(q), heads, n, qp, qs, op, os_, scale)
 
 
 def dv_prompt_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, workspace=None,
@@ -821,7 +843,7 @@ def dv_prompt_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, 
     over the cache rows up to their own, into ``out``.  ``workspace``: a device
     buffer of ``dv_attention_workspace`` bytes (None when that is 0)."""
     s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
-    _, a = _queries(cache, s, e, q, out, scale)
+    _, a = _queries(cache, q, out, scale)
     w, wn = _buf(workspace)
     _check(_prompt_attention(cache.ref, layer, sp, ep, ctypes.byref(a), w, wn, _stream(stream)))
 
@@ -832,7 +854,7 @@ def dv_tree_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, wo
     before them, and of the new rows those set in ``tree`` (T 64-bit integers;
     None: a chain, a decode step for one token)."""
     s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
-    n, a = _queries(cache, s, e, q, out, scale)
+    n, a = _queries(cache, q, out, scale)
     w, wn = _buf(workspace)
     t = None if tree is None else _words(tree, "tree", n, 8)
     _check(_tree_attention(cache.ref, layer, sp, ep, ctypes.byref(a), t, w, wn, _stream(stream)))

@@ -50,8 +50,9 @@ def test_attention_refusals(kind):
     _refused(dv.DV_ERR_UNSUPPORTED, lambda: call(c=_cache(D=60), D=60))
     with pytest.raises(TypeError):
         call(q=_qo(dt=torch.float32))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(q=_qo(n=4)))  # not the ranges' tokens
     with pytest.raises(ValueError):
-        call(q=_qo(n=4))
+        call(q=(_qo()[0], _qo(n=4)[1]))
     with pytest.raises(TypeError):  # elements of a head not contiguous
         q = torch.zeros(5, 64, 8, dtype=F16).transpose(1, 2)
         call(q=(q, torch.zeros(5, 8, 64, dtype=F16)))
