@@ -712,12 +712,13 @@ dv_status dv_attention_check(dv_stream stream);
 /* Moves rows together, in place, in layers [l0, l1): row seq_start[b] + i of
  * sequence b (for every i below its range's length) gets what row
  * keep[T-index of (b, i)] of the sequence held before the call.  keep: device
- * memory, T int32 entries, 4-byte aligned.  An entry that is negative, not
+ * memory, `count` = T int32 entries (else DV_ERR_INVALID_ARG), 4-byte aligned.  An entry that is negative, not
  * below max_seq, or below its own destination row leaves that row as it was
  * (so that a list of fixed length can be padded with -1).  Rows outside the
  * ranges are untouched.  Any elem_bytes. */
 dv_status dv_kv_compact(const dv_cache* cache, int32_t l0, int32_t l1, const int32_t* seq_start,
-                        const int32_t* seq_end, const int32_t* keep, dv_stream stream);
+                        const int32_t* seq_end, const int32_t* keep, int64_t count,
+                        dv_stream stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

@@ -18,6 +18,8 @@
 //    groups start at multiples of 8, so a range's edges alone leave lanes idle.
 //  * append_token_kernel: decode steps and short trees, a CTA per token and
 //    slice of its chunks, the angles' table in shared memory.
+#include <type_traits>
+
 #include "dv_ops.h"
 
 namespace dv {
@@ -56,56 +58,82 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turn, int32_t pos, float fact
   return make_float2(c * factor, s * factor);
 }
 
-// The frequency index of element d (d < rot), and the sign its partner's sine
-// takes: the first of a pair loses y sin, the second gains x sin.
-template <typename P>
-__device__ __forceinline__ int pair_of(const P& p, int d, float* sign) {
-  if (p.interleaved) {
-    *sign = (d & 1) ? 1.f : -1.f;
-    return d >> 1;
-  }
-  *sign = d < p.half ? -1.f : 1.f;
-  return d < p.half ? d : d - p.half;
-}
+// How pairs lie in a head's 16-byte chunks.
+enum Pairs {
+  kNeighbours,  // interleaved: both of a pair in one word
+  kHalves,      // the other half's chunk: rot / 2 a multiple of 8
+  kAcross       // the other half, at any element
+};
 
-// The partners of the 8 elements of chunk c of a head's row.
-template <typename P>
-__device__ __forceinline__ uint4 partner(const P& p, const uint16_t* row, int c, uint4 x) {
-  if (p.interleaved) {  // neighbours: swap the halves of each 32-bit word
-    return make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032),
-                      __byte_perm(x.z, 0, 0x1032), __byte_perm(x.w, 0, 0x1032));
-  }
+// The partners of the 8 elements of chunk c of a head's row x (kHalves, kAcross).
+template <Pairs W, typename P>
+__device__ __forceinline__ uint4 partner(const P& p, const uint16_t* row, int c) {
   const int d0 = c * 8;
-  if ((p.half & 7) == 0)  // a whole chunk of the other half
-    return __ldg(reinterpret_cast<const uint4*>(row) + (d0 < p.half ? c + (p.half >> 3) : c - (p.half >> 3)));
-  uint16_t y[8];
+  if constexpr (W == kHalves) {
+    return __ldg(reinterpret_cast<const uint4*>(row) +
+                 (d0 < p.half ? c + (p.half >> 3) : c - (p.half >> 3)));
+  } else {
+    uint16_t y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = d0 + i;
-    y[i] = d >= p.rot ? (uint16_t)0 : __ldg(row + (d < p.half ? d + p.half : d - p.half));
+    for (int i = 0; i < 8; ++i) {
+      const int d = d0 + i;
+      y[i] = d >= p.rot ? (uint16_t)0 : __ldg(row + (d < p.half ? d + p.half : d - p.half));
+    }
+    return make_uint4(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16,
+                      y[4] | (uint32_t)y[5] << 16, y[6] | (uint32_t)y[7] << 16);
   }
-  return make_uint4(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16,
-                    y[4] | (uint32_t)y[5] << 16, y[6] | (uint32_t)y[7] << 16);
 }
 
-// x cos + y sin for 8 elements, rounded once; the first `n` of them rotate,
-// the others keep their bits.
-template <typename T>
-__device__ __forceinline__ uint4 rotate(uint4 x, uint4 y, const float* cs, const float* sn, int n) {
+// A chunk's cosines and sines: of its 4 pairs (kNeighbours), or of its 8
+// elements with the sign that the partner's sine takes (the first of a pair
+// loses y sin, the second gains x sin).
+template <Pairs W>
+struct Angles {
+  static constexpr int N = W == kNeighbours ? 4 : 8;
+  float c[N], s[N];
+  // `of(f)`: cosine and sine of frequency f; the first n elements rotate
+  template <typename P, typename F>
+  __device__ __forceinline__ void fill(const P& p, int chunk, int n, F&& of) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = W == kNeighbours ? 2 * i : i, d = chunk * 8 + e;
+      c[i] = 1.f;
+      s[i] = 0.f;
+      if (e < n) {
+        const float2 w = of(W == kNeighbours ? d >> 1 : d < p.half ? d : d - p.half);
+        c[i] = w.x;
+        s[i] = W != kNeighbours && d < p.half ? -w.y : w.y;
+      }
+    }
+  }
+};
+
+// 8 elements turned, rounded once; the first n rotate, the others keep their bits.
+template <typename T, Pairs W>
+__device__ __forceinline__ uint4 rotate(uint4 x, uint4 y, const Angles<W>& a, int n) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = Pack2<T>::unpack(xs[i]), b = Pack2<T>::unpack(ys[i]);
-    const uint32_t w = Pack2<T>::pack(fmaf(b.x, sn[2 * i], a.x * cs[2 * i]),
-                                      fmaf(b.y, sn[2 * i + 1], a.y * cs[2 * i + 1]));
-    r[i] = 2 * i + 1 < n ? w : 2 * i < n ? (w & 0xffffu) | (xs[i] & 0xffff0000u) : xs[i];
+    const float2 u = Pack2<T>::unpack(xs[i]);
+    uint32_t w;
+    if (W == kNeighbours) {
+      w = Pack2<T>::pack(fmaf(-u.y, a.s[i], u.x * a.c[i]), fmaf(u.x, a.s[i], u.y * a.c[i]));
+      r[i] = 2 * i < n ? w : xs[i];
+    } else {
+      const float2 v = Pack2<T>::unpack(ys[i]);
+      w = Pack2<T>::pack(fmaf(v.x, a.s[2 * i], u.x * a.c[2 * i]),
+                         fmaf(v.y, a.s[2 * i + 1], u.y * a.c[2 * i + 1]));
+      r[i] = 2 * i + 1 < n ? w : 2 * i < n ? (w & 0xffffu) | (xs[i] & 0xffff0000u) : xs[i];
+    }
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <typename T, int MAXB>
-__global__ __launch_bounds__(kAppendThreads) void append_tile_kernel(
+// Four CTAs an SM: with the 87 registers the compiler would take, two of them
+// kept too few loads in flight (ragged prompts at 2.7 TB/s).
+template <typename T, Pairs W, int MAXB>
+__global__ __launch_bounds__(kAppendThreads, 4) void append_tile_kernel(
     const __grid_constant__ AppendParams<MAXB> p) {
   ops_pdl_enter();
   const int lane = threadIdx.x & 31;
@@ -123,57 +151,60 @@ __global__ __launch_bounds__(kAppendThreads) void append_tile_kernel(
   const int64_t tok = p.seq.pre[b] + (row - s);
 
   const int nrot = min(8, max(0, p.rot - c * 8));  // rotated elements of the chunk
-  float cs[8], sn[8];
+  Angles<W> ang;
   if (nrot > 0) {
     const int32_t pos = p.positions ? p.positions[tok] : row;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i < nrot) {
-        float sign;
-        const int f = pair_of(p, c * 8 + i, &sign);
-        if (p.interleaved && (i & 1)) {  // the pair's first element has them
-          cs[i] = cs[i - 1];
-          sn[i] = -sn[i - 1];
-        } else {
-          const float2 w = cos_sin(p.turn[f], pos, p.factor);
-          cs[i] = w.x;
-          sn[i] = sign * w.y;
-        }
-      } else {
-        cs[i] = 1.f;
-        sn[i] = 0.f;
-      }
-    }
+    ang.fill(p, c, nrot, [&](int f) { return cos_sin(p.turn[f], pos, p.factor); });
   }
-  constexpr int U = 4;  // heads in flight
-  const auto rows = [&](const uint16_t* base, int heads, bool turn, auto&& put) {
+  // `put(chunk of head h)` for the warp's heads, U of them in flight.
+  const auto turned = [&](const uint16_t* base, int heads, auto&& put) {
+    constexpr int U = W == kNeighbours ? 4 : 3;
+#pragma unroll 1
     for (int h = h0; h < heads; h += U * step) {
       uint4 x[U], y[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (h + u * step < heads) {
-          const uint16_t* r = base + (int64_t)(h + u * step) * p.D;
+          const uint16_t* r = base + (h + u * step) * p.D;
           x[u] = __ldg(reinterpret_cast<const uint4*>(r) + c);
-          if (turn) y[u] = partner(p, r, c, x[u]);
+          y[u] = W == kNeighbours ? x[u] : partner<W>(p, r, c);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (h + u * step < heads) put(h + u * step, turn ? rotate<T>(x[u], y[u], cs, sn, nrot) : x[u]);
+        if (h + u * step < heads) put(h + u * step, rotate<T, W>(x[u], y[u], ang, nrot));
     }
   };
-  const int64_t head0 = (int64_t)b * p.H;
-  rows(p.q + tok * p.q_stride, p.Hq, nrot > 0, [&](int h, uint4 x) {
-    reinterpret_cast<uint4*>(p.q_out + tok * p.q_out_stride + (int64_t)h * p.D)[c] = x;
-  });
-  rows(p.k + tok * p.k_stride, p.H, nrot > 0, [&](int h, uint4 x) {
-    p.kc[((head0 + h) * p.C + c) * p.S + row] = x;
-  });
-  rows(p.v + tok * p.v_stride, p.H, false, [&](int h, uint4 x) {
-    p.vc[((head0 + h) * p.S + row) * p.C + c] = x;
-  });
+  const auto copied = [&](const uint16_t* base, int heads, auto&& put) {
+    constexpr int U = 6;
+#pragma unroll 1
+    for (int h = h0; h < heads; h += U * step) {
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * step < heads)
+          x[u] = __ldg(reinterpret_cast<const uint4*>(base + (h + u * step) * p.D) + c);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * step < heads) put(h + u * step, x[u]);
+    }
+  };
+  uint4* const qo = reinterpret_cast<uint4*>(p.q_out + tok * p.q_out_stride) + c;
+  uint4* const kc = p.kc + ((int64_t)b * p.H * p.C + c) * p.S + row;
+  uint4* const vc = p.vc + ((int64_t)b * p.H * p.S + row) * p.C + c;
+  const auto put_q = [&](int h, uint4 x) { qo[h * p.C] = x; };
+  const auto put_k = [&](int h, uint4 x) { kc[(int64_t)h * p.C * p.S] = x; };
+  if (nrot > 0) {
+    turned(p.q + tok * p.q_stride, p.Hq, put_q);
+    turned(p.k + tok * p.k_stride, p.H, put_k);
+  } else {
+    copied(p.q + tok * p.q_stride, p.Hq, put_q);
+    copied(p.k + tok * p.k_stride, p.H, put_k);
+  }
+  copied(p.v + tok * p.v_stride, p.H,
+         [&](int h, uint4 x) { vc[(int64_t)h * p.S * p.C] = x; });
 }
 
-template <typename T, int MAXB>
+template <typename T, Pairs W, int MAXB>
 __global__ __launch_bounds__(kAppendThreads) void append_token_kernel(
     const __grid_constant__ AppendParams<MAXB> p) {
   __shared__ float2 table[DV_MAX_ROT / 2];
@@ -198,16 +229,9 @@ __global__ __launch_bounds__(kAppendThreads) void append_token_kernel(
     uint4 x = __ldg(reinterpret_cast<const uint4*>(r) + c);
     const int nrot = min(8, max(0, p.rot - c * 8));
     if (kind != 2 && nrot > 0) {
-      const uint4 y = partner(p, r, c, x);
-      float cs[8], sn[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float sign = 0.f;
-        const float2 w = k < nrot ? table[pair_of(p, c * 8 + k, &sign)] : make_float2(1.f, 0.f);
-        cs[k] = w.x;
-        sn[k] = sign * w.y;
-      }
-      x = rotate<T>(x, y, cs, sn, nrot);
+      Angles<W> ang;
+      ang.fill(p, c, nrot, [&](int f) { return table[f]; });
+      x = rotate<T, W>(x, W == kNeighbours ? x : partner<W>(p, r, c), ang, nrot);
     }
     const int64_t head = (int64_t)b * p.H + h;
     if (kind == 0)
@@ -219,7 +243,7 @@ __global__ __launch_bounds__(kAppendThreads) void append_token_kernel(
   }
 }
 
-template <typename T, int MAXB>
+template <typename T, Pairs W, int MAXB>
 cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t stream) {
   AppendParams<MAXB> kp;
   kp.q = static_cast<const uint16_t*>(t.q);
@@ -251,7 +275,7 @@ cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t st
     // one chunk a thread while the grid is small, more once it fills the GPU
     const int fit = (int)((int64_t)152 * 64 / p.tokens);
     const int y = slices < fit ? slices : fit > 1 ? fit : 1;
-    return ops_launch(append_token_kernel<T, MAXB>, dim3((unsigned)p.tokens, y < 65535 ? y : 65535),
+    return ops_launch(append_token_kernel<T, W, MAXB>, dim3((unsigned)p.tokens, y < 65535 ? y : 65535),
                       kAppendThreads, 0, stream, kp);
   }
   int64_t groups = 0;
@@ -271,7 +295,7 @@ cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t st
   if (warps < quads) warps = quads;
   int64_t y = (warps + kWarps - 1) / kWarps;
   if (y > 65535) y = 65535;
-  return ops_launch(append_tile_kernel<T, MAXB>, dim3((unsigned)groups, (unsigned)y),
+  return ops_launch(append_tile_kernel<T, W, MAXB>, dim3((unsigned)groups, (unsigned)y),
                     kAppendThreads, 0, stream, kp);
 }
 
@@ -366,13 +390,19 @@ extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const in
                                              &dev)) != DV_OK)
     return st;
   if (t.positions) t.positions = static_cast<const int32_t*>(dev);
-  cudaError_t err;
-  const bool small = p.B <= dv::kSmallBatch;
-  if (t.dtype == DV_DTYPE_FP16)
-    err = small ? dv::launch_append<__half, dv::kSmallBatch>(p, t, stream)
-                : dv::launch_append<__half, dv::kMaxBatch>(p, t, stream);
-  else
-    err = small ? dv::launch_append<__nv_bfloat16, dv::kSmallBatch>(p, t, stream)
-                : dv::launch_append<__nv_bfloat16, dv::kMaxBatch>(p, t, stream);
+  const auto launch = [&](auto elem) {
+    using T = decltype(elem);
+    const auto batch = [&](auto pairs) {
+      constexpr dv::Pairs W = decltype(pairs)::value;
+      return p.B <= dv::kSmallBatch ? dv::launch_append<T, W, dv::kSmallBatch>(p, t, stream)
+                                    : dv::launch_append<T, W, dv::kMaxBatch>(p, t, stream);
+    };
+    if (t.rope && t.rope->interleaved)
+      return batch(std::integral_constant<dv::Pairs, dv::kNeighbours>());
+    if (!t.rope || t.rope->rot_dim % 16 == 0)
+      return batch(std::integral_constant<dv::Pairs, dv::kHalves>());
+    return batch(std::integral_constant<dv::Pairs, dv::kAcross>());
+  };
+  const cudaError_t err = t.dtype == DV_DTYPE_FP16 ? launch(__half()) : launch(__nv_bfloat16());
   return err == cudaSuccess ? DV_OK : dv::cuda_fail(err, "append launch");
 }

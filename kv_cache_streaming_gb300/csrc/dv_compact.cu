@@ -16,7 +16,7 @@ namespace dv {
 namespace {
 
 constexpr int kCompactThreads = 256;
-constexpr int kCells = 16;  // 16-byte chunks in flight per lane
+constexpr int kCells = 16;  // 16-byte chunks in flight per lane; 4 where the longest range needs no more
 
 template <int MAXB>
 struct CompactParams {
@@ -30,7 +30,7 @@ struct CompactParams {
   SeqTable<MAXB> seq;
 };
 
-template <int MAXB>
+template <int U, int MAXB>
 __global__ __launch_bounds__(kCompactThreads) void compact_kernel(
     const __grid_constant__ CompactParams<MAXB> p) {
   ops_pdl_enter();
@@ -49,19 +49,22 @@ __global__ __launch_bounds__(kCompactThreads) void compact_kernel(
   const int cw = min(p.slice, p.C - c0);
   uint4* base = (is_k ? p.k : p.v) + (p.l0 + (lkv >> 1)) * p.layer_chunks +
                 ((int64_t)b * p.H + h) * p.C * p.S;
-  const int step = kCells * 32 / cw;
+  const int step = U * 32 / cw;
   for (int i0 = 0; i0 < n; i0 += step) {
     const int m = min(step, n - i0);  // rows of this step
     const int cells = m * cw;
-    uint4 x[kCells];
-    int64_t to[kCells];
+    // K: a lane per row, then the next chunk; V: a row's chunks side by side.  The
+    // quotient by a multiplication (j and the divisor are at most 512).
+    const uint32_t inner = is_k ? m : cw, inv = ((1u << 20) + inner - 1) / inner;
+    uint4 x[U];
+    int64_t to[U];
 #pragma unroll
-    for (int u = 0; u < kCells; ++u) {
-      const int j = u * 32 + lane;
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = u * 32 + lane;
       to[u] = -1;
-      if (j < cells) {
-        const int i = is_k ? j % m : j / cw;
-        const int c = c0 + (is_k ? j / m : j % cw);
+      if (j < (uint32_t)cells) {
+        const int outer = (int)((j * inv) >> 20), rest = (int)(j - outer * inner);
+        const int i = is_k ? rest : outer, c = c0 + (is_k ? outer : rest);
         const int dst = s + i0 + i, src = __ldg(p.keep + t0 + i0 + i);
         if (src > dst && src < p.S) {  // an entry outside this leaves its row alone
           const int64_t row = is_k ? (int64_t)c * p.S : c, pitch = is_k ? 1 : p.C;
@@ -72,7 +75,7 @@ __global__ __launch_bounds__(kCompactThreads) void compact_kernel(
     }
     __syncwarp();
 #pragma unroll
-    for (int u = 0; u < kCells; ++u)
+    for (int u = 0; u < U; ++u)
       if (to[u] >= 0) base[to[u]] = x[u];
     __syncwarp();
   }
@@ -103,7 +106,12 @@ cudaError_t launch_compact(const Plan& p, const int32_t* keep, cudaStream_t stre
   kp.units = rows * kp.slices;
   const int64_t ctas = (kp.units + kCompactThreads / 32 - 1) / (kCompactThreads / 32);
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  return ops_launch(compact_kernel<MAXB>, dim3((unsigned)ctas), kCompactThreads, 0, stream, kp);
+  // Few rows (an accepted path): a quarter of the registers, so that more warps are resident.
+  if ((int64_t)p.max_len * slice <= 4 * 32)
+    return ops_launch(compact_kernel<4, MAXB>, dim3((unsigned)ctas), kCompactThreads, 0, stream,
+                      kp);
+  return ops_launch(compact_kernel<kCells, MAXB>, dim3((unsigned)ctas), kCompactThreads, 0, stream,
+                    kp);
 }
 
 }  // namespace
@@ -111,11 +119,14 @@ cudaError_t launch_compact(const Plan& p, const int32_t* keep, cudaStream_t stre
 
 extern "C" dv_status dv_kv_compact(const dv_cache* cache, int32_t l0, int32_t l1,
                                    const int32_t* seq_start, const int32_t* seq_end,
-                                   const int32_t* keep, dv_stream stream) {
+                                   const int32_t* keep, int64_t count, dv_stream stream) {
   dv::Trace trace("dv_kv_compact");
   dv::Plan p;
   dv_status st = dv::plan_ranges(cache, l0, l1, seq_start, seq_end, &p);
   if (st != DV_OK) return st;
+  if (count != p.tokens)
+    return dv::fail(DV_ERR_INVALID_ARG, "keep holds %lld entries, the ranges %lld",
+                    (long long)count, (long long)p.tokens);
   if (p.bytes == 0) return DV_OK;
   if ((int64_t)p.H * p.C > INT32_MAX / 2 || 2 * (int64_t)(l1 - l0) * p.B * p.H > INT32_MAX)
     return dv::fail(DV_ERR_UNSUPPORTED, "%d layers, %d sequences, %d heads of %d chunks", l1 - l0,

@@ -135,7 +135,7 @@ _prompt_attention = _sig("dv_prompt_attention", [_CP, _I32, _I32P, _I32P,
 _tree_attention = _sig("dv_tree_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
                                              _P, _P, _SZ, _P])
 _attention_check = _sig("dv_attention_check", [_P])
-_compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _P])
+_compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _I64, _P])
 
 
 class DvError(RuntimeError):
@@ -760,13 +760,19 @@ def _token_rows(t, name, shape, dtype):
     return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
-def _words(t, name, tokens, size):
-    if t.numel() != tokens or t.element_size() != size or t.is_floating_point():
-        raise ValueError(f"{name} must hold {tokens} integers of {size} bytes (got "
-                         f"{tuple(t.shape)} {t.dtype})")
+def _words(t, name, size):
+    """Address of a contiguous integer tensor of ``size``-byte words."""
+    if t.element_size() != size or t.is_floating_point():
+        raise ValueError(f"{name} must hold integers of {size} bytes (got {t.dtype})")
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _words_of(t, name, n, size):
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} integers (got {list(t.shape)})")
+    return _words(t, name, size)
 
 
 def dv_rope_init(rot_dim, interleaved=False, base=10000.0, scaling=DV_ROPE_NONE, factor=1.0,
@@ -813,7 +819,7 @@ def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=No
         shape = (n, heads, D)
         qp, qs = _token_rows(q, "q", shape, dtype)
         op, os_ = _token_rows(q_out, "q_out", shape, dtype)
-    pos = None if positions is None else _words(positions, "positions", n, 4)
+    pos = None if positions is None else _words_of(positions, "positions", n, 4)
     rp = None if rope is None else ctypes.addressof(rope.c if isinstance(rope, Rope) else rope)
     t = dv_new_tokens(_dtype(k), heads, n, kp, ks, vp, vs, qp, qs, op, os_, pos, rp)
     _check(_append(cache.ref, layer, sp, ep, ctypes.byref(t), _stream(stream)))
@@ -856,7 +862,7 @@ def dv_tree_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, wo
     s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
     n, a = _queries(cache, q, out, scale)
     w, wn = _buf(workspace)
-    t = None if tree is None else _words(tree, "tree", n, 8)
+    t = None if tree is None else _words_of(tree, "tree", n, 8)
     _check(_tree_attention(cache.ref, layer, sp, ep, ctypes.byref(a), t, w, wn, _stream(stream)))
 
 
@@ -870,5 +876,5 @@ def dv_kv_compact(cache: Cache, l0, l1, seq_start, seq_end, keep, stream=None) -
     """Row seq_start[b] + i of every sequence gets row keep[...] of it, in
     place, in layers [l0, l1); ``keep``: int32, packed over the ranges."""
     s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
-    kp = _words(keep, "keep", int((e - s).sum()), 4)
-    _check(_compact(cache.ref, l0, l1, sp, ep, kp, _stream(stream)))
+    _check(_compact(cache.ref, l0, l1, sp, ep, _words(keep, "keep", 4), keep.numel(),
+                    _stream(stream)))
