@@ -25,7 +25,7 @@
 namespace dv {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kTileRows = 8;  // cache rows of a warp in the tile kernel
 // Ranges of fewer tokens than this on average go to the token kernel: the
 // tile kernel's lanes are tied to 8 rows, so shorter ranges leave most idle.
@@ -130,10 +130,10 @@ __device__ __forceinline__ uint4 rotate(uint4 x, uint4 y, const Angles<W>& a, in
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Four CTAs an SM: with the 87 registers the compiler would take, two of them
-// kept too few loads in flight (ragged prompts at 2.7 TB/s).
+// 1024 threads an SM: with the 87 registers the compiler would take, half of
+// them kept too few loads in flight (ragged prompts at 2.7 TB/s).
 template <typename T, Pairs W, int MAXB>
-__global__ __launch_bounds__(kAppendThreads, 4) void append_tile_kernel(
+__global__ __launch_bounds__(kAppendThreads, 8) void append_tile_kernel(
     const __grid_constant__ AppendParams<MAXB> p) {
   ops_pdl_enter();
   const int lane = threadIdx.x & 31;
@@ -285,14 +285,11 @@ cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t st
     if (e > s) groups += (e + kTileRows - 1) / kTileRows - s / kTileRows;
   }
   kp.group_pre[p.B] = (int32_t)groups;
-  // Warps over the heads: enough of them to fill the GPU (8 CTAs of 8 warps an
-  // SM), but at least 4 heads to a warp, so that a chunk's angles are used again.
+  // Warps over the heads: 4 heads to a warp, what it has in flight at once (451 MB of ragged
+  // prompts in 87 us; 99 at 2 heads, 92 at 6, 101 where a warp walked over 30).
   const int quads = (p.C + 3) / 4;
   const int most_heads = t.q_heads > p.H ? t.q_heads : p.H;
-  int64_t warps = ((int64_t)152 * 64 + groups - 1) / groups;  // a group's warps
-  const int64_t cap = (int64_t)quads * ((most_heads + 3) / 4);
-  if (warps > cap) warps = cap;
-  if (warps < quads) warps = quads;
+  const int64_t warps = (int64_t)quads * ((most_heads + 3) / 4);
   int64_t y = (warps + kWarps - 1) / kWarps;
   if (y > 65535) y = 65535;
   return ops_launch(append_tile_kernel<T, W, MAXB>, dim3((unsigned)groups, (unsigned)y),

@@ -522,7 +522,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         };
         // In the order K0 V0 K1 V1 ...; a unit's queries before its first K.
         int j = 0, head = 0, v_row = 0, v_rows = 0;  // the V tile that is due (none: v_rows 0)
-        bool first = true;
+        bool fetch = true, step = true;  // the next unit is to be published; to be begun
 #pragma unroll 1
         while (ok) {
           if (v_rows > 0) {
@@ -543,23 +543,23 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             ++nv;
             v_rows = 0;
           }
-          if (j == 0) {
-            if (!first && it.n == 0) break;
-            // ahead of need: the next unit, SPLIT its queries
+          if (fetch) {  // ahead of need, under a unit's first loads: the next unit, SPLIT its queries
             walk.template next<PAIR>(&after);
             publish(after);
             if (!PAIR && ok && after.n > 0) load_q(after, 0);
-            if (first) {
-              first = false;
-              it = after;
-              continue;
-            }
+            fetch = false;
+          }
+          if (step) {
+            it = after;
+            if (it.n == 0) break;
+            j = 0;
+            step = false;
+            head = it.b * p.H + it.h;
             // (the row tiles' buffers are free once the unit before has used them up)
             if (PAIR)
 #pragma unroll 1
               for (int i = 0; i < 2 && ok; ++i)
                 if ((i ? it.nt1 : it.nt0) > 0) load_q(it, i);
-            head = it.b * p.H + it.h;
           }
           if (!ok) break;
           const int row = (it.t0 + j) * kTile, rows = min(kTile, it.row_end - row);
@@ -582,10 +582,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           ++nk;
           v_row = row;
           v_rows = rows;
-          if (++j == it.n) {
-            it = after;
-            j = 0;
-          }
+          fetch = j == 0;
+          step = ++j == it.n;
         }
         // A CTA that gave up leaves no copy in flight.
         if (!ok) {
