@@ -10,12 +10,13 @@
 //
 // Memory bound: every value is read once and written once (the half layout's
 // partner chunk comes from L1).  Two kernels:
-//  * append_tile_kernel: a warp covers 8 consecutive cache rows x 4 chunks of
-//    16 bytes, and walks over heads with its lanes' 8 cosines and sines in
-//    registers.  On the token-major side that is 64 contiguous bytes a token,
-//    on the x-interleaved K side 128 contiguous bytes a chunk row: whole
-//    32-byte sectors on both, with no transpose through shared memory.  Row
-//    groups start at multiples of 8, so a range's edges alone leave lanes idle.
+//  * append_tile_kernel: a warp covers 4 consecutive cache rows x 8 chunks of
+//    16 bytes, and walks over heads with its lanes' cosines and sines in
+//    registers.  On the token-major side that is 128 contiguous bytes a token, on
+//    the x-interleaved K side 64 a chunk row: whole 32-byte sectors on both, with
+//    no transpose through shared memory.  Row groups start at multiples of 4, so
+//    a range's edges alone leave lanes idle.  (451 MB of ragged prompts, 40 heads of
+//    128: 72 us, 6.3 TB/s; as 8 rows x 4 chunks 87 us, as 16 x 2 94 us.)
 //  * append_token_kernel: decode steps and short trees, a CTA per token and
 //    slice of its chunks, the angles' table in shared memory.
 #include <type_traits>
@@ -26,9 +27,10 @@ namespace dv {
 namespace {
 
 constexpr int kAppendThreads = 128;
-constexpr int kTileRows = 8;  // cache rows of a warp in the tile kernel
+constexpr int kTileRows = 4;    // cache rows of a warp in the tile kernel
+constexpr int kTileChunks = 8;  // and 16-byte chunks of them
 // Ranges of fewer tokens than this on average go to the token kernel: the
-// tile kernel's lanes are tied to 8 rows, so shorter ranges leave most idle.
+// tile kernel's lanes are tied to 4 rows, so shorter ranges leave most idle.
 constexpr int kTileMinMean = 4;
 
 template <int MAXB>
@@ -46,7 +48,7 @@ struct AppendParams {
   float factor;
   uint64_t turn[DV_MAX_ROT / 2];
   SeqTable<MAXB> seq;
-  int32_t group_pre[MAXB + 1];  // tile kernel: 8-row groups before the sequence
+  int32_t group_pre[MAXB + 1];  // tile kernel: row groups before the sequence
 };
 
 __device__ __forceinline__ float2 cos_sin(uint64_t turn, int32_t pos, float factor) {
@@ -138,14 +140,14 @@ __global__ __launch_bounds__(kAppendThreads, 8) void append_tile_kernel(
   ops_pdl_enter();
   const int lane = threadIdx.x & 31;
   const int gid = blockIdx.y * (kAppendThreads / 32) + (threadIdx.x >> 5);
-  const int quads = (p.C + 3) >> 2;
-  const int step = (gridDim.y * (kAppendThreads / 32)) / quads;  // warps over the heads
-  const int quad = gid % quads, h0 = gid / quads;
+  const int parts = (p.C + kTileChunks - 1) / kTileChunks;  // of a head's row
+  const int step = (gridDim.y * (kAppendThreads / 32)) / parts;  // warps over the heads
+  const int part = gid % parts, h0 = gid / parts;
   if (h0 >= step) return;
   const int b = find_span(p.group_pre, p.seq.batch, blockIdx.x);
   const int s = p.seq.start[b];
-  const int row = ((s >> 3) + (blockIdx.x - p.group_pre[b])) * kTileRows + (lane & 7);
-  const int c = quad * 4 + (lane >> 3);
+  const int row = (s / kTileRows + (blockIdx.x - p.group_pre[b])) * kTileRows + (lane & (kTileRows - 1));
+  const int c = part * kTileChunks + lane / kTileRows;
   const int n = p.seq.pre[b + 1] - p.seq.pre[b];
   if (row < s || row >= s + n || c >= p.C) return;
   const int64_t tok = p.seq.pre[b] + (row - s);
@@ -285,11 +287,11 @@ cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t st
     if (e > s) groups += (e + kTileRows - 1) / kTileRows - s / kTileRows;
   }
   kp.group_pre[p.B] = (int32_t)groups;
-  // Warps over the heads: 4 heads to a warp, what it has in flight at once (451 MB of ragged
-  // prompts in 87 us; 99 at 2 heads, 92 at 6, 101 where a warp walked over 30).
-  const int quads = (p.C + 3) / 4;
+  // Warps over the heads: 4 heads to a warp, what it has in flight at once (as 8 rows x 4
+  // chunks: 87 us of ragged prompts; 99 at 2 heads, 92 at 6, 101 where a warp walked over 30).
+  const int parts = (p.C + kTileChunks - 1) / kTileChunks;
   const int most_heads = t.q_heads > p.H ? t.q_heads : p.H;
-  const int64_t warps = (int64_t)quads * ((most_heads + 3) / 4);
+  const int64_t warps = (int64_t)parts * ((most_heads + 3) / 4);
   int64_t y = (warps + kWarps - 1) / kWarps;
   if (y > 65535) y = 65535;
   return ops_launch(append_tile_kernel<T, W, MAXB>, dim3((unsigned)groups, (unsigned)y),
