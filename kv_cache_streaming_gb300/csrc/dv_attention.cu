@@ -50,6 +50,7 @@ namespace {
 constexpr int kTile = 128;        // rows of Q and of K/V in a tile
 constexpr int kThreadsAttn = 384;  // two softmax warpgroups, and one of the other warps
 constexpr uint32_t kSpinLimit = 1u << 22;
+constexpr int kJoinThreads = 256;
 constexpr int kTurnPolls = 32;     // of another chain's progress, a preference (about 1 us)
 constexpr float kLazy = 8.f;       // log2 of the growth that is left to the old maximum
 
@@ -57,6 +58,13 @@ constexpr float kLazy = 8.f;       // log2 of the growth that is left to the old
 __device__ unsigned int g_attention_timeout;
 // The second half of the last contraction step when head_dim is an odd number of chunks.
 __device__ uint4 g_zero_rows[kTile];
+
+// A unit that a cut divides (the first cut that does), for the join.
+struct Divided {
+  int32_t tok, head, tokens;  // first token and query head of its output; tokens (0: none here)
+  int32_t last, slot;         // the last CTA with a piece; the first piece's slot
+  int32_t pad[3];
+};
 
 template <int MAXB>
 struct AttnParams {
@@ -68,7 +76,8 @@ struct AttnParams {
   const uint4* k;
   const uint16_t* v;
   const uint64_t* tree;
-  float* part;
+  float* part;       // two slots a CTA for pieces' sums
+  Divided* divided;  // of the cut before each CTA but the first
   int64_t out_stride;
   int32_t share, extra;  // a CTA's part of the units' cost; the first `extra` have one more
   int32_t H, G, D, C, S;
@@ -475,7 +484,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(~0u, ctl.tmem, 0);
-  ops_pdl_enter();
+  // (Global memory is touched only past this; the load warp finds its first unit before.)
+  if (warp != 8) ops_pdl_enter();
 
   // The k-th item, from the ring.
   const auto get_item = [&](uint32_t k, Item* it) {
@@ -492,6 +502,24 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         const bool on = elect();
         Walk<AttnParams<MAXB>> walk(p, cut(p, blockIdx.x),
                                     cut(p, blockIdx.x + 1));
+        ops_pdl_enter();
+        if (blockIdx.x > 0 && on) {
+          Divided d = {};
+          const int from = cut(p, blockIdx.x - 1);
+          if (walk.t > 0 && from <= walk.pos + p.unit_cost) {
+            const int n_tok = p.seq.pre[walk.b + 1] - p.seq.pre[walk.b] - walk.tok0;
+            const int end = walk.pos + p.unit_cost +
+                            (unit_rows(p, walk.b, walk.tok0) + kTile - 1) / kTile;
+            d.tok = p.seq.pre[walk.b] + walk.tok0;
+            d.head = walk.h * p.G;
+            d.tokens = min(n_tok, p.unit_tok);
+            d.last = blockIdx.x;
+#pragma unroll 1
+            while (cut(p, d.last + 1) < end) ++d.last;
+            d.slot = from < walk.pos ? 1 : 0;
+          }
+          p.divided[blockIdx.x - 1] = d;
+        }
         Item it, after;
         Ring<SM::kK> kr;
         Ring<SM::kV> vr;
@@ -1030,59 +1058,69 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 
 // ---- the join ----------------------------------------------------------------------
 
-// Adds up the pieces of the unit that the cut after CTA blockIdx.x divides, if
-// that is the unit's first cut:
+struct JoinParams {
+  uint16_t* out;
+  const float* part;
+  const Divided* divided;
+  int64_t out_stride;
+  int32_t G, D, tile_tok, rows;  // rows: of a piece's slot
+};
+
+// Adds up the pieces of the unit that the cut after CTA blockIdx.x is the
+// first to divide:
 //   out = sum_i f_i O_i / sum_i f_i l_i,  f_i = exp2(m_i - max m).
-template <typename T, int MAXB>
-__global__ __launch_bounds__(256) void join_kernel(const __grid_constant__ AttnParams<MAXB> p,
-                                                   int rows_per_unit) {
+// Bound by latency (a launch of a few microseconds): a thread per 4 output
+// values, with no load waiting for another but for the unit's description.
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constant__ JoinParams p) {
   ops_pdl_enter();
   const int i0 = blockIdx.x;
-  const int at = cut(p, i0 + 1);
-  const Walk<AttnParams<MAXB>> walk(p, at, at + 1);  // the unit that holds place `at`
-  if (walk.t == 0) return;                           // no unit is divided here
-  const int lo = walk.pos, from = cut(p, i0);
-  if (from > lo + p.unit_cost) return;  // an earlier cut divides it too
-  const int rows_end = unit_rows(p, walk.b, walk.tok0);
-  const int hi = lo + p.unit_cost + (rows_end + kTile - 1) / kTile;
-  int i1 = i0 + 1;  // the last CTA with a piece
-  while (cut(p, i1 + 1) < hi) ++i1;
-  const int n_tok = min(p.seq.pre[walk.b + 1] - p.seq.pre[walk.b] - walk.tok0, p.unit_tok);
-  const int lane = threadIdx.x & 31;
-  const int64_t slot = (int64_t)rows_per_unit * (p.D + 2);
-  for (int q = blockIdx.y * 8 + (threadIdx.x >> 5); q < n_tok * p.G; q += gridDim.y * 8) {
+  const Divided d = p.divided[i0];
+  const int d4 = p.D / 4, n = d.tokens * p.G * d4, pieces = d.last - i0 + 1;
+  const int64_t slot = (int64_t)p.rows * (p.D + 2);
+  const auto piece = [&](int i) { return p.part + slot * (2 * (i0 + i) + (i == 0 ? d.slot : 0)); };
+#pragma unroll 1
+  for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < n; e += gridDim.y * kJoinThreads) {
+    const int q = e / d4, c = e - q * d4;
     const int tok = q / p.G, g = q - tok * p.G;
     const int tile = tok / p.tile_tok;
     const int r = tile * kTile + (tok - tile * p.tile_tok) * p.G + g;
-    const auto piece = [&](int i) {
-      return p.part + slot * (2 * i + (i == i0 && from < lo ? 1 : 0));
-    };
-    float m = -INFINITY;
-    for (int i = i0; i <= i1; ++i)
-      m = fmaxf(m, reinterpret_cast<const float2*>(piece(i) + (int64_t)rows_per_unit * p.D)[r].x);
-    float l = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = i0; i <= i1; ++i) {
-      const float* const pc = piece(i);
-      const float2 ml = reinterpret_cast<const float2*>(pc + (int64_t)rows_per_unit * p.D)[r];
-      if (ml.x == -INFINITY) continue;
-      const float f = ex2(ml.x - m);
-      l += f * ml.y;
-      if (lane * 4 < p.D) {
-        const float4 a = reinterpret_cast<const float4*>(pc + (int64_t)r * p.D)[lane];
-        o.x += f * a.x;
-        o.y += f * a.y;
-        o.z += f * a.z;
-        o.w += f * a.w;
+#pragma unroll 1
+    for (int i = 0; i < pieces; i += 4) {
+      float2 ml[4];
+      float4 a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (i + k < pieces) {
+          const float* const pc = piece(i + k);
+          ml[k] = reinterpret_cast<const float2*>(pc + (int64_t)p.rows * p.D)[r];
+          a[k] = reinterpret_cast<const float4*>(pc + (int64_t)r * p.D)[c];
+        }
       }
+      const float m_new = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+      const float f0 = m == -INFINITY ? 0.f : ex2(m - m_new);
+      m = m_new;
+      l *= f0;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (ml[k].x != -INFINITY) {
+          const float f = ex2(ml[k].x - m);
+          l += f * ml[k].y;
+          o.x += f * a[k].x;
+          o.y += f * a[k].y;
+          o.z += f * a[k].z;
+          o.w += f * a[k].w;
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (lane * 4 < p.D) {
-      uint16_t* const out = p.out + (int64_t)(p.seq.pre[walk.b] + walk.tok0 + tok) * p.out_stride +
-                            (int64_t)(walk.h * p.G + g) * p.D;
-      reinterpret_cast<uint2*>(out)[lane] =
-          make_uint2(Pack2<T>::pack(o.x * inv, o.y * inv), Pack2<T>::pack(o.z * inv, o.w * inv));
-    }
+    uint16_t* const out =
+        p.out + (int64_t)(d.tok + tok) * p.out_stride + (int64_t)(d.head + g) * p.D;
+    reinterpret_cast<uint2*>(out)[c] =
+        make_uint2(Pack2<T>::pack(o.x * inv, o.y * inv), Pack2<T>::pack(o.z * inv, o.w * inv));
   }
 }
 
@@ -1096,7 +1134,7 @@ struct Schedule {
   int unit_cost;
   int64_t units;
   int ctas;
-  size_t bytes;  // of workspace
+  size_t part_bytes, bytes;  // of workspace: the pieces' sums, all
 };
 
 int sm_count() {
@@ -1144,7 +1182,8 @@ Schedule schedule(const Plan& p, int group, bool is_tree, int32_t* cost_pre) {
   if (ctas > sms) ctas = sms;
   if (ctas < 1) ctas = 1;
   s.ctas = (int)ctas;
-  s.bytes = ctas > 1 ? (size_t)ctas * 2 * (s.pair ? 2 : 1) * kTile * (p.D + 2) * sizeof(float) : 0;
+  s.part_bytes = (size_t)ctas * 2 * (s.pair ? 2 : 1) * kTile * (p.D + 2) * sizeof(float);
+  s.bytes = ctas > 1 ? s.part_bytes + (size_t)ctas * sizeof(Divided) : 0;
   return s;
 }
 
@@ -1211,6 +1250,7 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
   kp.v = static_cast<const uint16_t*>(v);
   kp.tree = tree;
   kp.part = part;
+  kp.divided = reinterpret_cast<Divided*>(reinterpret_cast<uint8_t*>(part) + s.part_bytes);
   kp.out_stride = q.out_stride;
   kp.share = (int32_t)(s.total / s.ctas);
   kp.extra = (int32_t)(s.total % s.ctas);
@@ -1235,9 +1275,18 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
                  : launch_kernel<T, 128, false, MAXB>(kp, s.ctas, stream);
   if (err != cudaSuccess) return cuda_fail(err, "attention launch");
   if (s.ctas > 1) {
-    void (*const join)(AttnParams<MAXB>, int) = join_kernel<T, MAXB>;
-    err = ops_launch(join, dim3((unsigned)s.ctas - 1, 8), 256, 0, stream, kp,
-                     (s.pair ? 2 : 1) * kTile);
+    JoinParams jp;
+    jp.out = kp.out;
+    jp.part = part;
+    jp.divided = kp.divided;
+    jp.out_stride = kp.out_stride;
+    jp.G = group;
+    jp.D = p.D;
+    jp.tile_tok = s.tile_tok;
+    jp.rows = (s.pair ? 2 : 1) * kTile;
+    const int unit = (s.unit_tok < p.max_len ? s.unit_tok : p.max_len) * group * (p.D / 4);
+    err = ops_launch(join_kernel<T>, dim3((unsigned)s.ctas - 1, (unit + kJoinThreads - 1) / kJoinThreads),
+                     kJoinThreads, 0, stream, jp);
     if (err != cudaSuccess) return cuda_fail(err, "attention join launch");
   }
   return DV_OK;
