@@ -30,6 +30,12 @@
  *   dv_delta_*       §3 "Token computation and streaming parallelization"
  *                    (Fig 7c): each step's delta streamed on a side stream
  *                    while the next step computes.
+ *   dv_kv_append, dv_prompt_attention, dv_tree_attention, dv_kv_compact
+ *                    (no counterpart on the pages) what a decoder layer does to
+ *                    the cache between two transfers: new tokens' rows
+ *                    written with rotary positions, attention over them for
+ *                    prompts, for trees of drafted tokens and for decode
+ *                    steps, and rows moved together in place.
  *   dv_host_alloc    pinned, mapped host memory on huge pages for replica
  *                    arenas and swap buffers (the host side of every
  *                    transfer above).
@@ -109,7 +115,7 @@ typedef enum {
   DV_ERR_BUFFER_TOO_SMALL = 3, /* destination / source / staging too small */
   DV_ERR_MISALIGNED = 4,       /* a pointer or stride not 16-byte aligned */
   DV_ERR_CUDA = 5,             /* a CUDA runtime call or launch failed */
-  DV_ERR_TIMEOUT = 6,          /* reserved for bounded waits */
+  DV_ERR_TIMEOUT = 6,          /* a wait inside an attention kernel gave up */
   DV_ERR_UNSUPPORTED = 7       /* a geometry the library does not handle */
 } dv_status;
 

@@ -19,27 +19,45 @@
 //   SPLIT  one row tile, the even K/V tiles on one chain and the odd ones on
 //          the other, joined at the end: decode steps and small trees, bound
 //          by reading K and V once.
+// PAIR where some sequence has more rows than a row tile, SPLIT otherwise.  P is
+// handed over in two halves, so that the products with V start under the second
+// half's exponentials.
 //
 // Warps: 0-3 and 4-7 the chains' softmax, 8 loads (and walks over the units,
-// publishing each in a ring), 9 and 10 issue the chains' products, 11 looks after V's hidden rows.  K
-// goes to shared memory by TMA in its own layout: the cache's [D/8][S][8] is,
-// per tile, exactly the tensor core's unswizzled layout of 8 x 16-byte core
-// matrices, so nothing is transposed.  V goes in with the 128-byte swizzle and
-// is read with its rows as the contraction.  A sequence's last, partial tile is
-// fetched up to the last attended row (K in bulk copies, V in 32s).
+// publishing each in a ring), 9 and 10 issue the chains' products, 11 looks
+// after V's hidden rows.  K goes to shared memory by TMA in its own layout: the
+// cache's [D/8][S][8] is, per tile, exactly the tensor core's unswizzled layout
+// of 8 x 16-byte core matrices, so nothing is transposed.  V goes in with the
+// 128-byte swizzle and is read with its rows as the contraction.  A sequence's
+// last, partial tile is fetched up to the last attended row (K in bulk copies,
+// V in 32s).
 //
-// The units form one line, each as long as its cost, cut into equal stretches, one for
-// each CTA (one CTA an SM); a unit that a cut divides leaves partial sums in
-// the workspace, which join_kernel adds up.
+// The units form one line, each as long as its cost, cut into equal stretches,
+// one for each CTA (one CTA an SM); a unit that a cut divides leaves partial
+// sums in the workspace, which join_kernel adds up.
 //
 // Rows a mask hides must have no effect, but 0 x NaN is NaN in a product: in
 // tiles that hold hidden rows, warp 11 sets V's non-finite values to zero in
-// shared memory (rows past the last attended one altogether), while the tile's scores
-// are computed, and should there have been any, the epilogue adds them to the
-// outputs of the rows that do attend them.
+// shared memory (rows past the last attended one altogether), while the tile's
+// scores are computed, and should there have been any, the epilogue adds them
+// to the outputs of the rows that do attend them.
 //
 // Every wait gives up after kSpinLimit tries: the CTA then drains its copies,
 // frees its tensor memory and returns, and dv_attention_check reports it.
+//
+// Measured (bf16, heads of 128 unless said).  SPLIT is bound by HBM: a decode
+// step of 32 sequences of 64 to 1791 rows, 112 heads (1.52 GB) 232 us, 6.5 TB/s.
+// PAIR is bound by the chain scores - softmax - products of a tile, about 3100
+// cycles for a pair of tiles whose products take 2048 on the tensor cores: 4096
+// tokens after 28672, 64 query heads on 8, 2.6 ms, 1.55 to 1.6 PFLOP/s; on
+// short prompts the filling and draining of the chains come on top, and the
+// half of the diagonal tiles that is hidden: 32 prompts of 64 to 1536 tokens,
+// 112 heads, 0.80 ms, 0.91 PFLOP/s attended.
+// Heads of 64 halve the products but not the softmax: 8 prompts of 1000, 25
+// heads (fp16), 53 us.  What was tried and was slower: S in halves of 64
+// columns two steps ahead; two buffers of 96 columns for heads of 64; the
+// maximum from a second pass over S, or only when a sum grows too large (7 to
+// 10% each); one product warp for both chains (28% on ragged prompts).
 #include <cuda.h>
 
 #include "dv_ops.h"
@@ -1147,7 +1165,11 @@ int sm_count() {
   return n;
 }
 
-constexpr int kMinTiles = 4;  // a CTA's share is not cut below this many tiles
+// A CTA's share is not cut below this many tiles, one for each chain, where
+// there are fewer units than SMs: a finer cut gains nothing that the join does
+// not take (one sequence's decode step over 1000 rows, 8 key heads: 8.7 us at 2
+// and at 1, 10.5 at 4, 12.3 at 8; over 2000: 9.3, 9.8, 10.3, 13.5).
+constexpr int kMinTiles = 2;
 // What a unit costs besides its tiles (fetching its queries, filling and
 // draining the two chains, its output), in tiles: without it CTAs with many
 // short sequences took twice as long as the others (decode of a ragged batch:
