@@ -227,6 +227,30 @@ dv_status resolve(const void* ptr, size_t need, bool allow_host, const char* wha
 
 dv_status resolve_words(const void* ptr, size_t need, unsigned align, const char* what,
                         void** dev) {
+  // The plain case in one driver call (a third of the time, and an operator has up to eight
+  // buffers); anything else takes the long way, which also words the errors.
+  using GetFn = CUresult (*)(unsigned, CUpointer_attribute*, void**, CUdeviceptr);
+  static const GetFn get = reinterpret_cast<GetFn>(driver_fn("cuPointerGetAttributes"));
+  int cur = -1;
+  if (get && ptr && (reinterpret_cast<uintptr_t>(ptr) & (align - 1)) == 0 &&
+      cudaGetDevice(&cur) == cudaSuccess) {
+    unsigned type = 0, managed = 0;
+    int device = -1;
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    CUpointer_attribute attr[5] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED,
+                                   CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                   CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
+                                   CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+    void* out[5] = {&type, &managed, &device, &base, &size};
+    const uintptr_t p0 = reinterpret_cast<uintptr_t>(ptr);
+    if (get(5, attr, out, static_cast<CUdeviceptr>(p0)) == CUDA_SUCCESS &&
+        type == CU_MEMORYTYPE_DEVICE && !managed && device == cur && size > 0 &&
+        p0 + need <= static_cast<uintptr_t>(base) + size) {
+      *dev = const_cast<void*>(ptr);
+      return DV_OK;
+    }
+  }
   return resolve_aligned(ptr, need, align, false, what, dev, nullptr);
 }
 

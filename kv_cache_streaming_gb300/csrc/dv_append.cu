@@ -368,7 +368,7 @@ extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const in
     return fail(DV_ERR_INVALID_ARG, "the buffers hold %lld tokens, the ranges %lld",
                 (long long)t.tokens, (long long)p.tokens);
   if (p.tokens == 0) return DV_OK;
-  if ((st = dv::resolve_cache(cache, &p)) != DV_OK) return st;
+  if ((st = dv::resolve_layers(&p)) != DV_OK) return st;
   void* dev = nullptr;
   size_t nk = 0, nv = 0, nq = 0, no = 0;
   if ((st = dv::resolve_rows(p, t.k, p.H, t.k_stride, "k", &dev, &nk)) != DV_OK) return st;

@@ -1352,7 +1352,7 @@ dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, cons
   if (workspace_bytes < need)
     return fail(DV_ERR_BUFFER_TOO_SMALL, "attention needs %zu workspace bytes (got %zu)", need,
                 workspace_bytes);
-  if ((st = resolve_cache(cache, &p)) != DV_OK) return st;
+  if ((st = resolve_layers(&p)) != DV_OK) return st;
   void* dev = nullptr;
   size_t nq = 0, no = 0;
   if ((st = resolve_rows(p, q.q, q.q_heads, q.q_stride, "q", &dev, &nq)) != DV_OK) return st;
@@ -1366,10 +1366,8 @@ dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, cons
   }
   float* part = nullptr;
   if (need > 0) {
-    if ((st = resolve(workspace, need, false, "workspace", &dev)) != DV_OK) return st;
+    if ((st = resolve_words(workspace, need, 32, "workspace", &dev)) != DV_OK) return st;
     part = static_cast<float*>(dev);
-    if (reinterpret_cast<uintptr_t>(part) % 32 != 0)
-      return fail(DV_ERR_MISALIGNED, "workspace %p is not 32-byte aligned", workspace);
     if (overlap(part, need, q.q, nq) || overlap(part, need, q.out, no))
       return fail(DV_ERR_INVALID_ARG, "workspace overlaps q or out");
   }

@@ -110,8 +110,7 @@ dv_status plan_ranges(const dv_cache* c, int32_t l0, int32_t l1, const int32_t* 
 dv_status resolve(const void* ptr, size_t need, bool allow_host, const char* what, void** dev,
                   bool* is_host = nullptr);
 
-// The same for a device array of words of `align` bytes (4 or 8), which need
-// only that alignment.
+// The same for device memory that needs an alignment of `align` bytes.
 dv_status resolve_words(const void* ptr, size_t need, unsigned align, const char* what,
                         void** dev);
 

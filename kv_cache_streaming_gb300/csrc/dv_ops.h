@@ -122,7 +122,21 @@ inline dv_status resolve_rows(const Plan& p, const void* ptr, int32_t heads, int
     return fail(DV_ERR_MISALIGNED, "%s: a stride of %lld elements is not a multiple of 8", what,
                 (long long)stride);
   *span = (size_t)(((p.tokens - 1) * stride + row) * 2);
-  return resolve(ptr, *span, false, what, dev);
+  return resolve_words(ptr, *span, 16, what, dev);
+}
+
+// As resolve_cache: the cache's K and V bases, up to the last layer of the plan.
+inline dv_status resolve_layers(Plan* p) {
+  const int64_t dense = (int64_t)p->B * p->H * p->D * p->S;
+  const size_t need = (size_t)((p->l1 - 1) * p->layer_chunks * 16 + dense * p->P);
+  void* k = nullptr;
+  void* v = nullptr;
+  dv_status st = resolve_words(p->k, need, 16, "cache.k_base", &k);
+  if (st == DV_OK) st = resolve_words(p->v, need, 16, "cache.v_base", &v);
+  if (st != DV_OK) return st;
+  p->k = k;
+  p->v = v;
+  return DV_OK;
 }
 
 inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {

@@ -198,6 +198,9 @@ def _stream(s):
     return s.cuda_stream
 
 
+_addressof, _from_buffer = ctypes.addressof, ctypes.c_int32.from_buffer
+
+
 def _addr(a):
     """Address of a contiguous int32 numpy array's data (the cheapest route
     through ctypes; read-only arrays are copied first)."""
@@ -208,9 +211,21 @@ def _addr(a):
         return ctypes.addressof(ctypes.c_int32.from_buffer(a)), a
 
 
+_INT32 = np.dtype(np.int32)
+
+
 def _ranges(seq_start, seq_end, batch):
     """int32 copies (or views) of the ranges and their addresses; the library
     reads exactly `batch` entries of each, so shorter arrays are refused."""
+    if (type(seq_start) is np.ndarray and type(seq_end) is np.ndarray
+            and seq_start.dtype == _INT32 and seq_end.dtype == _INT32
+            and seq_start.shape == seq_end.shape == (batch,)
+            and seq_start.strides == seq_end.strides == (4,)):
+        try:  # as they are
+            return (seq_start, seq_end, _addressof(_from_buffer(seq_start)),
+                    _addressof(_from_buffer(seq_end)))
+        except (TypeError, ValueError):
+            pass
     s = np.ascontiguousarray(seq_start, dtype=np.int32).reshape(-1)
     e = np.ascontiguousarray(seq_end, dtype=np.int32).reshape(-1)
     if s.size != batch or e.size != batch:
