@@ -98,6 +98,34 @@ def test_append(dtype, B, H, G, D, S, ctx, new, rot, inter, scaling, far):
     assert torch.equal(K[0], K0[0]) and torch.equal(V[0], V0[0])
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_append(seed):
+    rng = np.random.default_rng(seed)
+    gen = _gen(seed)
+    dtype = ["fp16", "bf16"][rng.integers(2)]
+    B, H, G, D = int(rng.integers(1, 9)), int(rng.integers(1, 9)), int(rng.integers(1, 6)), 8 * int(rng.integers(1, 25))
+    rot = 2 * int(rng.integers(1, min(D, 256) // 2 + 1))
+    inter, scaling = bool(rng.integers(2)), str(rng.choice(["none", "linear", "parts"]))
+    s = rng.integers(0, 50, size=B).astype(np.int32)
+    e = s + rng.integers(0, int(rng.choice([2, 5, 60])), size=B).astype(np.int32)
+    S, T = int(e.max()) + int(rng.integers(0, 9)) + 1, int((e - s).sum())
+    cache, K, V = R.make_cache(dtype, 1, B, H, D, S, gen)
+    q = torch.empty(T, H * G, D, dtype=R.DT[dtype], device="cuda").normal_(generator=gen)
+    k, v = (torch.empty(T, H, D, dtype=R.DT[dtype], device="cuda").normal_(generator=gen) for _ in range(2))
+    pos = torch.randint(0, 1 << 19, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    q_out = dv.dv_kv_append(cache, 0, s, e, k, v, q=q, positions=pos,
+                            rope=dv.Rope(rot, interleaved=inter, scaling=scaling, factor=8.0, original_max=4096))
+    f, m = R.rope_freqs(rot, 10000.0, scaling, 8.0, 4096)
+    want, tol = R.rotate_ref(q, pos, rot, inter, f, m)
+    R.assert_within(q_out[..., :rot], want[..., :rot], tol[..., :rot])
+    assert torch.equal(q_out[..., rot:], q[..., rot:])
+    want, tol = R.rotate_ref(k, pos, rot, inter, f, m)
+    for b, t, a, z in R.spans(s, e):
+        got = K[0, b, :, :, a:z].permute(2, 0, 1, 3).reshape(z - a, H, D)
+        R.assert_within(got, want[t:t + z - a], tol[t:t + z - a] + (torch.arange(D, device="cuda") >= rot) * 0.0)
+        assert torch.equal(V[0, b, :, a:z].transpose(0, 1), v[t:t + z - a])
+
+
 def test_append_without_rotation_or_queries_copies():
     gen = _gen(3)
     s, e = np.array([5, 0], np.int32), np.array([25, 11], np.int32)
@@ -259,6 +287,56 @@ def test_growing_and_falling_scores(dtype):
     want, tol = R.attention_ref(K[0], V[0], s, e, q, 0.125)
     R.assert_within(_attend(cache, 0, s, e, q, 0.125), want, tol)
     R.assert_within(_attend(cache, 0, s, e, q, 0.125, prompt=True), want, tol)
+
+
+@pytest.mark.parametrize("seed", range(32))
+def test_random_attention(seed):
+    """Seeded draws over types, head sizes and groups, lengths, masks, layers
+    with a gap between them, and strided queries."""
+    rng = np.random.default_rng(1000 + seed)
+    gen = _gen(seed)
+    dtype = ["fp16", "bf16"][rng.integers(2)]
+    B, H, G = int(rng.integers(1, 7)), int(rng.integers(1, 7)), int(rng.choice([1, 2, 3, 4, 7, 8, 16]))
+    D = 8 * int(rng.integers(1, 17))
+    prompt = bool(rng.integers(2))
+    most = int(rng.integers(1, 500)) if prompt else int(rng.integers(1, 65))
+    ctx = int(rng.choice([0, int(rng.integers(1, 700))]))
+    s = rng.integers(0, ctx + 1, size=B).astype(np.int32)
+    e = s + rng.integers(0 if B > 1 else 1, most + 1, size=B).astype(np.int32)
+    if e.sum() == s.sum():
+        e[0] += 1
+    S, T = int(e.max()) + int(rng.integers(0, 40)), int((e - s).sum())
+    cache, K, V = R.make_cache(dtype, 3, B, H, D, S, gen, stride=B * H * D * S + 8 * int(rng.integers(0, 5)))
+    wide = torch.empty(T, (H * G + 3) * D, dtype=R.DT[dtype], device="cuda").normal_(generator=gen)
+    q = wide[:, D:(H * G + 1) * D].view(T, H * G, D)
+    masked = not prompt and bool(rng.integers(2))
+    bits = sum((R.random_tree(int(z - a), rng)[0] for a, z in zip(s, e)), []) if masked else None
+    layer, scale = int(rng.integers(3)), float(rng.uniform(0.3, 2.0)) * D ** -0.5
+    want, tol = R.attention_ref(K[layer], V[layer], s, e, q, scale, bits)
+    for b, _, a, z in R.spans(s, e):
+        K[:, b, :, :, z:], V[:, b, :, z:] = math.nan, math.nan
+    out = torch.empty(T, H * G, D, dtype=R.DT[dtype], device="cuda")
+    _attend(cache, layer, s, e, q, scale, tree=R.bits_tensor(bits) if masked else None, prompt=prompt, out=out)
+    R.assert_within(out, want, tol)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with workspaces of their own, in flight together."""
+    gen = _gen(77)
+    jobs = []
+    for i, (H, D, ctx, n) in enumerate([(8, 128, 3000, 5), (20, 64, 900, 33)]):
+        s, e = np.array([ctx, 7], np.int32), np.array([ctx + n, 8 + n], np.int32)
+        cache, K, V = R.make_cache("bf16", 1, 2, H, D, ctx + n, gen)
+        q = torch.empty(2 * n + 1, H, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+        want, tol = R.attention_ref(K[0], V[0], s, e, q, D ** -0.5)
+        jobs.append((cache, s, e, q, D ** -0.5, want, tol, torch.empty_like(q), _ws(cache, s, e, H), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for r in range(20):
+        for cache, s, e, q, scale, _, _, out, ws, stream in jobs:
+            dv.dv_tree_attention(cache, 0, s, e, q, out, scale, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, _, _, want, tol, out, _, _ in jobs:
+        R.assert_within(out, want, tol)
 
 
 def test_strided_queries_and_output_leave_the_rest():
