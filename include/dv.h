@@ -646,7 +646,7 @@ typedef struct {
   int64_t v_stride;
   const void* q; /* [T][q_heads][head_dim] */
   int64_t q_stride;
-  void* q_out; /* rotated queries; overlaps none of q, k, v */
+  void* q_out; /* rotated queries; overlaps none of q, k, v, nor the cache's layer */
   int64_t q_out_stride;
   const int32_t* positions; /* [T] position of each token; NULL: its cache row */
   const dv_rope* rope;      /* NULL: nothing is rotated (q is copied) */
@@ -659,7 +659,7 @@ typedef struct {
  * ranges), DV_ERR_INVALID_ARG (null or overlapping buffers, strides too
  * small, unknown dtype, rot_dim above head_dim), DV_ERR_MISALIGNED,
  * DV_ERR_BUFFER_TOO_SMALL (a buffer's allocation ends before its last token),
- * DV_ERR_UNSUPPORTED (elem_bytes). */
+ * DV_ERR_UNSUPPORTED (elem_bytes; more than 2^23 elements of a token's keys). */
 dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
                        const int32_t* seq_end, const dv_new_tokens* tokens, dv_stream stream);
 
@@ -671,7 +671,7 @@ typedef struct {
   int64_t tokens;  /* T: what q and out hold, and the ranges' sum (else DV_ERR_INVALID_ARG) */
   const void* q;   /* [T][q_heads][head_dim] */
   int64_t q_stride; /* elements from one token to the next, a multiple of 8 */
-  void* out;        /* the same shape; does not overlap q */
+  void* out;        /* the same shape; overlaps none of q, the cache's layer, the tree */
   int64_t out_stride;
   float scale; /* on q.k; finite and positive */
 } dv_queries;
@@ -691,7 +691,8 @@ dv_status dv_attention_workspace(const dv_cache* cache, const int32_t* seq_start
  * infinities included).  head_dim a multiple of 8 up to 128, elem_bytes 2
  * (else DV_ERR_UNSUPPORTED).  `workspace`: device memory, 32-byte aligned,
  * of dv_attention_workspace bytes (NULL when that is 0), for this call alone
- * until the stream has passed it; it needs no initial value. */
+ * until the stream has passed it; it needs no initial value and overlaps no
+ * other buffer of the call. */
 dv_status dv_prompt_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
                               const int32_t* seq_end, const dv_queries* queries, void* workspace,
                               size_t workspace_bytes, dv_stream stream);

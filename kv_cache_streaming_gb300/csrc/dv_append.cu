@@ -287,8 +287,8 @@ cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t st
     if (e > s) groups += (e + kTileRows - 1) / kTileRows - s / kTileRows;
   }
   kp.group_pre[p.B] = (int32_t)groups;
-  // Warps over the heads: 4 heads to a warp, what it has in flight at once (as 8 rows x 4
-  // chunks: 87 us of ragged prompts; 99 at 2 heads, 92 at 6, 101 where a warp walked over 30).
+  // Warps over the heads: 4 heads to a warp, about what it has in flight at once (ragged
+  // prompts, 40 heads of 128: 72 us; 89 at 2 heads, 76 at 6, 74 at 8).
   const int parts = (p.C + kTileChunks - 1) / kTileChunks;
   const int most_heads = t.q_heads > p.H ? t.q_heads : p.H;
   const int64_t warps = (int64_t)parts * ((most_heads + 3) / 4);
@@ -355,7 +355,7 @@ extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const in
   dv_new_tokens t = *tokens;
   if (t.q_heads < 0 || (int64_t)t.q_heads * p.D > INT32_MAX / 2)
     return fail(DV_ERR_INVALID_ARG, "q_heads is %d", t.q_heads);
-  if ((int64_t)p.H * p.D > INT32_MAX / 8)
+  if ((int64_t)p.H * p.D > 1 << 23)  // the tile kernel's grid has a warp for each 64 of a head's
     return fail(DV_ERR_UNSUPPORTED, "%d heads of %d elements", p.H, p.D);
   if (t.rope) {
     if (t.rope->rot_dim < 2 || t.rope->rot_dim > DV_MAX_ROT || t.rope->rot_dim % 2 != 0 ||
@@ -384,6 +384,8 @@ extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const in
     if (dv::overlap(t.q_out, no, t.q, nq) || dv::overlap(t.q_out, no, t.k, nk) ||
         dv::overlap(t.q_out, no, t.v, nv))
       return fail(DV_ERR_INVALID_ARG, "q_out overlaps q, k or v");
+    if (dv::overlaps_layer(p, t.q_out, no))
+      return fail(DV_ERR_INVALID_ARG, "q_out overlaps the cache's layer");
   }
   if (t.positions && (st = dv::resolve_words(t.positions, (size_t)p.tokens * 4, 4, "positions",
                                              &dev)) != DV_OK)

@@ -57,7 +57,8 @@
 // heads (fp16), 53 us.  What was tried and was slower: S in halves of 64
 // columns two steps ahead; two buffers of 96 columns for heads of 64; the
 // maximum from a second pass over S, or only when a sum grows too large (7 to
-// 10% each); one product warp for both chains (28% on ragged prompts).
+// 10% each); one product warp for both chains (28% on ragged prompts); the next
+// tile's second half of scores issued as soon as S has been read (4 to 6%).
 #include <cuda.h>
 
 #include "dv_ops.h"
@@ -1173,7 +1174,8 @@ constexpr int kMinTiles = 2;
 // What a unit costs besides its tiles (fetching its queries, filling and
 // draining the two chains, its output), in tiles: without it CTAs with many
 // short sequences took twice as long as the others (decode of a ragged batch:
-// 353 us at 0, 256 at 1, 236 at 2, 249 at 5).
+// 346 us at 0, 252 at 1, 232 at 2, 246 at 5; ragged prompts: 902 at 0, 823 at 1,
+// 814 at 2, 828 at 3, where prompts of 1000 take 57, 53, 55, 55).
 constexpr int kUnitCostPair = 1, kUnitCostSplit = 2;
 
 Schedule schedule(const Plan& p, int group, bool is_tree, int32_t* cost_pre) {
@@ -1360,9 +1362,13 @@ dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, cons
   if ((st = resolve_rows(p, q.out, q.q_heads, q.out_stride, "out", &dev, &no)) != DV_OK) return st;
   q.out = dev;
   if (overlap(q.out, no, q.q, nq)) return fail(DV_ERR_INVALID_ARG, "out overlaps q");
+  if (overlaps_layer(p, q.out, no))
+    return fail(DV_ERR_INVALID_ARG, "out overlaps the cache's layer");
   if (tree) {
     if ((st = resolve_words(tree, (size_t)p.tokens * 8, 8, "tree", &dev)) != DV_OK) return st;
     tree = static_cast<const uint64_t*>(dev);
+    if (overlap(q.out, no, tree, (size_t)p.tokens * 8))
+      return fail(DV_ERR_INVALID_ARG, "out overlaps tree");
   }
   float* part = nullptr;
   if (need > 0) {
@@ -1370,6 +1376,9 @@ dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, cons
     part = static_cast<float*>(dev);
     if (overlap(part, need, q.q, nq) || overlap(part, need, q.out, no))
       return fail(DV_ERR_INVALID_ARG, "workspace overlaps q or out");
+    if (overlaps_layer(p, part, need) ||
+        (tree && overlap(part, need, tree, (size_t)p.tokens * 8)))
+      return fail(DV_ERR_INVALID_ARG, "workspace overlaps the cache's layer or tree");
   }
   const bool small = p.B <= kSmallBatch;
   if (q.dtype == DV_DTYPE_FP16)

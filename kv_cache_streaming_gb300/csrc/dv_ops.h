@@ -144,4 +144,12 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// Whether a buffer shares bytes with K or V of the plan's (one) layer, bases resolved.
+inline bool overlaps_layer(const Plan& p, const void* a, size_t n) {
+  const size_t at = (size_t)(p.l0 * p.layer_chunks) * 16;
+  const size_t bytes = (size_t)p.B * p.H * p.D * p.S * p.P;
+  return overlap(a, n, static_cast<const char*>(p.k) + at, bytes) ||
+         overlap(a, n, static_cast<const char*>(p.v) + at, bytes);
+}
+
 }  // namespace dv

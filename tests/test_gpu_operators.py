@@ -472,6 +472,34 @@ def test_gpu_refusals():
     torch.cuda.synchronize()
 
 
+def test_outputs_and_workspace_on_the_cache_are_refused():
+    """What a call writes besides its rows shares no bytes with the layer it
+    reads (another layer's are the caller's business), nor with the tree."""
+    cache, K, V = R.make_cache("fp16", 2, 1, 2, 64, 4096, _gen(2))
+    before = K.clone(), V.clone()
+    s, e = np.array([0], np.int32), np.array([8], np.int32)
+    q = torch.zeros(8, 2, 64, dtype=torch.float16, device="cuda")
+    o, ws = torch.zeros_like(q), _ws(cache, s, e, 2)
+    tree = torch.full((8,), 255, dtype=torch.int64, device="cuda")
+
+    def refused(fn):
+        with pytest.raises(dv.DvError) as ei:
+            fn()
+        assert ei.value.status == dv.DV_ERR_INVALID_ARG and "overlaps" in str(ei.value)
+
+    for t in (K, V):
+        on = t[1].reshape(-1)[:8 * 128].view(8, 2, 64)
+        refused(lambda: dv.dv_kv_append(cache, 1, s, e, q, q, q=q, q_out=on))
+        refused(lambda: dv.dv_prompt_attention(cache, 1, s, e, q, on, 0.125, ws))
+        refused(lambda: dv.dv_tree_attention(cache, 1, s, e, q, on, 0.125, ws, tree=tree))
+        refused(lambda: dv.dv_prompt_attention(cache, 1, s, e, q, o, 0.125, t[1].reshape(-1)))
+    bits = o.view(-1).view(torch.int64)[:8]
+    refused(lambda: dv.dv_tree_attention(cache, 0, s, e, q, o, 0.125, ws, tree=bits))
+    refused(lambda: dv.dv_tree_attention(cache, 0, s, e, q, o, 0.125, ws, tree=ws.view(torch.int64)[:8]))
+    torch.cuda.synchronize()
+    assert torch.equal(K, before[0]) and torch.equal(V, before[1])
+
+
 # ---- compact ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("P", [1, 2, 4])

@@ -106,6 +106,13 @@ def test_append_refusals():
     call(s=[1, 2], e=[1, 2])
 
 
+def test_append_refuses_tokens_of_more_than_8m_elements():
+    D = (1 << 23) + 8
+    k = torch.empty(1, 1, D, dtype=F16)
+    _refused(dv.DV_ERR_UNSUPPORTED,
+             lambda: dv.dv_kv_append(_cache(L=1, B=1, H=1, D=D, S=4), 0, [0], [1], k, k, stream=0))
+
+
 def test_compact_refusals():
     keep = torch.zeros(5, dtype=torch.int32)
     _refused(dv.DV_ERR_RANGE, lambda: dv.dv_kv_compact(_cache(), 0, 3, S2, E2, keep, stream=0))
