@@ -52,7 +52,7 @@
 // tokens after 28672, 64 query heads on 8, 2.6 ms, 1.55 to 1.6 PFLOP/s; on
 // short prompts the filling and draining of the chains come on top, and the
 // half of the diagonal tiles that is hidden: 32 prompts of 64 to 1536 tokens,
-// 112 heads, 0.80 ms, 0.91 PFLOP/s attended.
+// 112 heads, 0.80 to 0.82 ms, 0.88 to 0.91 PFLOP/s attended.
 // Heads of 64 halve the products but not the softmax: 8 prompts of 1000, 25
 // heads (fp16), 53 us.  What was tried and was slower: S in halves of 64
 // columns two steps ahead; two buffers of 96 columns for heads of 64; the
