@@ -761,6 +761,18 @@ def _dtype(t):
     return d
 
 
+def _empty_on(t, raw):
+    """An uninitialised tensor like ``t`` whose memory belongs to the stream
+    ``raw``: torch reuses a tensor's memory in the order of the stream that it
+    was allocated under, which has to be the one that writes it."""
+    if not t.is_cuda or raw == _current_stream():
+        return t.new_empty(t.shape)
+    import torch
+    s = torch.cuda.ExternalStream(raw, device=t.device) if raw else torch.cuda.default_stream(t.device)
+    with torch.cuda.stream(s):
+        return t.new_empty(t.shape)
+
+
 def _token_rows(t, name, shape, dtype):
     """(address, stride) of a tensor of ``shape`` (tokens, heads, head_dim) whose
     tokens may be strided."""
@@ -814,11 +826,12 @@ class Rope:
 
 def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=None, rope=None,
                  positions=None, stream=None):
-    """Rotates ``q`` (into ``q_out``, allocated when None) and ``k`` by
-    ``positions`` (int32, or None: their cache rows) and writes ``k`` and ``v``
-    to rows [seq_start, seq_end) of ``layer``.  k, v: [T, num_heads, head_dim];
-    q: [T, q_heads, head_dim]; T new tokens, packed.  Returns ``q_out``."""
-    c = cache.c
+    """Rotates ``q`` (into ``q_out``; None: a tensor allocated under ``stream``)
+    and ``k`` by ``positions`` (int32, or None: their cache rows) and writes
+    ``k`` and ``v`` to rows [seq_start, seq_end) of ``layer``.  k, v:
+    [T, num_heads, head_dim]; q: [T, q_heads, head_dim]; T new tokens, packed.
+    Returns ``q_out``."""
+    c, raw = cache.c, _stream(stream)
     s, e, sp, ep = _ranges(seq_start, seq_end, c.batch)
     n, D, dtype = k.shape[0], c.head_dim, k.dtype
     shape = (n, c.num_heads, D)
@@ -829,7 +842,7 @@ def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=No
         if q.dim() != 3:
             raise ValueError(f"q must be [{n}, q_heads, {D}] (got {list(q.shape)})")
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = _empty_on(q, raw)
         heads = q.shape[1]
         shape = (n, heads, D)
         qp, qs = _token_rows(q, "q", shape, dtype)
@@ -837,7 +850,7 @@ def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=No
     pos = None if positions is None else _words_of(positions, "positions", n, 4)
     rp = None if rope is None else ctypes.addressof(rope.c if isinstance(rope, Rope) else rope)
     t = dv_new_tokens(_dtype(k), heads, n, kp, ks, vp, vs, qp, qs, op, os_, pos, rp)
-    _check(_append(cache.ref, layer, sp, ep, ctypes.byref(t), _stream(stream)))
+    _check(_append(cache.ref, layer, sp, ep, ctypes.byref(t), raw))
     return q_out
 
 
