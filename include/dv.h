@@ -646,11 +646,13 @@ typedef struct {
   int64_t v_stride;
   const void* q; /* [T][q_heads][head_dim] */
   int64_t q_stride;
-  void* q_out; /* rotated queries; overlaps none of q, k, v, nor the cache's layer */
+  void* q_out; /* rotated queries */
   int64_t q_out_stride;
   const int32_t* positions; /* [T] position of each token; NULL: its cache row */
   const dv_rope* rope;      /* NULL: nothing is rotated (q is copied) */
 } dv_new_tokens;
+/* What is written (q_out and the cache's layer) shares no bytes with what is
+ * read (k, v, q, positions), nor q_out with the layer. */
 
 /* Rotates q and k by their positions and writes k and v to rows
  * [seq_start, seq_end) of layer `layer`, in the cache's layout.  Values are

@@ -368,29 +368,39 @@ extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const in
     return fail(DV_ERR_INVALID_ARG, "the buffers hold %lld tokens, the ranges %lld",
                 (long long)t.tokens, (long long)p.tokens);
   if (p.tokens == 0) return DV_OK;
+  // What the call writes (q_out and the layer) shares no bytes with what it reads.
+  size_t nk = 0, nv = 0, nq = 0, no = 0;
+  const size_t np = (size_t)p.tokens * 4;
+  if ((st = dv::span_rows(p, p.H, t.k_stride, "k", &nk)) != DV_OK) return st;
+  if ((st = dv::span_rows(p, p.H, t.v_stride, "v", &nv)) != DV_OK) return st;
+  if (t.q_heads > 0) {
+    if ((st = dv::span_rows(p, t.q_heads, t.q_stride, "q", &nq)) != DV_OK) return st;
+    if ((st = dv::span_rows(p, t.q_heads, t.q_out_stride, "q_out", &no)) != DV_OK) return st;
+    if (dv::overlap(t.q_out, no, t.q, nq) || dv::overlap(t.q_out, no, t.k, nk) ||
+        dv::overlap(t.q_out, no, t.v, nv) || dv::overlap(t.q_out, no, t.positions, np))
+      return fail(DV_ERR_INVALID_ARG, "q_out overlaps q, k, v or positions");
+    if (dv::overlaps_layers(p, t.q_out, no) || dv::overlaps_layers(p, t.q, nq))
+      return fail(DV_ERR_INVALID_ARG, "q or q_out overlaps the cache's layer");
+  }
+  if (dv::overlaps_layers(p, t.k, nk) || dv::overlaps_layers(p, t.v, nv) ||
+      dv::overlaps_layers(p, t.positions, np))
+    return fail(DV_ERR_INVALID_ARG, "k, v or positions overlaps the cache's layer");
   if ((st = dv::resolve_layers(&p)) != DV_OK) return st;
   void* dev = nullptr;
-  size_t nk = 0, nv = 0, nq = 0, no = 0;
-  if ((st = dv::resolve_rows(p, t.k, p.H, t.k_stride, "k", &dev, &nk)) != DV_OK) return st;
+  if ((st = dv::resolve_words(t.k, nk, 16, "k", &dev)) != DV_OK) return st;
   t.k = dev;
-  if ((st = dv::resolve_rows(p, t.v, p.H, t.v_stride, "v", &dev, &nv)) != DV_OK) return st;
+  if ((st = dv::resolve_words(t.v, nv, 16, "v", &dev)) != DV_OK) return st;
   t.v = dev;
   if (t.q_heads > 0) {
-    if ((st = dv::resolve_rows(p, t.q, t.q_heads, t.q_stride, "q", &dev, &nq)) != DV_OK) return st;
+    if ((st = dv::resolve_words(t.q, nq, 16, "q", &dev)) != DV_OK) return st;
     t.q = dev;
-    if ((st = dv::resolve_rows(p, t.q_out, t.q_heads, t.q_out_stride, "q_out", &dev, &no)) != DV_OK)
-      return st;
+    if ((st = dv::resolve_words(t.q_out, no, 16, "q_out", &dev)) != DV_OK) return st;
     t.q_out = dev;
-    if (dv::overlap(t.q_out, no, t.q, nq) || dv::overlap(t.q_out, no, t.k, nk) ||
-        dv::overlap(t.q_out, no, t.v, nv))
-      return fail(DV_ERR_INVALID_ARG, "q_out overlaps q, k or v");
-    if (dv::overlaps_layer(p, t.q_out, no))
-      return fail(DV_ERR_INVALID_ARG, "q_out overlaps the cache's layer");
   }
-  if (t.positions && (st = dv::resolve_words(t.positions, (size_t)p.tokens * 4, 4, "positions",
-                                             &dev)) != DV_OK)
-    return st;
-  if (t.positions) t.positions = static_cast<const int32_t*>(dev);
+  if (t.positions) {
+    if ((st = dv::resolve_words(t.positions, np, 4, "positions", &dev)) != DV_OK) return st;
+    t.positions = static_cast<const int32_t*>(dev);
+  }
   const auto launch = [&](auto elem) {
     using T = decltype(elem);
     const auto batch = [&](auto pairs) {

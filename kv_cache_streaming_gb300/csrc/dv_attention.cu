@@ -1354,31 +1354,31 @@ dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, cons
   if (workspace_bytes < need)
     return fail(DV_ERR_BUFFER_TOO_SMALL, "attention needs %zu workspace bytes (got %zu)", need,
                 workspace_bytes);
+  // What the call writes (out and the workspace) shares no bytes with what it reads.
+  size_t nq = 0, no = 0;
+  const size_t nt = (size_t)p.tokens * 8;
+  if ((st = span_rows(p, q.q_heads, q.q_stride, "q", &nq)) != DV_OK) return st;
+  if ((st = span_rows(p, q.q_heads, q.out_stride, "out", &no)) != DV_OK) return st;
+  if (overlap(q.out, no, q.q, nq) || overlap(q.out, no, tree, nt) || overlaps_layers(p, q.out, no))
+    return fail(DV_ERR_INVALID_ARG, "out overlaps q, tree or the cache's layer");
+  if (need > 0 &&
+      (overlap(workspace, need, q.q, nq) || overlap(workspace, need, q.out, no) ||
+       overlap(workspace, need, tree, nt) || overlaps_layers(p, workspace, need)))
+    return fail(DV_ERR_INVALID_ARG, "workspace overlaps q, out, tree or the cache's layer");
   if ((st = resolve_layers(&p)) != DV_OK) return st;
   void* dev = nullptr;
-  size_t nq = 0, no = 0;
-  if ((st = resolve_rows(p, q.q, q.q_heads, q.q_stride, "q", &dev, &nq)) != DV_OK) return st;
+  if ((st = resolve_words(q.q, nq, 16, "q", &dev)) != DV_OK) return st;
   q.q = dev;
-  if ((st = resolve_rows(p, q.out, q.q_heads, q.out_stride, "out", &dev, &no)) != DV_OK) return st;
+  if ((st = resolve_words(q.out, no, 16, "out", &dev)) != DV_OK) return st;
   q.out = dev;
-  if (overlap(q.out, no, q.q, nq)) return fail(DV_ERR_INVALID_ARG, "out overlaps q");
-  if (overlaps_layer(p, q.out, no))
-    return fail(DV_ERR_INVALID_ARG, "out overlaps the cache's layer");
   if (tree) {
-    if ((st = resolve_words(tree, (size_t)p.tokens * 8, 8, "tree", &dev)) != DV_OK) return st;
+    if ((st = resolve_words(tree, nt, 8, "tree", &dev)) != DV_OK) return st;
     tree = static_cast<const uint64_t*>(dev);
-    if (overlap(q.out, no, tree, (size_t)p.tokens * 8))
-      return fail(DV_ERR_INVALID_ARG, "out overlaps tree");
   }
   float* part = nullptr;
   if (need > 0) {
     if ((st = resolve_words(workspace, need, 32, "workspace", &dev)) != DV_OK) return st;
     part = static_cast<float*>(dev);
-    if (overlap(part, need, q.q, nq) || overlap(part, need, q.out, no))
-      return fail(DV_ERR_INVALID_ARG, "workspace overlaps q or out");
-    if (overlaps_layer(p, part, need) ||
-        (tree && overlap(part, need, tree, (size_t)p.tokens * 8)))
-      return fail(DV_ERR_INVALID_ARG, "workspace overlaps the cache's layer or tree");
   }
   const bool small = p.B <= kSmallBatch;
   if (q.dtype == DV_DTYPE_FP16)

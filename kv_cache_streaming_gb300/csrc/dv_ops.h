@@ -108,10 +108,10 @@ inline dv_status plan_layer(const dv_cache* c, int32_t layer, const int32_t* s, 
   return DV_OK;
 }
 
-// Checks a packed buffer of p.tokens rows of `heads` heads, `stride` elements
-// from row to row, and gives its device address and the bytes it spans.
-inline dv_status resolve_rows(const Plan& p, const void* ptr, int32_t heads, int64_t stride,
-                              const char* what, void** dev, size_t* span) {
+// Checks the stride of a packed buffer of p.tokens rows of `heads` heads, in elements from
+// row to row, and gives the bytes it spans.
+inline dv_status span_rows(const Plan& p, int32_t heads, int64_t stride, const char* what,
+                           size_t* span) {
   const int64_t row = (int64_t)heads * p.D;
   if (stride < row)
     return fail(DV_ERR_INVALID_ARG, "%s: a stride of %lld elements is less than a token's %lld",
@@ -122,7 +122,7 @@ inline dv_status resolve_rows(const Plan& p, const void* ptr, int32_t heads, int
     return fail(DV_ERR_MISALIGNED, "%s: a stride of %lld elements is not a multiple of 8", what,
                 (long long)stride);
   *span = (size_t)(((p.tokens - 1) * stride + row) * 2);
-  return resolve_words(ptr, *span, 16, what, dev);
+  return DV_OK;
 }
 
 // As resolve_cache: the cache's K and V bases, up to the last layer of the plan.
@@ -141,15 +141,20 @@ inline dv_status resolve_layers(Plan* p) {
 
 inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
+  return a && b && x < y + nb && y < x + na;
 }
 
-// Whether a buffer shares bytes with K or V of the plan's (one) layer, bases resolved.
-inline bool overlaps_layer(const Plan& p, const void* a, size_t n) {
-  const size_t at = (size_t)(p.l0 * p.layer_chunks) * 16;
+// Whether a buffer shares bytes with K or V of one of the plan's layers (not with what lies
+// between them).  By address alone: the buffers need not be resolved.
+inline bool overlaps_layers(const Plan& p, const void* a, size_t n) {
   const size_t bytes = (size_t)p.B * p.H * p.D * p.S * p.P;
-  return overlap(a, n, static_cast<const char*>(p.k) + at, bytes) ||
-         overlap(a, n, static_cast<const char*>(p.v) + at, bytes);
+  for (int32_t l = p.l0; l < p.l1; ++l) {
+    const size_t at = (size_t)(l * p.layer_chunks) * 16;
+    if (overlap(a, n, static_cast<const char*>(p.k) + at, bytes) ||
+        overlap(a, n, static_cast<const char*>(p.v) + at, bytes))
+      return true;
+  }
+  return false;
 }
 
 }  // namespace dv

@@ -1,0 +1,66 @@
+"""What the operators over the cache refuse by addresses and sizes alone, before any
+pointer is looked up (CPU: the tensors here are host memory that no call reaches)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_streaming_gb300 as dv
+
+F16 = torch.float16
+
+
+def _refused(status, words, fn):
+    with pytest.raises(dv.DvError) as ei:
+        fn()
+    assert ei.value.status == status and words in str(ei.value), ei.value
+
+
+class _Case:
+    """Two layers of one key head, 8 new tokens of the only sequence, in layer 1."""
+
+    def __init__(self, H=1, D=64, S=64):
+        self.K, self.V = (torch.zeros(2, H * D * S, dtype=F16) for _ in range(2))
+        self.cache = dv.Cache(2, 1, H, D, S, 2, self.K, self.V)
+        self.s, self.e = np.array([8], np.int32), np.array([16], np.int32)
+        self.k, self.v, self.q, self.out = (torch.zeros(8, n, D, dtype=F16) for n in (H, H, 2 * H, 2 * H))
+        self.positions = torch.zeros(8, dtype=torch.int32)
+
+    def on(self, t, layer, rows=0):
+        """[8, 1, D] rows of a layer: with one head, a valid tensor of tokens."""
+        return t[layer].view(-1, 1, 64)[rows:rows + 8]
+
+    def append(self, **kw):
+        a = dict(k=self.k, v=self.v, q=self.q, q_out=self.out, positions=self.positions) | kw
+        dv.dv_kv_append(self.cache, 1, self.s, self.e, a["k"], a["v"], q=a["q"], q_out=a["q_out"],
+                        positions=a["positions"], stream=0)
+
+
+@pytest.mark.parametrize("name", ["k", "v", "q", "q_out", "positions"])
+@pytest.mark.parametrize("which", ["K", "V"])
+@pytest.mark.parametrize("rows", [0, 8, 40])
+def test_append_refuses_to_read_the_layer_it_writes(name, which, rows):
+    c = _Case()
+    on = c.on(getattr(c, which), 1, rows)
+    if name in ("q", "q_out"):
+        kw = {"q": torch.zeros(8, 1, 64, dtype=F16), "q_out": torch.zeros(8, 1, 64, dtype=F16)} | {name: on}
+    else:
+        kw = {name: on.reshape(-1).view(torch.int32)[:8] if name == "positions" else on}
+    _refused(dv.DV_ERR_INVALID_ARG, "overlaps the cache's layer", lambda: c.append(**kw))
+
+
+@pytest.mark.parametrize("name", ["k", "v", "q", "positions"])
+def test_append_refuses_to_read_where_it_writes_the_queries(name):
+    c = _Case()
+    buf = torch.zeros(8 * 2 * 64, dtype=F16)
+    kw = {"q_out": buf.view(8, 2, 64)}
+    kw |= {"k": dict(k=buf[:8 * 64].view(8, 1, 64)), "v": dict(v=buf[-8 * 64:].view(8, 1, 64)),
+           "q": dict(q=buf.view(8, 2, 64)), "positions": dict(positions=buf.view(torch.int32)[100:108])}[name]
+    _refused(dv.DV_ERR_INVALID_ARG, "q_out overlaps", lambda: c.append(**kw))
+
+
+def test_append_takes_another_layers_rows():
+    """Past the checks of addresses: what stops it here is that the memory is the host's."""
+    c = _Case()
+    with pytest.raises(dv.DvError) as ei:
+        c.append(k=c.on(c.K, 0), v=c.on(c.V, 0, 40))
+    assert "overlaps" not in str(ei.value)
