@@ -721,7 +721,8 @@ dv_status dv_attention_check(dv_stream stream);
 /* Moves rows together, in place, in layers [l0, l1): row seq_start[b] + i of
  * sequence b (for every i below its range's length) gets what row
  * keep[T-index of (b, i)] of the sequence held before the call.  keep: device
- * memory, `count` = T int32 entries (else DV_ERR_INVALID_ARG), 4-byte aligned.  An entry that is negative, not
+ * memory, `count` = T int32 entries (else DV_ERR_INVALID_ARG), 4-byte aligned, on none of the
+ * layers that are moved (else DV_ERR_INVALID_ARG).  An entry that is negative, not
  * below max_seq, or below its own destination row leaves that row as it was
  * (so that a list of fixed length can be padded with -1).  Rows outside the
  * ranges are untouched.  Any elem_bytes. */

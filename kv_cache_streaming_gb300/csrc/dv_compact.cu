@@ -134,6 +134,8 @@ extern "C" dv_status dv_kv_compact(const dv_cache* cache, int32_t l0, int32_t l1
   if ((int64_t)p.H * p.C > INT32_MAX / 2 || 2 * (int64_t)(l1 - l0) * p.B * p.H > INT32_MAX)
     return dv::fail(DV_ERR_UNSUPPORTED, "%d layers, %d sequences, %d heads of %d chunks", l1 - l0,
                     p.B, p.H, p.C);
+  if (dv::overlaps_layers(p, keep, (size_t)p.tokens * 4))
+    return dv::fail(DV_ERR_INVALID_ARG, "keep overlaps a layer that the call moves rows of");
   if ((st = dv::resolve_layers(&p)) != DV_OK) return st;
   void* dev = nullptr;
   if ((st = dv::resolve_words(keep, (size_t)p.tokens * 4, 4, "keep", &dev)) != DV_OK) return st;

@@ -64,3 +64,22 @@ def test_append_takes_another_layers_rows():
     with pytest.raises(dv.DvError) as ei:
         c.append(k=c.on(c.K, 0), v=c.on(c.V, 0, 40))
     assert "overlaps" not in str(ei.value)
+
+
+@pytest.mark.parametrize("l0, l1, at, refused", [(0, 2, 0, True), (0, 2, 1, True), (1, 2, 1, True), (1, 2, 0, False)])
+@pytest.mark.parametrize("which", ["K", "V"])
+def test_compact_refuses_a_list_on_a_layer_it_moves(which, l0, l1, at, refused):
+    c = _Case()
+    keep = getattr(c, which)[at].view(torch.int32)[200:208]
+    with pytest.raises(dv.DvError) as ei:
+        dv.dv_kv_compact(c.cache, l0, l1, c.s, c.e, keep, stream=0)
+    assert ei.value.status == dv.DV_ERR_INVALID_ARG and ("overlaps" in str(ei.value)) == refused
+
+
+def test_compact_takes_a_list_between_layers():
+    n = 64 * 64
+    K, V = (torch.zeros(2, n + 64, dtype=F16) for _ in range(2))
+    cache = dv.Cache(2, 1, 1, 64, 64, 2, K, V, layer_stride_elems=n + 64)
+    with pytest.raises(dv.DvError) as ei:
+        dv.dv_kv_compact(cache, 0, 2, np.array([8]), np.array([16]), K[0, n:n + 16].view(torch.int32), stream=0)
+    assert "overlaps" not in str(ei.value)
