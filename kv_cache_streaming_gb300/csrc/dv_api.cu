@@ -115,6 +115,11 @@ dv_status plan_ranges(const dv_cache* c, int32_t l0, int32_t l1, const int32_t* 
   const int32_t x = 16 / c->elem_bytes;
   if (c->head_dim % x != 0)
     return fail(DV_ERR_UNSUPPORTED, "head_dim %d is not a multiple of x = %d", c->head_dim, x);
+  // (what follows counts the cache's bytes in 64 bits)
+  const double most = (double)((int64_t)1 << 60);
+  if ((double)c->batch * c->num_heads * c->head_dim * c->max_seq * c->num_layers > most ||
+      (double)c->layer_stride_elems * c->num_layers > most)
+    return fail(DV_ERR_UNSUPPORTED, "a cache of more than 2^60 elements");
   const int64_t dense = (int64_t)c->batch * c->num_heads * c->head_dim * c->max_seq;
   const int64_t stride = c->layer_stride_elems ? c->layer_stride_elems : dense;
   if (stride < dense)
@@ -211,11 +216,11 @@ static dv_status resolve_aligned(const void* ptr, size_t need, unsigned align, b
   size_t size = 0;
   const GetRangeFn range = get_range_fn();
   if (range && range(&base, &size, reinterpret_cast<CUdeviceptr>(*dev)) == CUDA_SUCCESS) {
-    const uintptr_t p0 = reinterpret_cast<uintptr_t>(*dev);
-    if (p0 + need > (uintptr_t)base + size)
+    const size_t after = (uintptr_t)base + size - reinterpret_cast<uintptr_t>(*dev);
+    if (need > after)
       return fail(DV_ERR_BUFFER_TOO_SMALL,
                   "%s: %zu bytes needed from %p but its allocation ends %zu bytes after it", what,
-                  need, ptr, (size_t)((uintptr_t)base + size - p0));
+                  need, ptr, after);
   }
   return DV_OK;
 }
@@ -243,10 +248,10 @@ dv_status resolve_words(const void* ptr, size_t need, unsigned align, const char
                                    CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
                                    CU_POINTER_ATTRIBUTE_RANGE_SIZE};
     void* out[5] = {&type, &managed, &device, &base, &size};
-    const uintptr_t p0 = reinterpret_cast<uintptr_t>(ptr);
-    if (get(5, attr, out, static_cast<CUdeviceptr>(p0)) == CUDA_SUCCESS &&
-        type == CU_MEMORYTYPE_DEVICE && !managed && device == cur && size > 0 &&
-        p0 + need <= static_cast<uintptr_t>(base) + size) {
+    const CUdeviceptr p0 = reinterpret_cast<uintptr_t>(ptr);
+    if (get(5, attr, out, p0) == CUDA_SUCCESS && type == CU_MEMORYTYPE_DEVICE && !managed &&
+        device == cur && size > 0 && p0 >= base && p0 - base <= size &&
+        need <= size - (size_t)(p0 - base)) {
       *dev = const_cast<void*>(ptr);
       return DV_OK;
     }

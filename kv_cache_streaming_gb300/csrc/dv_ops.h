@@ -121,6 +121,9 @@ inline dv_status span_rows(const Plan& p, int32_t heads, int64_t stride, const c
   if (stride % 8 != 0)
     return fail(DV_ERR_MISALIGNED, "%s: a stride of %lld elements is not a multiple of 8", what,
                 (long long)stride);
+  if (p.tokens - 1 > (((int64_t)1 << 60) - row) / stride)  // (the product below stays in range)
+    return fail(DV_ERR_BUFFER_TOO_SMALL, "%s: no allocation holds %lld tokens %lld elements apart",
+                what, (long long)p.tokens, (long long)stride);
   *span = (size_t)(((p.tokens - 1) * stride + row) * 2);
   return DV_OK;
 }

@@ -1,5 +1,7 @@
 """What the operators over the cache refuse by addresses and sizes alone, before any
 pointer is looked up (CPU: the tensors here are host memory that no call reaches)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -83,3 +85,43 @@ def test_compact_takes_a_list_between_layers():
     with pytest.raises(dv.DvError) as ei:
         dv.dv_kv_compact(cache, 0, 2, np.array([8]), np.array([16]), K[0, n:n + 16].view(torch.int32), stream=0)
     assert "overlaps" not in str(ei.value)
+
+
+# ---- sizes that 64 bits do not hold ----------------------------------------------------
+
+FAR = 1 << 40       # elements from one token to the next
+MANY = (1 << 23) + 1  # (MANY - 1) * FAR * 2 bytes is 2^64
+
+
+@pytest.mark.parametrize("name", ["k", "v", "q", "q_out"])
+@pytest.mark.parametrize("tokens", [MANY, MANY - 1, 3 * (MANY // 2) + 1])
+def test_append_refuses_strides_whose_extent_wraps(name, tokens):
+    from kv_cache_streaming_gb300.dv import dv_new_tokens
+    c = dv.Cache(1, 1, 1, 8, 1 << 24, 2, 0x1000, 0x2000)
+    s, e = np.array([0], np.int32), np.array([tokens], np.int32)
+    x = {n: 0x10000000000 * (i + 1) for i, n in enumerate(("k", "v", "q", "q_out"))}
+    st = {n: FAR if n == name else 8 for n in x}
+    t = dv_new_tokens(dv.DV_DTYPE_FP16, 1, tokens, x["k"], st["k"], x["v"], st["v"], x["q"], st["q"], x["q_out"],
+                      st["q_out"], None, None)
+    assert dv.lib.dv_kv_append(c.ref, 0, s.ctypes.data, e.ctypes.data, ctypes.byref(t), None) == \
+        dv.DV_ERR_BUFFER_TOO_SMALL
+
+
+@pytest.mark.parametrize("name", ["q", "out"])
+def test_attention_refuses_strides_whose_extent_wraps(name):
+    from kv_cache_streaming_gb300.dv import dv_queries
+    c = dv.Cache(1, 1, 1, 8, 1 << 24, 2, 0x1000, 0x2000)
+    s, e = np.array([0], np.int32), np.array([MANY], np.int32)
+    a = dv_queries(dv.DV_DTYPE_FP16, 1, MANY, 0x10000000000, FAR if name == "q" else 8, 0x20000000000,
+                   FAR if name == "out" else 8, 1.0)
+    assert dv.lib.dv_prompt_attention(c.ref, 0, s.ctypes.data, e.ctypes.data, ctypes.byref(a), 0x30000000000,
+                                      1 << 40, None) == dv.DV_ERR_BUFFER_TOO_SMALL
+
+
+@pytest.mark.parametrize("kw", [dict(layer_stride_elems=1 << 60), dict(S=1 << 30, D=1 << 20, B=1 << 10, H=1 << 10)])
+def test_caches_whose_bytes_wrap_are_refused(kw):
+    g = dict(B=1, H=1, D=64, S=32) | kw
+    c = dv.Cache(17, g["B"], g["H"], g["D"], g["S"], 2, 0x1000, 0x2000, layer_stride_elems=g.get("layer_stride_elems", 0))
+    s, e = np.zeros(g["B"], np.int32), np.ones(g["B"], np.int32)
+    keep = torch.zeros(g["B"], dtype=torch.int32)
+    _refused(dv.DV_ERR_UNSUPPORTED, "2^60", lambda: dv.dv_kv_compact(c, 0, 17, s, e, keep, stream=0))
