@@ -1126,8 +1126,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constan
       o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (ml[k].x != -INFINITY) {
-          const float f = ex2(ml[k].x - m);
+        if (i + k < pieces) {  // (a piece of NaN scores alone has m = -inf and l = NaN)
+          const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - m);
           l += f * ml[k].y;
           o.x += f * a[k].x;
           o.y += f * a[k].y;

@@ -49,3 +49,36 @@ def test_rotated_queries_are_allocated_under_the_stream_that_writes_them(handle)
         assert _stream_of(other) == torch.cuda.default_stream().cuda_stream
     torch.cuda.synchronize()
     assert torch.equal(other, want)
+
+
+# ---- scores and values at the ends of their types --------------------------------------
+
+def _attend(cache, s, e, q, scale, tree=None, prompt=False):
+    n = dv.dv_attention_workspace(cache, s, e, q.shape[1])
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") if n else None
+    out = torch.full_like(q, 7.0)
+    if prompt:
+        dv.dv_prompt_attention(cache, 0, s, e, q, out, scale, ws)
+    else:
+        dv.dv_tree_attention(cache, 0, s, e, q, out, scale, ws, tree=tree)
+    return out
+
+
+# one tile, tiles of both chains, pieces joined through the workspace
+LENGTHS = [(0, 3), (100, 5), (300, 20), (20000, 2), (9000, 33), (5, 700), (6000, 150)]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("ctx, n", LENGTHS)
+def test_a_query_of_nan_gives_nan_however_its_rows_are_divided(dtype, ctx, n):
+    H, G, D = 2, 4, 64
+    gen = _gen(ctx + n)
+    s, e = np.array([ctx], np.int32), np.array([ctx + n], np.int32)
+    cache, K, V = R.make_cache(dtype, 1, 1, H, D, ctx + n, gen)
+    q = torch.empty(n, H * G, D, dtype=R.DT[dtype], device="cuda").normal_(generator=gen)
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, 0.125)
+    q[n - 1, 3, 5] = math.nan
+    want[n - 1, 3] = math.nan
+    for prompt in (False, True):
+        if prompt or n <= 64:
+            R.assert_within(_attend(cache, s, e, q, 0.125, prompt=prompt), want, tol)
