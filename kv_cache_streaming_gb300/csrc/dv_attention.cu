@@ -835,7 +835,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       const int tok = tile_tok0 + tr, nt = i ? it.nt1 : it.nt0;
       const bool valid = tr < p.tile_tok && tok < it.n_tok;
       const bool any_valid = __any_sync(~0u, valid);
-      uint64_t bits = 0;
+      uint64_t bits = 1;  // (a prompt's token attends itself)
       if (p.is_tree && valid) {
         bits = p.tree ? __ldg(p.tree + it.tok_at + tok) : (2ull << tok) - 1;
         if (it.n_tok < 64) bits &= (1ull << it.n_tok) - 1;
@@ -962,7 +962,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       // ---- the piece's output: SPLIT each chain half of the columns ----
       if (any_valid) {
         const bool whole = it.whole != 0;
-        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        // A row that attends nothing gives zeros.  One whose every attended score is -inf has
+        // l = 0 too: 0 x inf, NaN, as its softmax is.
+        const float inv = !whole ? 1.f : it.start == 0 && bits == 0 ? 0.f : 1.f / l;
         constexpr int kCols = PAIR ? DP : DP / 2;
         const int c0 = PAIR ? 0 : i * kCols;
         // slot 0: the CTA's first piece, 1: its last
@@ -1135,7 +1137,9 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constan
           o.w += f * a[k].w;
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    // Some row is attended (a token that attends none has at most 64 rows, one tile, which no
+    // cut divides): l = 0 means scores of -inf alone, NaN.
+    const float inv = 1.f / l;
     uint16_t* const out =
         p.out + (int64_t)(d.tok + tok) * p.out_stride + (int64_t)(d.head + g) * p.D;
     reinterpret_cast<uint2*>(out)[c] =

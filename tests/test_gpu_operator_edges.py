@@ -82,3 +82,39 @@ def test_a_query_of_nan_gives_nan_however_its_rows_are_divided(dtype, ctx, n):
     for prompt in (False, True):
         if prompt or n <= 64:
             R.assert_within(_attend(cache, s, e, q, 0.125, prompt=prompt), want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("ctx, n", LENGTHS)
+@pytest.mark.parametrize("part", [1.0, 0.6])
+def test_scores_of_minus_infinity(dtype, ctx, n, part):
+    """Rows whose score is -inf have no weight; where every attended row is one,
+    the softmax is 0 / 0.  (A token that attends no row at all has zeros.)"""
+    H, G, D = 2, 4, 64
+    gen = _gen(ctx + n + 1)
+    s, e = np.array([ctx], np.int32), np.array([ctx + n], np.int32)
+    cache, K, V = R.make_cache(dtype, 1, 1, H, D, ctx + n, gen)
+    K[0, 0, 0, 0, :int(part * (ctx + n)), 0] = -math.inf  # element 0 of key head 0
+    q = torch.empty(n, H * G, D, dtype=R.DT[dtype], device="cuda").normal_(generator=gen)
+    q[:, :, 0] = 1.0
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, 0.125)
+    last = torch.arange(ctx, ctx + n, device="cuda")  # the last row that each token attends
+    want[last < int(part * (ctx + n)), :G] = math.nan
+    for prompt in (False, True):
+        if prompt or n <= 64:
+            R.assert_within(_attend(cache, s, e, q, 0.125, prompt=prompt), want, tol)
+
+
+def test_masks_of_rows_of_minus_infinity_and_masks_of_nothing():
+    H, D, n = 2, 64, 4
+    gen = _gen(3)
+    s, e = np.array([0], np.int32), np.array([n], np.int32)
+    cache, K, V = R.make_cache("bf16", 1, 1, H, D, n, gen)
+    K[0, 0, 0, 0, 1, 0] = -math.inf
+    q = torch.ones(n, H, D, dtype=torch.bfloat16, device="cuda")
+    bits = [0b0001, 0b0010, 0b0000, 0b0110]
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, 0.125, bits)
+    want[1, 0] = math.nan
+    got = _attend(cache, s, e, q, 0.125, tree=R.bits_tensor(bits))
+    R.assert_within(got, want, tol)
+    assert not got[2].any()
