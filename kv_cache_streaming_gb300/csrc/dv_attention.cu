@@ -990,7 +990,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           if (!PAIR) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(w0 == 0.f ? 0.f : __uint_as_float(o[e]) * w0);
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * w0);
             if (it.nt1 > 0) {
               uint32_t o1[32];
               tmem_ld32(o1, to + kTile + k);
@@ -998,8 +998,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 o[e] = __float_as_uint(
-                    w1 == 0.f ? __uint_as_float(o[e])
-                              : fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+                    fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
             }
           }
           if (valid) {

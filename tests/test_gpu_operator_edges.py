@@ -118,3 +118,21 @@ def test_masks_of_rows_of_minus_infinity_and_masks_of_nothing():
     got = _attend(cache, s, e, q, 0.125, tree=R.bits_tensor(bits))
     R.assert_within(got, want, tol)
     assert not got[2].any()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("row", [5, 130, 260])
+def test_values_of_nan_reach_tokens_that_give_them_no_weight(dtype, row):
+    """0 x NaN is NaN in whichever chain of tiles the row lies."""
+    H, D, ctx = 2, 64, 300
+    gen = _gen(row)
+    s, e = np.array([ctx], np.int32), np.array([ctx + 1], np.int32)
+    cache, K, V = R.make_cache(dtype, 1, 1, H, D, ctx + 1, gen)
+    lo = row // 128 * 128
+    K[0, 0, :, 0, lo:lo + 128, 0] = -400.0
+    V[0, 0, 0, row, 3] = math.nan
+    q = torch.empty(1, H, D, dtype=R.DT[dtype], device="cuda").normal_(generator=gen)
+    q[:, :, 0] = 40.0  # scores of -2000 beside ordinary ones
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, 0.125)
+    assert torch.isnan(want[0, 0, 3]) and torch.isfinite(want[0, 1]).all()
+    R.assert_within(_attend(cache, s, e, q, 0.125), want, tol)
