@@ -688,7 +688,8 @@ dv_status dv_attention_workspace(const dv_cache* cache, const int32_t* seq_start
  * already and the new tokens' rows since their dv_kv_append:
  *   out = sum_j w_j v_j,  w = softmax over the attended rows of scale * q.k_j.
  * Scores, softmax sums and outputs are accumulated in 32 bits; the weights
- * are rounded to `dtype` before they multiply v, the output once.  Rows that
+ * are rounded to `dtype` before they multiply v, the output once.  (fp16: a
+ * weight below 2^-21 of its row's largest loses bits, one below 2^-32 its part in the output.)  Rows that
  * a token does not attend have no effect on it, whatever they hold (NaN and
  * infinities included).  head_dim a multiple of 8 up to 128, elem_bytes 2
  * (else DV_ERR_UNSUPPORTED).  `workspace`: device memory, 32-byte aligned,

@@ -11,7 +11,8 @@
 // tensor memory, from where O += P V reads it as the left operand.  O stays
 // in tensor memory over all tiles.  f is applied lazily: as long as no row of
 // a warp grows by more than 2^8 the old maximum stays the reference (p up to
-// 256; P keeps its relative precision, l is summed in 32 bits).
+// 256; P keeps its relative precision, l is summed in 32 bits; a published
+// method).  fp16's p are held 2^7 times as large, in the middle of its range.
 //
 // Two chains of such tiles run at once, one's softmax under the other's
 // products:
@@ -72,6 +73,10 @@ constexpr uint32_t kSpinLimit = 1u << 22;
 constexpr int kJoinThreads = 256;
 constexpr int kTurnPolls = 32;     // of another chain's progress, a preference (about 1 us)
 constexpr float kLazy = 8.f;       // log2 of the growth that is left to the old maximum
+// fp16 holds weights to 2^-25 of the largest and loses bits of those below 2^-14: log2 of a
+// factor on all of a row's weights, and on l with them, that takes both down by its share.
+// 2^(kLazy + kHalfUp) stays below fp16's 2^16.
+constexpr float kHalfUp = 7.f;
 
 // Set when a wait in an attention kernel gave up.
 __device__ unsigned int g_attention_timeout;
@@ -854,9 +859,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         ++s_count;
         fence_after();
         uint32_t x[kTile];
-        // Half of the row: p = exp2(c (s - m)), to tensor memory; gives its sum.
+        // Half of the row: p = 2^kUp exp2(c (s - m)), to tensor memory; gives its sum.
         const auto half_row = [&](int half) {
-          const float mb = m == -INFINITY ? 0.f : -m * p.c;
+          constexpr float kUp = std::is_same<T, __half>::value ? kHalfUp : 0.f;
+          const float mb = m == -INFINITY ? kUp : fmaf(-m, p.c, kUp);
           float sum[4] = {};
 #pragma unroll
           for (int k = 2 * half; k < 2 * half + 2; ++k) {

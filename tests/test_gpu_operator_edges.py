@@ -136,3 +136,26 @@ def test_values_of_nan_reach_tokens_that_give_them_no_weight(dtype, row):
     want, tol = R.attention_ref(K[0], V[0], s, e, q, 0.125)
     assert torch.isnan(want[0, 0, 3]) and torch.isfinite(want[0, 1]).all()
     R.assert_within(_attend(cache, s, e, q, 0.125), want, tol)
+
+
+@pytest.mark.parametrize("peak", [0, 70000, 131071])
+@pytest.mark.parametrize("nats", [9.0, 17.0])
+@pytest.mark.parametrize("n", [1, 200])
+def test_the_many_small_weights_below_a_peak(peak, nats, n):
+    """fp16: 131071 keys far below one peak have a good part of the output between
+    them. attention_ref's bound allows each weight 2^-25 of the largest; they
+    are held to 2^-32 (half a step of fp16's smallest, 2^-25, of weights 2^7 times
+    as large)."""
+    H, D, S = 1, 64, 131072 + n
+    gen = _gen(peak + n)
+    s, e = np.array([131072], np.int32), np.array([S], np.int32)
+    cache, K, V = R.make_cache("fp16", 1, 1, H, D, S, gen, fill=0.0)
+    V[0, 0, 0] = torch.rand(S, D, device="cuda", generator=gen).to(torch.float16)
+    K[0, 0, 0, 0, peak, 0], V[0, 0, 0, peak] = nats, 0.0
+    q = torch.zeros(n, H, D, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1.0
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, 1.0)
+    tol -= (2.0 ** -25 - 2.0 ** -32) * V[0, 0, 0].double().abs().sum(0)
+    if n <= 64:
+        R.assert_within(_attend(cache, s, e, q, 1.0), want, tol)
+    R.assert_within(_attend(cache, s, e, q, 1.0, prompt=True), want, tol)
