@@ -159,3 +159,23 @@ def test_the_many_small_weights_below_a_peak(peak, nats, n):
     if n <= 64:
         R.assert_within(_attend(cache, s, e, q, 1.0), want, tol)
     R.assert_within(_attend(cache, s, e, q, 1.0, prompt=True), want, tol)
+
+
+@pytest.mark.parametrize("peak", [0, 9000])
+@pytest.mark.parametrize("n", [1, 200])
+def test_the_many_small_weights_of_undivided_rows(peak, n):
+    """As above with two heads for each SM, so that no head's rows are divided: the
+    peak is the reference of all of its row's weights."""
+    H, D, ctx = 2 * torch.cuda.get_device_properties(0).multi_processor_count, 64, 16384
+    gen = _gen(peak + n)
+    s, e = np.array([ctx], np.int32), np.array([ctx + n], np.int32)
+    cache, K, V = R.make_cache("fp16", 1, 1, H, D, ctx + n, gen, fill=0.0)
+    V[0, 0] = torch.rand(H, ctx + n, D, device="cuda", generator=gen).to(torch.float16)
+    K[0, 0, :, 0, peak, 0], V[0, 0, :, peak] = 17.0, 0.0
+    q = torch.zeros(n, H, D, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1.0
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, 1.0)
+    tol -= (2.0 ** -25 - 2.0 ** -32) * V[0, 0].double().abs().sum(1)
+    for prompt in (False, True):
+        if prompt or n <= 64:
+            R.assert_within(_attend(cache, s, e, q, 1.0, prompt=prompt), want, tol)
