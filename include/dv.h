@@ -169,6 +169,12 @@ const char* dv_last_error(void);
  * it.  In the regular build it returns DV_ERR_UNSUPPORTED. */
 dv_status dv_debug_fault(uint64_t* fault);
 
+/* Debugging.  The tries that each wait inside an attention kernel launched from now on takes
+ * before it gives up (see dv_attention_check): at most 2^22, the regular number, which any
+ * negative value stands for; 0: every wait gives up at once.  For tests of the failure
+ * path: the outputs of a kernel that gave up are not valid. */
+dv_status dv_debug_attention_tries(int32_t tries);
+
 /* Bytes from `ptr` to the end of the CUDA allocation that holds it, as the
  * driver reports it; every call checks the buffers it is given against this
  * extent when the driver knows it.  DV_ERR_UNSUPPORTED when the driver cannot

@@ -43,8 +43,9 @@
 // scores are computed, and should there have been any, the epilogue adds them
 // to the outputs of the rows that do attend them.
 //
-// Every wait gives up after kSpinLimit tries: the CTA then drains its copies,
-// frees its tensor memory and returns, and dv_attention_check reports it.
+// Every wait gives up after a number of tries (kSpinLimit, unless a test has set fewer):
+// the CTA then drains its copies and products, each with a bounded wait too, frees its tensor
+// memory and returns, and dv_attention_check reports it.
 //
 // Measured (bf16, heads of 128 unless said).  SPLIT is bound by HBM: a decode
 // step of 32 sequences of 64 to 1791 rows, 112 heads (1.52 GB) 232 us, 6.5 TB/s.
@@ -61,6 +62,8 @@
 // 10% each); one product warp for both chains (28% on ragged prompts); the next
 // tile's second half of scores issued as soon as S has been read (4 to 6%).
 #include <cuda.h>
+
+#include <atomic>
 
 #include "dv_ops.h"
 
@@ -110,6 +113,7 @@ struct AttnParams {
   int32_t unit_tok;  // tokens of a unit
   int32_t unit_cost;  // in tiles, on top of a unit's tiles
   int32_t is_tree;
+  uint32_t tries;    // of a wait, before it gives up
   int32_t wide;  // every output row of a head is 32-byte aligned, of whole 32-byte sectors
   float c;  // scale * log2(e)
   SeqTable<MAXB> seq;
@@ -138,19 +142,22 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of `parity` to complete; false when it gave up.  Kept
-// short: it stands at some thirty places, and the kernel's speed hangs on its
-// size (an instruction cache miss in every loop made ragged prompts twice as slow).
+// Waits, as a whole warp, for the phase of `parity` to complete; false when it gave up after
+// `tries`.  The vote makes it one answer for the warp's lanes, which go on to instructions
+// that need all of them: a phase may complete between one lane's last try and another's.
+// (It costs about 1% on short prompts and trees.)  Kept short: it stands at some thirty
+// places, and the kernel's speed hangs on its size (an instruction cache miss in every loop
+// made ragged prompts twice as slow).
 __device__ __forceinline__ bool gave_up() {
   atomicExch(&g_attention_timeout, 1u);
   return false;
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  uint32_t left = kSpinLimit;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
+  bool ok = false;
 #pragma unroll 1
-  while (!bar_try(bar, parity))
-    if (--left == 0) return gave_up();
-  return true;
+  for (; tries != 0 && !(ok = bar_try(bar, parity)); --tries) {
+  }
+  return __all_sync(~0u, ok) || gave_up();
 }
 
 // The load and the product warp run their loops as whole warps on uniform
@@ -459,7 +466,11 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = smem_u32(sm);
   if ((base & 1023) != 0) {  // the swizzle goes by address bits
-    g_attention_timeout = 1;
+    ops_pdl_enter();
+    if (threadIdx.x == 0) {
+      gave_up();
+      if (blockIdx.x > 0) p.divided[blockIdx.x - 1] = Divided{};  // nothing for the join
+    }
     return;
   }
   typename SM::Ctl& ctl = *reinterpret_cast<typename SM::Ctl*>(sm + SM::kCtl);
@@ -511,9 +522,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
   // (Global memory is touched only past this; the load warp finds its first unit before.)
   if (warp != 8) ops_pdl_enter();
 
+  const auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.tries); };
   // The k-th item, from the ring.
   const auto get_item = [&](uint32_t k, Item* it) {
-    if (!bar_wait(at(ctl.item_full[k % kItems]), k / kItems & 1)) return false;
+    if (!wait(at(ctl.item_full[k % kItems]), k / kItems & 1)) return false;
     *it = ctl.item[k % kItems];
     return __all_sync(~0u, it->n > 0) != 0;
   };
@@ -551,7 +563,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         bool ok = true;
         const auto publish = [&](const Item& x) {
           if (n_items >= kItems)
-            ok = bar_wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1);
+            ok = wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1);
           if (!ok) return;
           if (on) {
             ctl.item[n_items % kItems] = x;
@@ -562,7 +574,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         const auto load_q = [&](const Item& x, int i) {
           const int qb = PAIR ? i : (int)(n_q & 1);
           const uint32_t used = qb ? q1 : q0;  // the buffer's loads so far
-          if (used > 0) ok = bar_wait(at(ctl.q_empty[qb]), (used - 1) & 1);
+          if (used > 0) ok = wait(at(ctl.q_empty[qb]), (used - 1) & 1);
           if (!ok) return;
           if (qb) ++q1; else ++q0;
           ++n_q;
@@ -578,7 +590,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll 1
         while (ok) {
           if (v_rows > 0) {
-            if (nv >= SM::kV) ok = bar_wait(at(ctl.v_empty[vr.slot]), vr.turn ^ 1);
+            if (nv >= SM::kV) ok = wait(at(ctl.v_empty[vr.slot]), vr.turn ^ 1);
             if (!ok) break;
             // a whole tile in one copy a half, else in boxes of 32 rows
             const uint32_t bar = at(ctl.v_full[vr.slot]);
@@ -615,7 +627,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           }
           if (!ok) break;
           const int row = (it.t0 + j) * kTile, rows = min(kTile, it.row_end - row);
-          if (nk >= SM::kK) ok = bar_wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1);
+          if (nk >= SM::kK) ok = wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1);
           if (!ok) break;
           const uint32_t bar = at(ctl.k_full[kr.slot]);
           const uint32_t dst = base + SM::kKAt + kr.slot * SM::kSlot;
@@ -637,17 +649,15 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           fetch = j == 0;
           step = ++j == it.n;
         }
-        // A CTA that gave up leaves no copy in flight.
-        if (!ok) {
+        // No copy is left in flight, whichever warp gave up: nobody else may have waited for it.
 #pragma unroll 1
-          for (uint32_t i = 0; i < SM::kK && i < nk; ++i)  // a slot's last use
-            bar_wait(at(ctl.k_full[i]), (nk - i - 1) / SM::kK & 1);
+        for (uint32_t i = 0; i < SM::kK && i < nk; ++i)  // a slot's last use
+          bar_wait(at(ctl.k_full[i]), (nk - i - 1) / SM::kK & 1, kSpinLimit);
 #pragma unroll 1
-          for (uint32_t i = 0; i < SM::kV && i < nv; ++i)
-            bar_wait(at(ctl.v_full[i]), (nv - i - 1) / SM::kV & 1);
-          if (q0 > 0) bar_wait(at(ctl.q_full[0]), (q0 - 1) & 1);
-          if (q1 > 0) bar_wait(at(ctl.q_full[1]), (q1 - 1) & 1);
-        }
+        for (uint32_t i = 0; i < SM::kV && i < nv; ++i)
+          bar_wait(at(ctl.v_full[i]), (nv - i - 1) / SM::kV & 1, kSpinLimit);
+        if (q0 > 0) bar_wait(at(ctl.q_full[0]), (q0 - 1) & 1, kSpinLimit);
+        if (q1 > 0) bar_wait(at(ctl.q_full[1]), (q1 - 1) & 1, kSpinLimit);
       }
       __syncwarp();
     } else if (warp < 11) {
@@ -675,7 +685,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           const uint32_t q_parity = (PAIR ? n_q : n_items >> 1) & 1;
           if (nt > 0) ++n_q;
           if (!PAIR && nt == 0) {  // (once the buffer's last turn is over for both chains)
-            if (!(ok = bar_wait(at(ctl.q_full[qb]), q_parity))) break;
+            if (!(ok = wait(at(ctl.q_full[qb]), q_parity))) break;
             if (on) bar_arrive(at(ctl.q_empty[qb]));
           }
           const auto mine = [&](int j) { return PAIR ? j < nt : (j & 1) == i; };
@@ -689,9 +699,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             while (jk < n) {
               const bool own = mine(jk);
               if (!own && jk > jv + 1) break;
-              if (!bar_wait(at(ctl.k_full[kr.slot]), kr.turn)) return false;
+              if (!wait(at(ctl.k_full[kr.slot]), kr.turn)) return false;
               if (own) {
-                if (k_mine == 0 && !bar_wait(at(ctl.q_full[qb]), q_parity)) return false;
+                if (k_mine == 0 && !wait(at(ctl.q_full[qb]), q_parity)) return false;
                 if (PAIR && t0 + jk < masked) {
                   // The chains take turns: a chain's scores are computed once the other's softmax
                   // is at its exponentials, so that one's products run under the other's
@@ -730,7 +740,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             while (jv < jk) {
               const bool own = mine(jv);
               // (hidden rows have been looked at where the tile has any)
-              if (!bar_wait(at(own && t0 + jv >= masked ? ctl.v_ok[vr.slot] : ctl.v_full[vr.slot]),
+              if (!wait(at(own && t0 + jv >= masked ? ctl.v_ok[vr.slot] : ctl.v_full[vr.slot]),
                             vr.turn))
                 return false;
               if (own) {
@@ -739,12 +749,12 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
                 const int rows = min(kTile, row_end - (t0 + jv) * kTile);
                 const bool more = v_mine > 0;
-                if (!bar_wait(at(ctl.p_half[i]), p_count & 1)) return false;
+                if (!wait(at(ctl.p_half[i]), p_count & 1)) return false;
                 fence_after();
 #pragma unroll
                 for (int s = 0; s < kTile / 32; ++s)
                   mma_ts(o, s0 + s * 8, vd + s * 128, kIdescO, more || s > 0, on && s * 16 < rows);
-                if (!bar_wait(at(ctl.p_ready[i]), p_count & 1)) return false;
+                if (!wait(at(ctl.p_ready[i]), p_count & 1)) return false;
                 fence_after();
 #pragma unroll
                 for (int s = kTile / 32; s < kTile / 16; ++s)
@@ -772,7 +782,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         }
         // the products in flight end before tensor memory is given back
         mma_commit(at(ctl.drained), on);
-        bar_wait(at(ctl.drained), 0);
+        bar_wait(at(ctl.drained), 0, kSpinLimit);
       }
       __syncwarp();
     } else {
@@ -783,7 +793,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       for (uint32_t k = 0; ok && get_item(k, &it); ++k) {
 #pragma unroll 1
         for (int j = 0; j < it.n; ++j, vr.next()) {
-          if (!(ok = bar_wait(at(ctl.v_full[vr.slot]), vr.turn))) break;
+          if (!(ok = wait(at(ctl.v_full[vr.slot]), vr.turn))) break;
           const int row0 = (it.t0 + j) * kTile;
           if (it.t0 + j >= it.masked) {
 #pragma unroll 1
@@ -849,13 +859,13 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       const int masked = p.is_tree ? it.masked : (it.start + tile_tok0 + 1) / kTile;
       if (!PAIR && item > 0) {  // the other chain has read this chain's last O
         const uint32_t w = item - 1;
-        if (!(ok = bar_wait(at(ctl.o_read[w & 1]), w >> 1 & 1))) break;
+        if (!(ok = wait(at(ctl.o_read[w & 1]), w >> 1 & 1))) break;
       }
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < nt; ++j) {
         const int tile = it.t0 + (PAIR ? j : 2 * j + i);
-        if (!(ok = bar_wait(at(ctl.s_full[i]), s_count & 1))) break;
+        if (!(ok = wait(at(ctl.s_full[i]), s_count & 1))) break;
         ++s_count;
         fence_after();
         uint32_t x[kTile];
@@ -948,7 +958,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       }
       if (!ok) break;
       if (nt > 0) {
-        if (!(ok = bar_wait(at(ctl.o_done[i]), o_count & 1))) break;
+        if (!(ok = wait(at(ctl.o_done[i]), o_count & 1))) break;
         ++o_count;
         fence_after();
       }
@@ -957,7 +967,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         ctl.ml[i][r] = make_float2(m, l);
         fence_before();
         bar_arrive(at(ctl.xchg));
-        if (!(ok = bar_wait(at(ctl.xchg), item & 1))) break;
+        if (!(ok = wait(at(ctl.xchg), item & 1))) break;
         fence_after();  // the other chain's O has been waited for by its own threads
         const float2 a = ctl.ml[0][r], b = ctl.ml[1][r];
         m = fmaxf(a.x, b.x);
@@ -1165,6 +1175,8 @@ struct Schedule {
   size_t part_bytes, bytes;  // of workspace: the pieces' sums, all
 };
 
+std::atomic<uint32_t> g_tries{kSpinLimit};
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1298,6 +1310,7 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
   kp.is_tree = is_tree ? 1 : 0;
   kp.wide = p.D % 16 == 0 && q.out_stride % 16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 32 == 0;
   kp.c = q.scale * 1.4426950408889634f;
+  kp.tries = g_tries.load(std::memory_order_relaxed);
   fill_table(p, &kp.seq);
   cudaError_t err;
   if (p.D <= 64)
@@ -1415,6 +1428,13 @@ extern "C" dv_status dv_attention_workspace(const dv_cache* cache, const int32_t
   const size_t a = dv::schedule(p, group, false, nullptr).bytes;
   const size_t b = p.max_len <= DV_MAX_TREE ? dv::schedule(p, group, true, nullptr).bytes : 0;
   *bytes = a > b ? a : b;
+  return DV_OK;
+}
+
+extern "C" dv_status dv_debug_attention_tries(int32_t tries) {
+  if (tries > (int32_t)dv::kSpinLimit)
+    return dv::fail(DV_ERR_INVALID_ARG, "%d tries are more than %u", tries, dv::kSpinLimit);
+  dv::g_tries.store(tries < 0 ? dv::kSpinLimit : (uint32_t)tries, std::memory_order_relaxed);
   return DV_OK;
 }
 

@@ -135,6 +135,7 @@ _prompt_attention = _sig("dv_prompt_attention", [_CP, _I32, _I32P, _I32P,
 _tree_attention = _sig("dv_tree_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
                                              _P, _P, _SZ, _P])
 _attention_check = _sig("dv_attention_check", [_P])
+_attention_tries = _sig("dv_debug_attention_tries", [_I32])
 _compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _I64, _P])
 
 
@@ -898,6 +899,12 @@ def dv_attention_check(stream=None) -> None:
     """Waits for the stream; raises DvError (DV_ERR_TIMEOUT) if a wait inside an
     attention kernel gave up since the last check."""
     _check(_attention_check(_stream(stream)))
+
+
+def dv_debug_attention_tries(tries=-1) -> None:
+    """Tries of each wait inside an attention kernel before it gives up, for tests
+    of the failure path (negative: the regular number; 0: none)."""
+    _check(_attention_tries(tries))
 
 
 def dv_kv_compact(cache: Cache, l0, l1, seq_start, seq_end, keep, stream=None) -> None:

@@ -179,3 +179,55 @@ def test_the_many_small_weights_of_undivided_rows(peak, n):
     for prompt in (False, True):
         if prompt or n <= 64:
             R.assert_within(_attend(cache, s, e, q, 1.0, prompt=prompt), want, tol)
+
+
+# ---- waits that give up ------------------------------------------------------------------
+
+def _gives_up(stream=None):
+    """Whether the check reports a wait that gave up."""
+    try:
+        dv.dv_attention_check(stream)
+        return False
+    except dv.DvError as err:
+        assert err.status == dv.DV_ERR_TIMEOUT
+        return True
+
+
+@pytest.fixture
+def few_tries():
+    dv.dv_attention_check()
+    yield dv.dv_debug_attention_tries
+    dv.dv_debug_attention_tries(-1)
+    torch.cuda.synchronize()
+    _gives_up()  # (a record that a failed test has left)
+
+
+@pytest.mark.parametrize("H, G, D, ctx, n", [
+    (1, 1, 64, 0, 1),        # one unit of one tile: everything is loaded without a wait
+    (2, 4, 64, 300, 5),
+    (2, 4, 128, 5000, 40),   # rings that fill, pieces that are joined
+    (200, 1, 128, 700, 9),   # more units than SMs
+    (3, 1, 72, 100, 600),
+    (40, 2, 128, 0, 700),
+])
+def test_a_wait_that_gives_up_ends_in_a_status(few_tries, H, G, D, ctx, n):
+    """With no tries at all every wait gives up at once, with copies in flight and
+    tensor memory held; with a few, here and there. The kernel ends, the check
+    says so once, and the next call works."""
+    gen = _gen(ctx + n)
+    s, e = np.array([ctx, 0], np.int32), np.array([ctx + n, 1], np.int32)
+    cache, K, V = R.make_cache("bf16", 1, 2, H, D, ctx + n, gen)
+    q = torch.empty(n + 1, H * G, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, 0.125)
+    for prompt in (False, True):
+        if n > 64 and not prompt:
+            continue
+        for tries in (0, 1, 2, 3, 5, 10, 30, 100):
+            few_tries(tries)
+            for _ in range(3):
+                _attend(cache, s, e, q, 0.125, prompt=prompt)
+            assert _gives_up() or tries > 0
+            assert not _gives_up()
+            few_tries(-1)
+            R.assert_within(_attend(cache, s, e, q, 0.125, prompt=prompt), want, tol)
+            assert not _gives_up()

@@ -125,3 +125,9 @@ def test_caches_whose_bytes_wrap_are_refused(kw):
     s, e = np.zeros(g["B"], np.int32), np.ones(g["B"], np.int32)
     keep = torch.zeros(g["B"], dtype=torch.int32)
     _refused(dv.DV_ERR_UNSUPPORTED, "2^60", lambda: dv.dv_kv_compact(c, 0, 17, s, e, keep, stream=0))
+
+
+def test_tries_of_a_wait_are_at_most_the_regular_number():
+    _refused(dv.DV_ERR_INVALID_ARG, "tries", lambda: dv.dv_debug_attention_tries((1 << 22) + 1))
+    dv.dv_debug_attention_tries(1 << 22)
+    dv.dv_debug_attention_tries(-5)
