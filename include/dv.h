@@ -719,10 +719,12 @@ dv_status dv_tree_attention(const dv_cache* cache, int32_t layer, const int32_t*
                             const uint64_t* tree, void* workspace, size_t workspace_bytes,
                             dv_stream stream);
 
-/* Waits for `stream` and reports whether a wait inside an attention kernel
- * has given up since the last check (DV_ERR_TIMEOUT; the record is cleared).  The
- * kernels' internal waits are bounded, so that a defect would end in this status and an
- * output that is not valid, not in a hang; DV_OK otherwise. */
+/* Waits for `stream` and reports whether a wait inside an attention kernel on
+ * this device has given up since the last check on this stream (its first: since the
+ * library was loaded): DV_ERR_TIMEOUT, else DV_OK.  Every stream that is checked is
+ * told, whichever one the kernel ran on, for a launch from a graph too.  The kernels'
+ * internal waits are bounded, so that a defect would end in this status and an output
+ * that is not valid, not in a hang. */
 dv_status dv_attention_check(dv_stream stream);
 
 /* Moves rows together, in place, in layers [l0, l1): row seq_start[b] + i of

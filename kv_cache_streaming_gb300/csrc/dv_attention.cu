@@ -64,6 +64,8 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <mutex>
+#include <vector>
 
 #include "dv_ops.h"
 
@@ -81,8 +83,9 @@ constexpr float kLazy = 8.f;       // log2 of the growth that is left to the old
 // 2^(kLazy + kHalfUp) stays below fp16's 2^16.
 constexpr float kHalfUp = 7.f;
 
-// Set when a wait in an attention kernel gave up.
-__device__ unsigned int g_attention_timeout;
+// Waits in attention kernels that gave up, one for each lane; only ever grows, so that no
+// caller's check takes another's record away.
+__device__ unsigned long long g_attention_gave_up;
 // The second half of the last contraction step when head_dim is an odd number of chunks.
 __device__ uint4 g_zero_rows[kTile];
 
@@ -149,7 +152,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // places, and the kernel's speed hangs on its size (an instruction cache miss in every loop
 // made ragged prompts twice as slow).
 __device__ __forceinline__ bool gave_up() {
-  atomicExch(&g_attention_timeout, 1u);
+  atomicAdd(&g_attention_gave_up, 1ull);
   return false;
 }
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
@@ -1438,18 +1441,49 @@ extern "C" dv_status dv_debug_attention_tries(int32_t tries) {
   return DV_OK;
 }
 
-extern "C" dv_status dv_attention_check(dv_stream stream) {
-  void* flag = nullptr;
-  cudaError_t err = cudaGetSymbolAddress(&flag, dv::g_attention_timeout);
-  unsigned int v = 0;
-  if (err == cudaSuccess)
-    err = cudaMemcpyAsync(&v, flag, sizeof(v), cudaMemcpyDeviceToHost, stream);
-  if (err == cudaSuccess && (err = cudaStreamSynchronize(stream)) == cudaSuccess && v != 0) {
-    err = cudaMemsetAsync(flag, 0, sizeof(v), stream);
-    if (err == cudaSuccess)
-      return dv::fail(DV_ERR_TIMEOUT, "an attention kernel gave up a wait; its output is not valid");
+namespace {
+
+// The count of waits that gave up as a stream's last check found it; streams without an entry
+// have found none.
+struct Checked {
+  unsigned long long context, stream, count;
+};
+
+// Whether `count` is news to the stream; remembers it.
+bool count_is_new(unsigned long long context, unsigned long long stream, unsigned long long count) {
+  static std::mutex mu;
+  static std::vector<Checked> checked;
+  if (count == 0) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  for (Checked& c : checked)
+    if (c.context == context && c.stream == stream) {
+      const bool news = c.count != count;
+      c.count = count;
+      return news;
+    }
+  try {
+    checked.push_back({context, stream, count});
+  } catch (...) {  // reported again by the next check
   }
-  return err == cudaSuccess ? DV_OK : dv::cuda_fail(err, "reading the attention kernels' flag");
+  return true;
+}
+
+}  // namespace
+
+extern "C" dv_status dv_attention_check(dv_stream stream) {
+  cudaError_t err = cudaSuccess;
+  void* counter = nullptr;
+  unsigned long long id = 0, context = 0, count = 0;
+  if (err == cudaSuccess) err = cudaStreamGetId(stream, &id);
+  if (err == cudaSuccess) err = cudaGetSymbolAddress(&counter, dv::g_attention_gave_up);
+  if (err == cudaSuccess)
+    err = cudaMemcpyAsync(&count, counter, sizeof(count), cudaMemcpyDeviceToHost, stream);
+  if (err == cudaSuccess) err = cudaStreamSynchronize(stream);
+  if (err != cudaSuccess) return dv::cuda_fail(err, "reading the attention kernels' count");
+  dv::context_id(&context);
+  if (count_is_new(context, id, count))
+    return dv::fail(DV_ERR_TIMEOUT, "an attention kernel gave up a wait; its output is not valid");
+  return DV_OK;
 }
 
 extern "C" dv_status dv_prompt_attention(const dv_cache* cache, int32_t layer,

@@ -897,7 +897,7 @@ def dv_tree_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, wo
 
 def dv_attention_check(stream=None) -> None:
     """Waits for the stream; raises DvError (DV_ERR_TIMEOUT) if a wait inside an
-    attention kernel gave up since the last check."""
+    attention kernel gave up since the last check on this stream."""
     _check(_attention_check(_stream(stream)))
 
 

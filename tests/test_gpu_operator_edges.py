@@ -231,3 +231,29 @@ def test_a_wait_that_gives_up_ends_in_a_status(few_tries, H, G, D, ctx, n):
             few_tries(-1)
             R.assert_within(_attend(cache, s, e, q, 0.125, prompt=prompt), want, tol)
             assert not _gives_up()
+
+
+def test_every_streams_check_reports_a_wait_that_gave_up(few_tries):
+    """One caller's check takes no other caller's record away."""
+    s, e = np.array([300], np.int32), np.array([305], np.int32)
+    cache, K, V = R.make_cache("bf16", 1, 1, 2, 64, 305, _gen(1))
+    q = torch.ones(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        _gives_up(st)
+        assert not _gives_up(st)
+    torch.cuda.synchronize()
+    few_tries(0)
+    for st in streams:
+        with torch.cuda.stream(st):
+            _attend(cache, s, e, q, 0.125)
+    few_tries(-1)
+    torch.cuda.synchronize()
+    for st in streams:
+        assert _gives_up(st)
+    for st in streams:
+        assert not _gives_up(st)
+    assert _gives_up() and not _gives_up()  # the current stream's, which has seen none of it
+    with torch.cuda.stream(streams[0]):
+        _attend(cache, s, e, q, 0.125)
+    assert not any(_gives_up(st) for st in streams)
