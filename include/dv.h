@@ -602,8 +602,8 @@ void dv_delta_streamer_destroy(dv_delta_streamer* ds);
  * ranges: the rows of the NEW tokens of each sequence.  Buffers with one entry per new
  * token hold the sequences' tokens one after the other (packed, no padding),
  * T = sum(seq_end - seq_start) of them; an empty range is a sequence that
- * takes no part.  Every pointer is device memory; every call can be captured
- * in a CUDA graph. */
+ * takes no part.  Every pointer is device memory; every call but
+ * dv_attention_check can be captured in a CUDA graph. */
 
 typedef enum { DV_DTYPE_FP16 = 0, DV_DTYPE_BF16 = 1 } dv_dtype;
 
@@ -724,7 +724,8 @@ dv_status dv_tree_attention(const dv_cache* cache, int32_t layer, const int32_t*
  * library was loaded): DV_ERR_TIMEOUT, else DV_OK.  Every stream that is checked is
  * told, whichever one the kernel ran on, for a launch from a graph too.  The kernels'
  * internal waits are bounded, so that a defect would end in this status and an output
- * that is not valid, not in a hang. */
+ * that is not valid, not in a hang.  No part of a graph: DV_ERR_INVALID_ARG while
+ * `stream` is being captured. */
 dv_status dv_attention_check(dv_stream stream);
 
 /* Moves rows together, in place, in layers [l0, l1): row seq_start[b] + i of

@@ -1471,7 +1471,11 @@ bool count_is_new(unsigned long long context, unsigned long long stream, unsigne
 }  // namespace
 
 extern "C" dv_status dv_attention_check(dv_stream stream) {
-  cudaError_t err = cudaSuccess;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaError_t err = cudaStreamIsCapturing(stream, &capture);
+  if (err == cudaSuccess && capture != cudaStreamCaptureStatusNone)
+    return dv::fail(DV_ERR_INVALID_ARG, "dv_attention_check waits for its stream, which is being "
+                    "captured into a graph");
   void* counter = nullptr;
   unsigned long long id = 0, context = 0, count = 0;
   if (err == cudaSuccess) err = cudaStreamGetId(stream, &id);

@@ -257,3 +257,25 @@ def test_every_streams_check_reports_a_wait_that_gave_up(few_tries):
     with torch.cuda.stream(streams[0]):
         _attend(cache, s, e, q, 0.125)
     assert not any(_gives_up(st) for st in streams)
+
+
+def test_the_check_is_refused_in_a_capture_and_leaves_it_whole():
+    s, e = np.array([300], np.int32), np.array([305], np.int32)
+    cache, K, V = R.make_cache("bf16", 1, 1, 2, 64, 305, _gen(2))
+    q = torch.ones(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    want = _attend(cache, s, e, q, 0.125)
+    out = torch.zeros_like(q)
+    n = dv.dv_attention_workspace(cache, s, e, 2)
+    ws = torch.empty(max(1, n), dtype=torch.uint8, device="cuda")
+    dv.dv_attention_check()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        dv.dv_tree_attention(cache, 0, s, e, q, out, 0.125, ws)
+        with pytest.raises(dv.DvError) as ei:
+            dv.dv_attention_check(side)
+        assert ei.value.status == dv.DV_ERR_INVALID_ARG
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    dv.dv_attention_check()
