@@ -239,9 +239,10 @@ def _ranges(seq_start, seq_end, batch):
 class Cache:
     """Geometry plus K/V base addresses of one cache (layout in ``dv.h``).
 
-    ``k`` and ``v`` are device tensors (any dtype; only their addresses are
-    used) or raw addresses.  ``layer_stride_elems`` 0 means layers are packed
-    densely."""
+    ``k`` and ``v`` are device tensors or raw addresses.  The copies use their
+    addresses alone, whatever their dtype; the operators over the cache take
+    tokens of another floating dtype than theirs for a mistake.
+    ``layer_stride_elems`` 0 means layers are packed densely."""
 
     def __init__(self, num_layers, batch, num_heads, head_dim, max_seq, elem_bytes, k, v,
                  layer_stride_elems=0):
@@ -249,6 +250,9 @@ class Cache:
             if hasattr(t, "is_contiguous") and not t.is_contiguous():
                 raise TypeError("K and V tensors must be contiguous (the layout is by address)")
         self.k, self.v = k, v  # keep the tensors alive
+        # what the tensors say their elements are, where it can be (not e.g. bytes)
+        self.float_dtypes = {t.dtype for t in (k, v) if getattr(getattr(t, "dtype", None), "is_floating_point", False)
+                             and t.element_size() == elem_bytes}
         kp = k.data_ptr() if hasattr(k, "data_ptr") else int(k)
         vp = v.data_ptr() if hasattr(v, "data_ptr") else int(v)
         self.c = dv_cache(num_layers, batch, num_heads, head_dim, max_seq, elem_bytes,
@@ -762,6 +766,12 @@ def _dtype(t):
     return d
 
 
+def _same_dtype(cache, dtype):
+    for d in cache.float_dtypes:
+        if d != dtype:
+            raise TypeError(f"the cache's tensors are {d}, the tokens {dtype}")
+
+
 def _empty_on(t, raw):
     """An uninitialised tensor like ``t`` whose memory belongs to the stream
     ``raw``: torch reuses a tensor's memory in the order of the stream that it
@@ -835,6 +845,7 @@ def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=No
     c, raw = cache.c, _stream(stream)
     s, e, sp, ep = _ranges(seq_start, seq_end, c.batch)
     n, D, dtype = k.shape[0], c.head_dim, k.dtype
+    _same_dtype(cache, dtype)
     shape = (n, c.num_heads, D)
     kp, ks = _token_rows(k, "k", shape, dtype)
     vp, vs = _token_rows(v, "v", shape, dtype)
@@ -867,6 +878,7 @@ def _queries(cache, q, out, scale):
         raise ValueError(f"q must be [tokens, q_heads, {cache.c.head_dim}] (got {list(q.shape)})")
     n, heads, _ = q.shape
     shape, dtype = (n, heads, cache.c.head_dim), q.dtype
+    _same_dtype(cache, dtype)
     qp, qs = _token_rows(q, "q", shape, dtype)
     op, os_ = _token_rows(out, "out", shape, dtype)
     return n, dv_queries(_dtype(q), heads, n, qp, qs, op, os_, scale)

@@ -131,3 +131,35 @@ def test_tries_of_a_wait_are_at_most_the_regular_number():
     _refused(dv.DV_ERR_INVALID_ARG, "tries", lambda: dv.dv_debug_attention_tries((1 << 22) + 1))
     dv.dv_debug_attention_tries(1 << 22)
     dv.dv_debug_attention_tries(-5)
+
+
+# ---- element types -----------------------------------------------------------------------
+
+def _ops(cache, dt):
+    s, e = np.array([8], np.int32), np.array([16], np.int32)
+    k, q, o = (torch.zeros(8, 1, 64, dtype=dt) for _ in range(3))
+    return [lambda: dv.dv_kv_append(cache, 0, s, e, k, k, q=q, q_out=o, stream=0),
+            lambda: dv.dv_prompt_attention(cache, 0, s, e, q, o, 0.125, None, stream=0),
+            lambda: dv.dv_tree_attention(cache, 0, s, e, q, o, 0.125, None, stream=0)]
+
+
+@pytest.mark.parametrize("op", range(3))
+@pytest.mark.parametrize("held, given", [(torch.float16, torch.bfloat16), (torch.bfloat16, torch.float16)])
+@pytest.mark.parametrize("which", ["K", "V", "both"])
+def test_tokens_of_another_float_type_than_the_caches_are_refused(op, held, given, which):
+    K, V = (torch.zeros(64 * 64, dtype=held if which in (n, "both") else given) for n in "KV")
+    with pytest.raises(TypeError, match="the cache's tensors are"):
+        _ops(dv.Cache(1, 1, 1, 64, 64, 2, K, V), given)[op]()
+
+
+@pytest.mark.parametrize("op", range(3))
+@pytest.mark.parametrize("kind", ["same", "bytes", "int16", "float32", "addresses"])
+def test_caches_of_other_words_take_either_type(op, kind):
+    """Memory whose dtype says nothing of its elements (the call goes on to the pointers)."""
+    for dt in (torch.float16, torch.bfloat16):
+        n = {"bytes": (torch.uint8, 2), "int16": (torch.int16, 1), "float32": (torch.float32, 1)}.get(kind, (dt, 1))
+        K, V = (torch.zeros(64 * 64 * n[1], dtype=n[0]) for _ in "KV")
+        if kind == "addresses":
+            K, V = 0x10000000, 0x20000000
+        with pytest.raises(dv.DvError):
+            _ops(dv.Cache(1, 1, 1, 64, 64, 2, K, V), dt)[op]()
