@@ -616,19 +616,25 @@ typedef enum {
   DV_ROPE_NONE = 0,   /* f_i = base^(-2i/rot_dim) */
   DV_ROPE_LINEAR = 1, /* f_i / factor (position interpolation) */
   DV_ROPE_NTK = 2,    /* base * factor^(rot_dim/(rot_dim-2)) in place of base */
-  DV_ROPE_PARTS = 3   /* by parts (YaRN): with r_i = original_max * f_i / 2 pi turns over the
+  DV_ROPE_PARTS = 3   /* by parts: with r_i = original_max * f_i / 2 pi turns over the
                          trained context and g = clamp((r_i - 1) / 31, 0, 1), g f_i +
-                         (1 - g) f_i / factor; rotated values times 0.1 ln(factor) + 1 */
+                         (1 - g) f_i / factor; rotated values times 0.1 ln(factor) + 1.
+                         This is YaRN's equation as its paper has it.  Models are also run
+                         with a g that is linear in the pair's index i between two rounded
+                         border indices, or with other borders than 1 and 32 turns or another
+                         factor on the values: their frequencies differ (by more than half
+                         for the middle pairs) and are to be given as they are, see dv_rope */
 } dv_rope_scaling;
 
-/* A rotation, filled by dv_rope_init and owned by the caller (plain data; it
- * may be copied).  turn[i] is pair i's frequency in turns per position as a
- * 64-bit binary fraction: position * turn[i] modulo 2^64 is the angle, exact
- * for any int32 position. */
+/* A rotation, owned by the caller (plain data; it may be copied) and filled by
+ * dv_rope_init, or by the caller with any frequencies: turn[i] is pair i's
+ * frequency f_i (radians a position) in turns per position as a 64-bit binary
+ * fraction, f_i / 2 pi * 2^64 modulo 2^64; position * turn[i] modulo 2^64 is the
+ * angle, exact for any int32 position. */
 typedef struct {
   int32_t rot_dim;     /* rotated elements, the first of each head; the rest pass through */
   int32_t interleaved; /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i+1) */
-  float value_factor;  /* on cos and sin */
+  float value_factor;  /* on cos and sin; finite */
   int32_t reserved;
   uint64_t turn[DV_MAX_ROT / 2];
 } dv_rope;

@@ -363,6 +363,8 @@ extern "C" dv_status dv_kv_append(const dv_cache* cache, int32_t layer, const in
       return fail(DV_ERR_INVALID_ARG, "rot_dim %d does not fit head_dim %d", t.rope->rot_dim, p.D);
     if (t.rope->interleaved != 0 && t.rope->interleaved != 1)
       return fail(DV_ERR_INVALID_ARG, "rope.interleaved is %d", t.rope->interleaved);
+    if (!std::isfinite(t.rope->value_factor))
+      return fail(DV_ERR_INVALID_ARG, "rope.value_factor is %g", (double)t.rope->value_factor);
   }
   if (t.tokens != p.tokens)
     return fail(DV_ERR_INVALID_ARG, "the buffers hold %lld tokens, the ranges %lld",

@@ -10,6 +10,7 @@ A status other than DV_OK raises ``DvError`` with the library's message.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from pathlib import Path
 
@@ -825,7 +826,9 @@ class Rope:
     """A rotation for ``dv_kv_append``: the first ``rot_dim`` elements of a
     head, in pairs (i, i + rot_dim/2) or, ``interleaved``, (2i, 2i+1).
     ``scaling``: "none", "linear", "ntk" or "parts", by ``factor``
-    (``original_max``: the trained context, for "parts")."""
+    (``original_max``: the trained context, for "parts").  A model whose
+    frequencies are none of these (``dv_rope_scaling`` in ``dv.h`` has the
+    formulas) gives them to ``from_frequencies``."""
 
     def __init__(self, rot_dim, interleaved=False, base=10000.0, scaling="none", factor=1.0,
                  original_max=0):
@@ -833,6 +836,20 @@ class Rope:
             raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)} (got {scaling!r})")
         self.c = dv_rope_init(rot_dim, interleaved, base, _ROPE_SCALING[scaling], factor,
                               original_max)
+
+    @classmethod
+    def from_frequencies(cls, frequencies, interleaved=False, value_factor=1.0):
+        """A rotation by ``frequencies`` (radians a position, one for each rotated
+        pair) with ``value_factor`` on the rotated values."""
+        f = np.asarray(frequencies, dtype=np.float64).reshape(-1)
+        if not 1 <= f.size <= DV_MAX_ROT // 2:
+            raise ValueError(f"1 to {DV_MAX_ROT // 2} frequencies are needed (got {f.size})")
+        if not np.isfinite(f).all():
+            raise ValueError("the frequencies must be finite")
+        turns = [int(math.ldexp(x / (2 * math.pi), 64)) % (1 << 64) for x in f.tolist()]
+        self = cls.__new__(cls)
+        self.c = dv_rope(2 * f.size, int(interleaved), value_factor, 0, (ctypes.c_uint64 * (DV_MAX_ROT // 2))(*turns))
+        return self
 
 
 def dv_kv_append(cache: Cache, layer, seq_start, seq_end, k, v, q=None, q_out=None, rope=None,
