@@ -279,3 +279,59 @@ def test_the_check_is_refused_in_a_capture_and_leaves_it_whole():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     dv.dv_attention_check()
+
+
+# ---- offsets past 32 bits ----------------------------------------------------------------
+
+def test_chunk_offsets_past_32_bits():
+    """One layer of more than 2^31 16-byte chunks: the last heads' rows lie past
+    what a 32-bit chunk index reaches, in full tiles and in a partial one, with
+    values of their own in every head and a non-finite one among the last's."""
+    H, G, D, S, ctx, n = 131, 2, 128, (1 << 20) + 37, 295, 6
+    need = H * D * S * 2
+    if torch.cuda.mem_get_info()[0] < 2 * need + (8 << 30):
+        pytest.skip("needs 80 GB of free device memory")
+    assert (H - 1) * (D // 8) * S > 1 << 31
+    gen = _gen(8)
+    k, v = (torch.empty(H * D * S, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache = dv.Cache(1, 1, H, D, S, 2, k, v)
+    K, V = k.view(1, 1, H, D // 8, S, 8), v.view(1, 1, H, S, D)
+    end = ctx + n
+    K[0, 0, :, :, :end + 9].normal_(generator=gen)
+    V[0, 0, :, :end + 9].normal_(generator=gen)
+    K[0, 0, :, :, S - 9:], V[0, 0, :, S - 9:] = 3.0, 4.0
+    new = torch.empty(n, (G + 2) * H, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    s, e = np.array([ctx], np.int32), np.array([end], np.int32)
+    before = K[0, 0, :, :, :end + 9].clone(), V[0, 0, :, :end + 9].clone()
+    new[2, (G + 2) * H - 1, 7] = math.inf  # the last head's value of the third new token
+
+    # append, at the context's end and at the cache's
+    q = dv.dv_kv_append(cache, 0, s, e, new[:, G * H:(G + 1) * H], new[:, (G + 1) * H:], q=new[:, :G * H])
+    assert torch.equal(q, new[:, :G * H])
+    dv.dv_kv_append(cache, 0, np.array([S - n], np.int32), np.array([S], np.int32), new[:, G * H:(G + 1) * H],
+                    new[:, (G + 1) * H:])
+    for at in (ctx, S - n):
+        assert torch.equal(K[0, 0, :, :, at:at + n].permute(2, 0, 1, 3).reshape(n, H, D), new[:, G * H:(G + 1) * H])
+        assert torch.equal(V[0, 0, :, at:at + n].transpose(0, 1), new[:, (G + 1) * H:])
+    for now, was, dim in ((K[0, 0], before[0], 2), (V[0, 0], before[1], 1)):
+        assert torch.equal(now.narrow(dim, 0, ctx), was.narrow(dim, 0, ctx))
+        assert torch.equal(now.narrow(dim, end, 9), was.narrow(dim, end, 9))
+    assert (K[0, 0, :, :, S - 9:S - n] == 3).all() and (V[0, 0, :, S - 9:S - n] == 4).all()
+
+    # attention: two full tiles and a partial one of every head
+    want, tol = R.attention_ref(K[0], V[0], s, e, q, D ** -0.5)
+    assert torch.isinf(want[2:, (H - 1) * G:, 7]).all() and torch.isfinite(want[:2]).all()
+    R.assert_within(_attend(cache, s, e, q, D ** -0.5), want, tol)
+    R.assert_within(_attend(cache, s, e, q, D ** -0.5, prompt=True), want, tol)
+
+    # compact, at both ends
+    for at in (ctx, S - n):
+        rows = K[0, 0, :, :, at:at + n].clone(), V[0, 0, :, at:at + n].clone()
+        keep = torch.tensor([at + 1, at + 3, at + 5], dtype=torch.int32, device="cuda")
+        dv.dv_kv_compact(cache, 0, 1, np.array([at], np.int32), np.array([at + 3], np.int32), keep)
+        assert torch.equal(K[0, 0, :, :, at:at + 3], rows[0][:, :, [1, 3, 5]])
+        assert torch.equal(V[0, 0, :, at:at + 3], rows[1][:, [1, 3, 5]])
+        assert torch.equal(K[0, 0, :, :, at + 3:at + n], rows[0][:, :, 3:])
+        assert torch.equal(V[0, 0, :, at + 3:at + n], rows[1][:, 3:])
+    del k, v, K, V, cache
+    torch.cuda.empty_cache()
