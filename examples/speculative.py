@@ -4,7 +4,7 @@
 
 A few random decoder layers with grouped query heads run from prompt to generated
 tokens on the library's operators alone: every layer appends its new tokens to the
-cache (rotary positions), attends it, and is streamed to a host replica. Each step
+cache (rotary positions) and attends it; the prompts' rows go to a host replica. Each step
 drafts a small tree of tokens per sequence from what followed the last token before,
 checks the whole tree in one pass (tree attention), keeps the longest path that the
 model itself would have taken, moves that path's rows together (compact) and appends
@@ -36,7 +36,7 @@ class Model:
         self.v = torch.zeros_like(self.k)
         self.cache = dv.Cache(L, B, H, D, S, 2, self.k, self.v)
 
-    def forward(self, tokens, s, e, tree=None, positions=None, prompt=False, after_layer=None):
+    def forward(self, tokens, s, e, tree=None, positions=None, prompt=False):
         """Logits of the packed new tokens, which take rows [s, e) of the cache."""
         x = self.embed[tokens]
         n, hq = len(tokens), H * G
@@ -50,8 +50,6 @@ class Model:
                 dv.dv_prompt_attention(self.cache, l, s, e, q, o, D ** -0.5, ws)
             else:
                 dv.dv_tree_attention(self.cache, l, s, e, q, o, D ** -0.5, ws, tree=tree)
-            if after_layer:
-                after_layer(l)
             x = x + o.view(n, -1) @ self.out[l]
         return torch.nn.functional.layer_norm(x.float(), x.shape[1:]) @ self.head.float()
 
