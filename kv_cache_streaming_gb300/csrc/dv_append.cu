@@ -44,7 +44,7 @@ struct AppendParams {
   const int32_t* positions;
   int64_t q_stride, k_stride, v_stride, q_out_stride;
   int32_t Hq, H, D, C, S;
-  int32_t rot, half, interleaved;  // rot 0: nothing is rotated; half = rot / 2
+  int32_t rot, half;  // rot 0: nothing is rotated; half = rot / 2
   float factor;
   uint64_t turn[DV_MAX_ROT / 2];
   SeqTable<MAXB> seq;
@@ -266,7 +266,6 @@ cudaError_t launch_append(const Plan& p, const dv_new_tokens& t, cudaStream_t st
   kp.S = p.S;
   kp.rot = t.rope ? t.rope->rot_dim : 0;
   kp.half = kp.rot / 2;
-  kp.interleaved = t.rope ? t.rope->interleaved : 0;
   kp.factor = t.rope ? t.rope->value_factor : 1.f;
   for (int i = 0; i < kp.half; ++i) kp.turn[i] = t.rope->turn[i];
   fill_table(p, &kp.seq);
