@@ -161,7 +161,7 @@ const char* dv_last_error(void);
 
 /* Debugging.  A checked build of the library (built with DV_CHECKED=1, file
  * libdv_checked.so) checks every global access of its copy kernels (pack,
- * unpack, restore; not the attention operators below) against the
+ * unpack, restore; not the operators over the cache below) against the
  * extents the host validated; an access outside them is skipped and the
  * first one is recorded (nothing traps).  dv_debug_fault waits for the device,
  * returns that record in *fault (0: none; else bit 63 set, bits 56..62 the

@@ -6,7 +6,7 @@
 // f_i is held in turns per position as a 64-bit binary fraction, so that
 // position * f_i mod 1 is one integer product, exact at any position; the top
 // 32 bits of it, as a signed fraction of half a turn, go to sincospi.  (A
-// float product of a position near 10^6 and f_0 = 1 would be 0.06 rad off.)
+// float product would round an angle near 10^6 by up to 0.03 rad.)
 //
 // Memory bound: every value is read once and written once (the half layout's
 // partner chunk comes from L1).  Two kernels:
@@ -30,7 +30,10 @@ constexpr int kAppendThreads = 128;
 constexpr int kTileRows = 4;    // cache rows of a warp in the tile kernel
 constexpr int kTileChunks = 8;  // and 16-byte chunks of them
 // Ranges of fewer tokens than this on average go to the token kernel: the
-// tile kernel's lanes are tied to 4 rows, so shorter ranges leave most idle.
+// tile kernel's lanes are tied to 4 rows, so shorter ranges leave most idle (32 ranges
+// of 1 / 3 tokens, 40 heads of 128: 5.4 / 5.9 us there, 2.7 / 4.6 in the token kernel).  By the
+// call's tokens the crossover lies higher: 8 to 17 tokens a range there (7.4 and 6.9
+// at 8; 12.2 and 12.6 at 17; 31.3 and 35.2 at 64), past 64 with 4 ranges (6.8 and 6.7).
 constexpr int kTileMinMean = 4;
 
 template <int MAXB>

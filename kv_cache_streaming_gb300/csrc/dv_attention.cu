@@ -20,9 +20,15 @@
 //   SPLIT  one row tile, the even K/V tiles on one chain and the odd ones on
 //          the other, joined at the end: decode steps and small trees, bound
 //          by reading K and V once.
-// PAIR where some sequence has more rows than a row tile, SPLIT otherwise.  P is
-// handed over in two halves, so that the products with V start under the second
-// half's exponentials.
+// PAIR where some sequence has more rows than a row tile, SPLIT otherwise, one
+// form for a call.  PAIR and SPLIT, us: 8 prompts of 1000, 25 heads of 64, 51 and
+// 65, of 129 to 384 within 6% either way; 32 prompts of 256, 40 heads of 128, 67
+// and 73, of 1000 339 and 456; 2 x 64 nodes after 131000, 64 query heads on 8,
+// 362 and 587.  PAIR runs a sequence of one row tile on one chain: a chunk of
+// 2048 with 31 single tokens after 500 to 8000 rows takes 163 where SPLIT takes
+// 140, 8 x 64 nodes after 2000 rows 50 and 45.
+// P is handed over in two halves, so that the products with V start under the
+// second half's exponentials.
 //
 // Warps: 0-3 and 4-7 the chains' softmax, 8 loads (and walks over the units,
 // publishing each in a ring), 9 and 10 issue the chains' products, 11 looks
@@ -47,16 +53,17 @@
 // the CTA then drains its copies and products, each with a bounded wait too, frees its tensor
 // memory and returns, and dv_attention_check reports it.
 //
-// Measured (bf16, heads of 128 unless said).  SPLIT is bound by HBM: a decode
-// step of 32 sequences of 64 to 1791 rows, 112 heads (1.52 GB) 232 us, 6.5 TB/s.
+// Measured (bf16, heads of 128 unless said; in a long loop, where the power cap
+// counts).  SPLIT is bound by HBM: a decode step of 32 sequences of 64 to 1791
+// rows, 112 heads (1.52 GB) 230 to 232 us, 6.5 to 6.6 TB/s.
 // PAIR is bound by the chain scores - softmax - products of a tile, about 3100
 // cycles for a pair of tiles whose products take 2048 on the tensor cores: 4096
-// tokens after 28672, 64 query heads on 8, 2.6 ms, 1.55 to 1.6 PFLOP/s; on
-// short prompts the filling and draining of the chains come on top, and the
-// half of the diagonal tiles that is hidden: 32 prompts of 64 to 1536 tokens,
-// 112 heads, 0.80 to 0.82 ms, 0.88 to 0.91 PFLOP/s attended.
+// tokens after 28672, 64 query heads on 8, 2.72 to 2.74 ms, 1.5 PFLOP/s (2.63 to
+// 2.68 alone); on short prompts the filling and draining of the chains come on
+// top, and the half of the diagonal tiles that is hidden: 32 prompts of 64 to 1536
+// tokens, 112 heads, 0.85 ms, 0.85 PFLOP/s attended.
 // Heads of 64 halve the products but not the softmax: 8 prompts of 1000, 25
-// heads (fp16), 53 us.  What was tried and was slower: S in halves of 64
+// heads (fp16), 54 us.  What was tried and was slower: S in halves of 64
 // columns two steps ahead; two buffers of 96 columns for heads of 64; the
 // maximum from a second pass over S, or only when a sum grows too large (7 to
 // 10% each); one product warp for both chains (28% on ragged prompts); the next
@@ -148,7 +155,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // Waits, as a whole warp, for the phase of `parity` to complete; false when it gave up after
 // `tries`.  The vote makes it one answer for the warp's lanes, which go on to instructions
 // that need all of them: a phase may complete between one lane's last try and another's.
-// (It costs about 1% on short prompts and trees.)  Kept short: it stands at some thirty
+// (It costs 1 to 2% on short and ragged prompts, less on trees.)  Kept short: it stands at some thirty
 // places, and the kernel's speed hangs on its size (an instruction cache miss in every loop
 // made ragged prompts twice as slow).
 __device__ __forceinline__ bool gave_up() {
@@ -1279,8 +1286,9 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, bool is_tree, con
   const cuuint64_t vs[2] = {D * 2, D * 2 * p.S};
   const cuuint32_t vb[3] = {64, kTile, 1}, vp[3] = {64, 32, 1};
   // A chunk row's S rows of 16 bytes are one run, so the copy's innermost run may be several
-  // rows: as many as divide S, up to the 256 elements a box may have.  (Rows one by one, for an
-  // odd S, make 8 times as many 16-byte pieces of a tile.)
+  // rows: as many as divide S, up to the 256 elements a box may have: 512 bytes where 32 divide
+  // it, 16 for an odd S.  (2048 tokens after 14336, 64 query heads on 8, with S a multiple of 32,
+  // of 8, of 2, odd: 616, 617, 631, 661 us; a decode step of 16 x 16384 rows: 155, 156, 161, 185.)
   int w = 32;
   while (p.S % w != 0) w /= 2;
   kp.k_rows = w;

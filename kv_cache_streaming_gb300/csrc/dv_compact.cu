@@ -109,7 +109,8 @@ cudaError_t launch_compact(const Plan& p, const int32_t* keep, cudaStream_t stre
   kp.units = rows * kp.slices;
   const int64_t ctas = (kp.units + kCompactThreads / 32 - 1) / (kCompactThreads / 32);
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  // Few rows (an accepted path): a quarter of the registers, so that more warps are resident.
+  // Few rows (an accepted path): a quarter of the registers, so that more warps are resident
+  // (paths of 4 to 8 rows in 8 layers x 8 x 40 heads of 128: 6.3 us, 9.4 with 16 cells a lane).
   if ((int64_t)p.max_len * slice <= 4 * 32)
     return ops_launch(compact_kernel<4, MAXB>, dim3((unsigned)ctas), kCompactThreads, 0, stream,
                       kp);
