@@ -725,6 +725,17 @@ dv_status dv_tree_attention(const dv_cache* cache, int32_t layer, const int32_t*
                             const uint64_t* tree, void* workspace, size_t workspace_bytes,
                             dv_stream stream);
 
+/* As dv_prompt_attention, of prompts and of decode steps alike, through a window: the token
+ * at row r attends the rows j <= r with j > r - window or j < sinks, the last `window` rows up
+ * to its own and the first `sinks` of the sequence (which stay visible: "attention sinks"; 0:
+ * none).  Rows that no token attends are not read, and have no effect.  `workspace` and its size
+ * as for dv_prompt_attention.  window >= 1, sinks >= 0 (else DV_ERR_INVALID_ARG); a window of
+ * max_seq rows or more is plain causal attention. */
+dv_status dv_window_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
+                              const int32_t* seq_end, const dv_queries* queries, int32_t window,
+                              int32_t sinks, void* workspace, size_t workspace_bytes,
+                              dv_stream stream);
+
 /* Waits for `stream` and reports whether a wait inside an attention kernel on
  * this device has given up since the last check on this stream (its first: since the
  * library was loaded): DV_ERR_TIMEOUT, else DV_OK.  Every stream that is checked is

@@ -1,5 +1,5 @@
 // Internal to libdv: what the operators over the cache (dv_append.cu,
-// dv_compact.cu, dv_attention.cu) share: argument checks, the tables of the
+// dv_compact.cu, dv_attention.cuh and its forms) share: argument checks, the tables of the
 // packed token ranges that kernels take by value, and small device helpers.
 #pragma once
 
@@ -159,5 +159,11 @@ inline bool overlaps_layers(const Plan& p, const void* a, size_t n) {
   }
   return false;
 }
+
+// What the attention forms' translation units share: the tries of a wait, and where each one's
+// kernels count the waits that gave up (on the current device).
+uint32_t attention_tries();
+cudaError_t plain_waits(void** address);
+cudaError_t window_waits(void** address);
 
 }  // namespace dv

@@ -1,0 +1,27 @@
+// dv_window_attention: causal attention in which a token attends the last rows up to its own
+// and a few first ones (the kernel: dv_attention.cuh, form kWindow).
+#include "dv_attention.cuh"
+
+namespace dv {
+
+cudaError_t window_waits(void** address) {
+  return cudaGetSymbolAddress(address, g_attention_gave_up);
+}
+
+}  // namespace dv
+
+extern "C" dv_status dv_window_attention(const dv_cache* cache, int32_t layer,
+                                         const int32_t* seq_start, const int32_t* seq_end,
+                                         const dv_queries* queries, int32_t window, int32_t sinks,
+                                         void* workspace, size_t workspace_bytes,
+                                         dv_stream stream) {
+  dv::Trace trace("dv_window_attention");
+  if (!cache) return dv::fail(DV_ERR_INVALID_ARG, "cache is NULL");
+  if (window < 1 || sinks < 0)
+    return dv::fail(DV_ERR_INVALID_ARG, "a window of %d rows and %d first ones", window, sinks);
+  dv::Extra x;  // (more rows than there are: all of them)
+  x.window = window < cache->max_seq ? window : cache->max_seq;
+  x.sinks = sinks < cache->max_seq ? sinks : cache->max_seq;
+  return dv::attention<dv::kWindow>(cache, layer, seq_start, seq_end, queries, x, workspace,
+                                    workspace_bytes, stream);
+}

@@ -135,6 +135,8 @@ _prompt_attention = _sig("dv_prompt_attention", [_CP, _I32, _I32P, _I32P,
                                                  ctypes.POINTER(dv_queries), _P, _SZ, _P])
 _tree_attention = _sig("dv_tree_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
                                              _P, _P, _SZ, _P])
+_window_attention = _sig("dv_window_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
+                                                 _I32, _I32, _P, _SZ, _P])
 _attention_check = _sig("dv_attention_check", [_P])
 _attention_tries = _sig("dv_debug_attention_tries", [_I32])
 _compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _I64, _P])
@@ -922,6 +924,25 @@ def dv_tree_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, wo
     w, wn = _buf(workspace)
     t = None if tree is None else _words_of(tree, "tree", n, 8)
     _check(_tree_attention(cache.ref, layer, sp, ep, ctypes.byref(a), t, w, wn, _stream(stream)))
+
+
+def _int32(x, name):
+    """``x`` as it is, where 32 bits hold it (ctypes would take it modulo 2^32)."""
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name}: 32 bits do not hold {x}")
+    return x
+
+
+def dv_window_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, window, sinks=0,
+                        workspace=None, stream=None) -> None:
+    """Causal attention in which the token at row r attends the last ``window``
+    rows up to its own and the first ``sinks`` rows.  Everything else as
+    ``dv_prompt_attention``; serves decode steps too."""
+    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
+    _, a = _queries(cache, q, out, scale)
+    w, wn = _buf(workspace)
+    _check(_window_attention(cache.ref, layer, sp, ep, ctypes.byref(a), _int32(window, "window"),
+                             _int32(sinks, "sinks"), w, wn, _stream(stream)))
 
 
 def dv_attention_check(stream=None) -> None:
