@@ -736,6 +736,25 @@ dv_status dv_window_attention(const dv_cache* cache, int32_t layer, const int32_
                               int32_t sinks, void* workspace, size_t workspace_bytes,
                               dv_stream stream);
 
+/* As dv_prompt_attention, of prompts and of decode steps alike, and adds the weight that each
+ * cache row receives to `mass`, the layer's [batch][num_heads][max_seq] 32-bit floats (device
+ * memory, 4-byte aligned; on no other buffer of the call):
+ *   mass[b][h][j] += sum of w_j over the last `last` new tokens of sequence b (0: all of
+ *                    them) and the query heads of key head h.
+ * The weights added are not rounded to `dtype`.  Rows that no counted token attends keep their
+ * value, bit for bit.  A token whose weights are NaN (see dv_prompt_attention) makes the rows
+ * that it attends NaN.  The same call gives the same bits each time.  `workspace`: as for
+ * dv_prompt_attention, but of dv_scored_attention_workspace bytes.  last < 0 or mass NULL:
+ * DV_ERR_INVALID_ARG. */
+dv_status dv_scored_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
+                              const int32_t* seq_end, const dv_queries* queries, int32_t last,
+                              float* mass, void* workspace, size_t workspace_bytes,
+                              dv_stream stream);
+
+/* As dv_attention_workspace, for dv_scored_attention (any `last`). */
+dv_status dv_scored_attention_workspace(const dv_cache* cache, const int32_t* seq_start,
+                                        const int32_t* seq_end, int32_t q_heads, size_t* bytes);
+
 /* Waits for `stream` and reports whether a wait inside an attention kernel on
  * this device has given up since the last check on this stream (its first: since the
  * library was loaded): DV_ERR_TIMEOUT, else DV_OK.  Every stream that is checked is

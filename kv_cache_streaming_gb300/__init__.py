@@ -39,5 +39,6 @@ from .dv import (  # noqa: F401
     DV_DTYPE_FP16, DV_DTYPE_BF16, DV_MAX_ROT, DV_MAX_TREE, DV_MAX_GROUP,
     DV_ROPE_NONE, DV_ROPE_LINEAR, DV_ROPE_NTK, DV_ROPE_PARTS,
     Rope, dv_rope, dv_rope_init, dv_kv_append, dv_attention_workspace, dv_prompt_attention,
-    dv_tree_attention, dv_window_attention, dv_attention_check, dv_debug_attention_tries, dv_kv_compact,
+    dv_tree_attention, dv_window_attention, dv_scored_attention,
+    dv_scored_attention_workspace, dv_attention_check, dv_debug_attention_tries, dv_kv_compact,
 )

@@ -85,7 +85,7 @@ extern "C" dv_status dv_attention_check(dv_stream stream) {
                     "captured into a graph");
   // one count for each form's translation unit
   using Counter = cudaError_t (*)(void**);
-  constexpr Counter counters[] = {dv::plain_waits, dv::window_waits};
+  constexpr Counter counters[] = {dv::plain_waits, dv::window_waits, dv::scored_waits};
   constexpr int n = sizeof(counters) / sizeof(counters[0]);
   unsigned long long id = 0, context = 0, counts[n] = {}, count = 0;
   if (err == cudaSuccess) err = cudaStreamGetId(stream, &id);

@@ -143,6 +143,13 @@ template <int MAXB>
 struct AttnParams<MAXB, kWindow> : AttnBase<MAXB> {
   int32_t window, sinks;  // a token at row r attends rows (r - window, r] and [0, sinks)
 };
+template <int MAXB>
+struct AttnParams<MAXB, kScored> : AttnBase<MAXB> {
+  float* lse;     // [H][T][G]: log2 of each row's sum of exp2(c s)
+  float* scores;  // SPLIT, or NULL: of (b, query head, token, tile) 128 scores each
+  int32_t tokens;  // T
+  int32_t block_pre[MAXB + 1];  // (token, tile) pairs of the sequences before
+};
 
 // ---- instructions --------------------------------------------------------------
 
@@ -1047,6 +1054,16 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
               }
             }
           };
+          if constexpr (FORM == kScored && !PAIR) {
+            if (p.scores != nullptr && valid) {
+              const int tiles = (it.row_end + kTile - 1) / kTile;
+              float* const d =
+                  p.scores + kTile * ((int64_t)p.block_pre[it.b] * (p.H * p.G) +
+                                      ((int64_t)(it.h * p.G + g) * it.n_tok + tok) * tiles + tile);
+#pragma unroll
+              for (int k = 0; k < kTile; k += 8) st32(d + k, x + k);
+            }
+          }
           move_max(row_max());
           if (PAIR && r == 0) ctl.turn[i] = (int)s_count;
           l += half_row(0);
@@ -1097,6 +1114,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                               (int64_t)(it.h * p.G + g) * p.D;
         if (!whole && valid && (PAIR || i == 0))
           reinterpret_cast<float2*>(part + kRows * p.D)[prow] = make_float2(m * p.c, l);
+        if constexpr (FORM == kScored)
+          if (whole && valid && (PAIR || i == 0))
+            p.lse[((int64_t)it.h * p.tokens + it.tok_at + tok) * p.G + g] =
+                m * p.c + log2f(l) - (std::is_same<T, __half>::value ? kHalfUp : 0.f);
 #pragma unroll 1
         for (int k = c0; k < c0 + kCols; k += 32) {
           if (k >= p.D) break;
@@ -1211,6 +1232,8 @@ struct JoinParams {
   const Divided* divided;
   int64_t out_stride;
   int32_t G, D, tile_tok, rows;  // rows: of a piece's slot
+  float* lse;      // kScored, as in AttnParams
+  int32_t tokens;
 };
 
 // Adds up the pieces of the unit that the cut after CTA blockIdx.x is the
@@ -1218,7 +1241,7 @@ struct JoinParams {
 //   out = sum_i f_i O_i / sum_i f_i l_i,  f_i = exp2(m_i - max m).
 // Bound by latency (a launch of a few microseconds): a thread per 4 output
 // values, with no load waiting for another but for the unit's description.
-template <typename T>
+template <typename T, int FORM>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constant__ JoinParams p) {
   ops_pdl_enter();
   const int i0 = blockIdx.x;
@@ -1266,6 +1289,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constan
     // Some row is attended (a token that attends none has at most 64 rows, one tile, which no
     // cut divides): l = 0 means scores of -inf alone, NaN.
     const float inv = 1.f / l;
+    if constexpr (FORM == kScored)
+      if (c == 0)
+        p.lse[((int64_t)(d.head / p.G) * p.tokens + d.tok + tok) * p.G + g] =
+            m + log2f(l) - (std::is_same<T, __half>::value ? kHalfUp : 0.f);
     uint16_t* const out =
         p.out + (int64_t)(d.tok + tok) * p.out_stride + (int64_t)(d.head + g) * p.D;
     reinterpret_cast<uint2*>(out)[c] =
@@ -1291,6 +1318,9 @@ struct Extra {
   bool is_tree = false;
   const uint64_t* tree = nullptr;  // or NULL
   int32_t window = 0, sinks = 0;   // kWindow
+  float* mass = nullptr;           // kScored: the layer's
+  float* lse = nullptr;            // from the workspace
+  float* scores = nullptr;
 };
 
 inline int sm_count() {
@@ -1323,6 +1353,21 @@ inline int k_run(const Plan& p) {
   int w = 32;
   while (p.S % w != 0) w /= 2;
   return w;
+}
+
+// Bytes of a layer's accumulated weights.
+inline size_t mass_bytes(const Plan& p) { return (size_t)p.B * p.H * p.S * sizeof(float); }
+
+// Blocks of a tile's scores before each sequence, for each query head; gives their number.
+inline int64_t score_blocks(const Plan& p, int32_t* pre) {
+  int64_t n = 0;
+  for (int b = 0; b < p.B; ++b) {
+    if (pre) pre[b] = (int32_t)n;
+    const int64_t rows = (int64_t)p.seq_start[b] + p.seq_len[b];
+    n += p.seq_len[b] * ((rows + kTile - 1) / kTile);
+  }
+  if (pre) pre[p.B] = (int32_t)n;
+  return n;
 }
 
 template <int FORM>
@@ -1378,6 +1423,28 @@ inline bool encode(CUtensorMap* map, bool fp16, int rank, const void* base, cons
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// {D, G, H, T} in boxes of 64 elements of a group's heads of a row tile's tokens.
+inline bool encode_q(CUtensorMap* map, const Plan& p, const dv_queries& q, int group,
+                     int tile_tok) {
+  const cuuint64_t D = (cuuint64_t)p.D;
+  const cuuint64_t dims[4] = {D, (cuuint64_t)group, (cuuint64_t)p.H, (cuuint64_t)p.tokens};
+  const cuuint64_t strides[3] = {
+      D * 2, D * 2 * group,
+      (cuuint64_t)(p.tokens > 1 ? q.q_stride : (int64_t)q.q_heads * p.D) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)tile_tok};
+  return encode(map, q.dtype == DV_DTYPE_FP16, 4, q.q, dims, strides, box, true);
+}
+// A layer's keys, in boxes of a tile's rows of a head.
+inline bool encode_k(CUtensorMap* map, const Plan& p, bool fp16, const void* k) {
+  const int w = k_run(p);
+  const cuuint64_t dims[4] = {8 * (cuuint64_t)w, (cuuint64_t)p.S / w, (cuuint64_t)p.C,
+                              (cuuint64_t)p.B * p.H};
+  const cuuint64_t strides[3] = {16 * (cuuint64_t)w, 16 * (cuuint64_t)p.S,
+                                 16 * (cuuint64_t)p.S * p.C};
+  const cuuint32_t box[4] = {8 * (cuuint32_t)w, (cuuint32_t)(kTile / w), (cuuint32_t)p.C, 1};
+  return encode(map, fp16, 4, k, dims, strides, box, false);
+}
+
 template <typename T, int DP, bool PAIR, int MAXB, int FORM>
 cudaError_t launch_kernel(const AttnParams<MAXB, FORM>& kp, int ctas, cudaStream_t stream) {
   void (*const kernel)(AttnParams<MAXB, FORM>) = attention_kernel<T, DP, PAIR, MAXB, FORM>;
@@ -1398,21 +1465,11 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, const Extra& x, f
   const void* k = static_cast<const uint4*>(p.k) + p.l0 * p.layer_chunks;
   const void* v = static_cast<const uint4*>(p.v) + p.l0 * p.layer_chunks;
   const cuuint64_t D = (cuuint64_t)p.D;
-  const cuuint64_t qd[4] = {D, (cuuint64_t)group, (cuuint64_t)p.H, (cuuint64_t)p.tokens};
-  const cuuint64_t qs[3] = {D * 2, D * 2 * group,
-                            (cuuint64_t)(p.tokens > 1 ? q.q_stride : (int64_t)q.q_heads * p.D) * 2};
-  const cuuint32_t qb[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)s.tile_tok};
   const cuuint64_t vd[3] = {D, (cuuint64_t)p.S, (cuuint64_t)p.B * p.H};
   const cuuint64_t vs[2] = {D * 2, D * 2 * p.S};
   const cuuint32_t vb[3] = {64, kTile, 1}, vp[3] = {64, 32, 1};
-  const int w = k_run(p);
-  kp.k_rows = w;
-  const cuuint64_t kd[4] = {8 * (cuuint64_t)w, (cuuint64_t)p.S / w, (cuuint64_t)p.C,
-                            (cuuint64_t)p.B * p.H};
-  const cuuint64_t ks[3] = {16 * (cuuint64_t)w, 16 * (cuuint64_t)p.S, 16 * (cuuint64_t)p.S * p.C};
-  const cuuint32_t kb[4] = {8 * (cuuint32_t)w, (cuuint32_t)(kTile / w), (cuuint32_t)p.C, 1};
-  if (!encode(&kp.q_map, fp16, 4, q.q, qd, qs, qb, true) ||
-      !encode(&kp.k_map, fp16, 4, k, kd, ks, kb, false) ||
+  kp.k_rows = k_run(p);
+  if (!encode_q(&kp.q_map, p, q, group, s.tile_tok) || !encode_k(&kp.k_map, p, fp16, k) ||
       !encode(&kp.v_map, fp16, 3, v, vd, vs, vb, true) ||
       !encode(&kp.v_part, fp16, 3, v, vd, vs, vp, true))
     return fail(DV_ERR_CUDA, "cuTensorMapEncodeTiled refused the queries or the cache");
@@ -1442,6 +1499,12 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, const Extra& x, f
     kp.window = x.window;
     kp.sinks = x.sinks;
   }
+  if constexpr (FORM == kScored) {
+    kp.lse = x.lse;
+    kp.scores = x.scores;
+    kp.tokens = (int32_t)p.tokens;
+    if (x.scores) score_blocks(p, kp.block_pre);
+  }
   cudaError_t err;
   if (p.D <= 64)
     err = s.pair ? launch_kernel<T, 64, true, MAXB, FORM>(kp, s.ctas, stream)
@@ -1460,8 +1523,10 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, const Extra& x, f
     jp.D = p.D;
     jp.tile_tok = s.tile_tok;
     jp.rows = (s.pair ? 2 : 1) * kTile;
+    jp.lse = x.lse;
+    jp.tokens = (int32_t)p.tokens;
     const int unit = (s.unit_tok < p.max_len ? s.unit_tok : p.max_len) * group * (p.D / 4);
-    err = ops_launch(join_kernel<T>, dim3((unsigned)s.ctas - 1, (unit + kJoinThreads - 1) / kJoinThreads),
+    err = ops_launch(join_kernel<T, FORM>, dim3((unsigned)s.ctas - 1, (unit + kJoinThreads - 1) / kJoinThreads),
                      kJoinThreads, 0, stream, jp);
     if (err != cudaSuccess) return cuda_fail(err, "attention join launch");
   }
@@ -1481,64 +1546,100 @@ inline dv_status check_heads(const dv_cache* cache, const Plan& p, int32_t q_hea
   return DV_OK;
 }
 
+// Checks a call and resolves its pointers: gives its plan, its queries and what else it has,
+// and where the workspace is (the pieces' sums first, then what `more_bytes` asks for).
+// Nothing to do: p->tokens = 0.
 template <int FORM>
-dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, const int32_t* e,
-                    const dv_queries* queries, Extra x, void* workspace, size_t workspace_bytes,
-                    cudaStream_t stream) {
+dv_status check_call(const dv_cache* cache, int32_t layer, const int32_t* s, const int32_t* e,
+                     const dv_queries* queries, Extra* x, void* workspace, size_t workspace_bytes,
+                     size_t (*more_bytes)(const Plan&, int group), Plan* p, dv_queries* q,
+                     uint8_t** ws) {
   if (!queries) return fail(DV_ERR_INVALID_ARG, "queries is NULL");
-  Plan p;
-  dv_status st = plan_layer(cache, layer, s, e, queries->dtype, &p);
+  dv_status st = plan_layer(cache, layer, s, e, queries->dtype, p);
   if (st != DV_OK) return st;
-  dv_queries q = *queries;
-  if ((st = check_heads(cache, p, q.q_heads)) != DV_OK) return st;
-  if (!(q.scale > 0.f) || !std::isfinite(q.scale))
-    return fail(DV_ERR_INVALID_ARG, "scale must be finite and positive (got %g)", (double)q.scale);
-  if (x.is_tree && p.max_len > DV_MAX_TREE)
-    return fail(DV_ERR_UNSUPPORTED, "%d drafted tokens of a sequence, more than %d", p.max_len,
+  *q = *queries;
+  if ((st = check_heads(cache, *p, q->q_heads)) != DV_OK) return st;
+  if (!(q->scale > 0.f) || !std::isfinite(q->scale))
+    return fail(DV_ERR_INVALID_ARG, "scale must be finite and positive (got %g)",
+                (double)q->scale);
+  if (x->is_tree && p->max_len > DV_MAX_TREE)
+    return fail(DV_ERR_UNSUPPORTED, "%d drafted tokens of a sequence, more than %d", p->max_len,
                 DV_MAX_TREE);
-  if (q.tokens != p.tokens)
+  if (q->tokens != p->tokens)
     return fail(DV_ERR_INVALID_ARG, "q and out hold %lld tokens, the ranges %lld",
-                (long long)q.tokens, (long long)p.tokens);
-  if (p.tokens == 0) return DV_OK;
-  const Schedule sch = schedule<FORM>(p, q.q_heads / p.H, x, nullptr);
-  const size_t need = sch.bytes;
+                (long long)q->tokens, (long long)p->tokens);
+  if (p->tokens == 0) return DV_OK;
+  const int group = q->q_heads / p->H;
+  const Schedule sch = schedule<FORM>(*p, group, *x, nullptr);
   if (sch.total > INT32_MAX)
     return fail(DV_ERR_UNSUPPORTED, "%lld tiles of attention in one call", (long long)sch.total);
+  const size_t need = sch.bytes + (more_bytes ? more_bytes(*p, group) : 0);
   if (workspace_bytes < need)
     return fail(DV_ERR_BUFFER_TOO_SMALL, "attention needs %zu workspace bytes (got %zu)", need,
                 workspace_bytes);
   // What the call writes (out and the workspace) shares no bytes with what it reads.
   size_t nq = 0, no = 0;
-  const size_t nt = (size_t)p.tokens * 8;
-  if ((st = span_rows(p, q.q_heads, q.q_stride, "q", &nq)) != DV_OK) return st;
-  if ((st = span_rows(p, q.q_heads, q.out_stride, "out", &no)) != DV_OK) return st;
-  if (overlap(q.out, no, q.q, nq) || overlap(q.out, no, x.tree, nt) || overlaps_layers(p, q.out, no))
+  const size_t nt = (size_t)p->tokens * 8;
+  if ((st = span_rows(*p, q->q_heads, q->q_stride, "q", &nq)) != DV_OK) return st;
+  if ((st = span_rows(*p, q->q_heads, q->out_stride, "out", &no)) != DV_OK) return st;
+  if (overlap(q->out, no, q->q, nq) || overlap(q->out, no, x->tree, nt) ||
+      overlaps_layers(*p, q->out, no))
     return fail(DV_ERR_INVALID_ARG, "out overlaps q, tree or the cache's layer");
   if (need > 0 &&
-      (overlap(workspace, need, q.q, nq) || overlap(workspace, need, q.out, no) ||
-       overlap(workspace, need, x.tree, nt) || overlaps_layers(p, workspace, need)))
+      (overlap(workspace, need, q->q, nq) || overlap(workspace, need, q->out, no) ||
+       overlap(workspace, need, x->tree, nt) || overlaps_layers(*p, workspace, need)))
     return fail(DV_ERR_INVALID_ARG, "workspace overlaps q, out, tree or the cache's layer");
-  if ((st = resolve_layers(&p)) != DV_OK) return st;
-  void* dev = nullptr;
-  if ((st = resolve_words(q.q, nq, 16, "q", &dev)) != DV_OK) return st;
-  q.q = dev;
-  if ((st = resolve_words(q.out, no, 16, "out", &dev)) != DV_OK) return st;
-  q.out = dev;
-  if (x.tree) {
-    if ((st = resolve_words(x.tree, nt, 8, "tree", &dev)) != DV_OK) return st;
-    x.tree = static_cast<const uint64_t*>(dev);
+  if constexpr (FORM == kScored) {
+    const size_t nm = mass_bytes(*p);
+    if (overlap(x->mass, nm, q->q, nq) || overlap(x->mass, nm, q->out, no) ||
+        overlap(x->mass, nm, workspace, need) || overlaps_layers(*p, x->mass, nm))
+      return fail(DV_ERR_INVALID_ARG, "mass overlaps q, out, workspace or the cache's layer");
   }
-  float* part = nullptr;
+  if ((st = resolve_layers(p)) != DV_OK) return st;
+  void* dev = nullptr;
+  if ((st = resolve_words(q->q, nq, 16, "q", &dev)) != DV_OK) return st;
+  q->q = dev;
+  if ((st = resolve_words(q->out, no, 16, "out", &dev)) != DV_OK) return st;
+  q->out = dev;
+  if (x->tree) {
+    if ((st = resolve_words(x->tree, nt, 8, "tree", &dev)) != DV_OK) return st;
+    x->tree = static_cast<const uint64_t*>(dev);
+  }
+  if constexpr (FORM == kScored) {
+    if ((st = resolve_words(x->mass, mass_bytes(*p), 4, "mass", &dev)) != DV_OK) return st;
+    x->mass = static_cast<float*>(dev);
+  }
+  *ws = nullptr;
   if (need > 0) {
     if ((st = resolve_words(workspace, need, 32, "workspace", &dev)) != DV_OK) return st;
-    part = static_cast<float*>(dev);
+    *ws = static_cast<uint8_t*>(dev);
   }
+  return DV_OK;
+}
+
+// Launches the kernel of a checked call.
+template <int FORM>
+dv_status run_call(const Plan& p, const dv_queries& q, const Extra& x, uint8_t* ws,
+                   cudaStream_t stream) {
+  float* const part = reinterpret_cast<float*>(ws);
   const bool small = p.B <= kSmallBatch;
   if (q.dtype == DV_DTYPE_FP16)
     return small ? launch_attention<__half, kSmallBatch, FORM>(p, q, x, part, stream)
                  : launch_attention<__half, kMaxBatch, FORM>(p, q, x, part, stream);
   return small ? launch_attention<__nv_bfloat16, kSmallBatch, FORM>(p, q, x, part, stream)
                : launch_attention<__nv_bfloat16, kMaxBatch, FORM>(p, q, x, part, stream);
+}
+
+template <int FORM>
+dv_status attention(const dv_cache* cache, int32_t layer, const int32_t* s, const int32_t* e,
+                    const dv_queries* queries, Extra x, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
+  Plan p;
+  dv_queries q;
+  uint8_t* ws = nullptr;
+  const dv_status st = check_call<FORM>(cache, layer, s, e, queries, &x, workspace,
+                                        workspace_bytes, nullptr, &p, &q, &ws);
+  return st != DV_OK || p.tokens == 0 ? st : run_call<FORM>(p, q, x, ws, stream);
 }
 
 }  // namespace

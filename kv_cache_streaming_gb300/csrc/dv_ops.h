@@ -165,5 +165,6 @@ inline bool overlaps_layers(const Plan& p, const void* a, size_t n) {
 uint32_t attention_tries();
 cudaError_t plain_waits(void** address);
 cudaError_t window_waits(void** address);
+cudaError_t scored_waits(void** address);
 
 }  // namespace dv

@@ -1,0 +1,706 @@
+// dv_scored_attention: causal attention that also adds up, for each cache row and key head,
+// the weight that the new tokens gave it,
+//   mass[b][h][j] += sum_i sum_g w_{i,g,j},  w_{i,g,j} = exp2(c s_{i,g,j} - lse_{i,g}).
+//
+// A weight is known only once its row's softmax is complete, so the sums are a second pass.
+// The attention kernel (dv_attention.cuh, form kScored) leaves lse = log2 sum_j exp2(c s_j) of
+// each (token, query head); then
+//   few rows (a decode step): it has left the scores too, 4 bytes each, and few_kernel reads
+//     them back: 8 bytes a row of the cache beside the 4 D of K and V;
+//   else mass_kernel computes S^T = K Q^T again on the tensor cores, with the keys as rows, so
+//     that a thread that owns a key sums along its row of tensor memory and nothing is reduced
+//     across threads.
+//
+// mass_kernel: a unit of work is 128 cache rows of a (sequence, key head), against the counted
+// (token, head of the group) rows that attend some of them, in tiles of 128.  The units form
+// one line, each as long as its tiles and unit cost, cut into equal stretches, one a CTA (one
+// CTA an SM); a unit that a cut divides leaves partial sums, which mass_join_kernel adds in
+// order (no atomics: the same bits each time).  Warps 0-7 sum, two to a quarter of the rows with
+// half of the columns each; 8 loads (and walks over the units), 9 issues the products into four
+// buffers of tensor memory, 10 fetches lse.
+//
+// Every wait gives up after a number of tries, as in the attention kernel.
+#include <algorithm>
+
+#include "dv_attention.cuh"
+
+namespace dv {
+
+cudaError_t scored_waits(void** address) {
+  return cudaGetSymbolAddress(address, g_attention_gave_up);
+}
+
+namespace {
+
+// Rows (new tokens x heads of a group) up to which the scores are kept.
+constexpr int kFewRows = 16;
+constexpr int kFewThreads = 256;
+constexpr int kMassThreads = 352;
+constexpr int kSumWarps = 8;
+// What a unit costs besides its tiles (its keys' fetch, the sums' exchange), in tiles.
+constexpr int kMassUnitCost = 1;
+
+struct MassDivided {
+  int64_t at;    // of the unit's first row in mass
+  int32_t rows;  // of the unit (0: none here)
+  int32_t last, slot;  // the last CTA with a piece; the first piece's slot
+  int32_t pad[3];
+};
+
+template <int MAXB>
+struct MassParams {
+  CUtensorMap q_map;  // as in AttnBase
+  CUtensorMap k_map;
+  const uint4* k;
+  const float* lse;  // [H][T][G]
+  float* mass;       // [B][H][S]
+  float* part;       // two slots of kTile sums a CTA
+  MassDivided* divided;
+  int32_t share, extra;
+  int32_t H, G, C, S;
+  int32_t k_rows, tile_tok;
+  int32_t tokens, last;  // T; the counted tokens of a sequence (0: all)
+  uint32_t tries;
+  float c;
+  SeqTable<MAXB> seq;
+  int32_t cost_pre[MAXB + 1];
+};
+
+// The counted tokens of a sequence of n new ones: [first, n).
+__host__ __device__ __forceinline__ int first_counted(int n, int last) {
+  return last > 0 && n > last ? n - last : 0;
+}
+// The first counted token that attends some of the rows from `row` on.
+__host__ __device__ __forceinline__ int first_token(int start, int n, int last, int row) {
+  const int c0 = first_counted(n, last);
+  return row - start > c0 ? row - start : c0;
+}
+
+struct MassItem {
+  int b, h, row0;   // the unit's rows [row0, row0 + kTile)
+  int row_end;      // of the sequence
+  int tok0, n;      // the piece's first token; its tiles of tokens (0: no more items)
+  int whole;
+  int start, n_tok, tok_at;
+};
+
+template <int DP>
+struct MassSmem {
+  static constexpr int kSlot = kTile * DP * 2;
+  static constexpr int kK = 2, kQ = 4, kS = 4, kL = 8;  // tiles of K and Q, sums, lse
+  static constexpr int kQAt = kK * kSlot;
+  static constexpr int kCtl = kQAt + kQ * kSlot;
+  struct Ctl {
+    float lse[kL][kTile];  // negative
+    float sum[2][kTile];   // of the second half of the columns
+    uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ], s_full[kS], s_empty[kS];
+    uint64_t lse_full[kL], lse_empty[kL], sum_full[2], sum_empty[2];
+    uint64_t item_full[kItems], item_empty[kItems], drained;
+    MassItem item[kItems];
+    uint32_t tmem;
+  };
+  static constexpr int kBytes = kCtl + (int)sizeof(Ctl);
+  static_assert(kBytes <= 232448, "more shared memory than a CTA has");
+};
+
+template <typename P>
+struct MassWalk {
+  const P& p;
+  int pos, end;     // as in Walk
+  int b, h, kt, t;  // the next piece: its unit and first tile of tokens
+
+  __device__ int tiles(int first) const {  // of tokens, from `first` on
+    return (p.seq.pre[b + 1] - p.seq.pre[b] - first + p.tile_tok - 1) / p.tile_tok;
+  }
+  __device__ int token0() const {
+    return first_token(p.seq.start[b], p.seq.pre[b + 1] - p.seq.pre[b], p.last, kt * kTile);
+  }
+
+  __device__ MassWalk(const P& p_, int lo, int hi) : p(p_), pos(lo), end(hi) {
+    b = h = kt = t = 0;
+    if (lo >= hi) return;
+    int x = 0, y = p.seq.batch;
+#pragma unroll 1
+    while (y - x > 1) {
+      const int m = (x + y) >> 1;
+      if (p.cost_pre[m] <= lo) x = m; else y = m;
+    }
+    b = x;
+    int rem = lo - p.cost_pre[b];
+    const int head = (p.cost_pre[b + 1] - p.cost_pre[b]) / p.H;
+    h = rem / head;
+    rem -= h * head;
+    // the rows that every counted token attends: units of one cost
+    const int c0 = first_counted(p.seq.pre[b + 1] - p.seq.pre[b], p.last);
+    const int flat = (p.seq.start[b] + c0) / kTile + 1, cost0 = kMassUnitCost + tiles(c0);
+    kt = min(rem / cost0, flat);
+    rem -= kt * cost0;
+    if (kt == flat)
+#pragma unroll 1
+      for (;;) {
+        const int cost = kMassUnitCost + tiles(token0());
+        if (rem < cost) break;
+        rem -= cost;
+        ++kt;
+      }
+    pos = lo - rem;
+    t = max(0, rem - kMassUnitCost);
+  }
+
+  __device__ void next(MassItem* it) {
+    it->n = 0;
+    if (pos >= end) return;
+    const int start = p.seq.start[b], at = p.seq.pre[b], n_tok = p.seq.pre[b + 1] - at;
+    const int first = token0(), cnt = tiles(first);
+    const int n = min(cnt, end - pos - kMassUnitCost) - t;
+    if (n <= 0) return;
+    it->b = b;
+    it->h = h;
+    it->row0 = kt * kTile;
+    it->row_end = start + n_tok;
+    it->tok0 = first + t * p.tile_tok;
+    it->n = n;
+    it->whole = t == 0 && n == cnt;
+    it->start = start;
+    it->n_tok = n_tok;
+    it->tok_at = at;
+    pos += kMassUnitCost + cnt;
+    t = 0;
+    if (++kt * kTile >= it->row_end) {
+      kt = 0;
+      if (++h == p.H) {
+        h = 0;
+        if (pos < end) do ++b; while (p.seq.pre[b + 1] == p.seq.pre[b]);
+      }
+    }
+  }
+};
+
+// (a, b) = (a, b) * c + (d, e)
+__device__ __forceinline__ void fma2(float& a, float& b, float c, float d, float e) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n"
+      " mov.b64 z, {%3, %4};\n fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d), "f"(e));
+}
+
+template <typename T, int DP, int MAXB>
+__global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
+    const __grid_constant__ MassParams<MAXB> p) {
+  using SM = MassSmem<DP>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t base = smem_u32(sm);
+  if ((base & 1023) != 0) {  // the swizzle goes by address bits
+    ops_pdl_enter();
+    if (threadIdx.x == 0) {
+      gave_up();
+      if (blockIdx.x > 0) p.divided[blockIdx.x - 1] = MassDivided{};
+    }
+    return;
+  }
+  typename SM::Ctl& ctl = *reinterpret_cast<typename SM::Ctl*>(sm + SM::kCtl);
+  const int warp = __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const auto at = [&](const uint64_t& bar) {
+    return base + (uint32_t)(reinterpret_cast<const uint8_t*>(&bar) - sm);
+  };
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     base + (uint32_t)(reinterpret_cast<uint8_t*>(&ctl.tmem) - sm)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SM::kK; ++i) {
+      bar_init(at(ctl.k_full[i]), 1);
+      bar_init(at(ctl.k_empty[i]), 1);
+    }
+    for (int i = 0; i < SM::kQ; ++i) {
+      bar_init(at(ctl.q_full[i]), 1);
+      bar_init(at(ctl.q_empty[i]), 1);
+    }
+    for (int i = 0; i < SM::kS; ++i) {
+      bar_init(at(ctl.s_full[i]), 1);
+      bar_init(at(ctl.s_empty[i]), kSumWarps);
+    }
+    for (int i = 0; i < SM::kL; ++i) {
+      bar_init(at(ctl.lse_full[i]), 1);
+      bar_init(at(ctl.lse_empty[i]), kSumWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(at(ctl.sum_full[i]), kTile);
+      bar_init(at(ctl.sum_empty[i]), kTile);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      bar_init(at(ctl.item_full[i]), 1);
+      bar_init(at(ctl.item_empty[i]), kSumWarps + 2);
+    }
+    bar_init(at(ctl.drained), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = __shfl_sync(~0u, ctl.tmem, 0);
+  ops_pdl_enter();
+
+  const int used = p.tile_tok * p.G;  // rows of a tile of Q that hold a token
+  const auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.tries); };
+  const auto get_item = [&](uint32_t k, MassItem* it) {
+    if (!wait(at(ctl.item_full[k % kItems]), k / kItems & 1)) return false;
+    *it = ctl.item[k % kItems];
+    return __all_sync(~0u, it->n > 0) != 0;
+  };
+  const auto done_item = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(at(ctl.item_empty[k % kItems]));
+  };
+
+  if (warp == 8) {
+    // ---- the walk, and loads ----
+    const bool on = elect();
+    MassWalk<MassParams<MAXB>> walk(p, cut(p, blockIdx.x), cut(p, blockIdx.x + 1));
+    if (blockIdx.x > 0 && on) {
+      MassDivided d = {};
+      const int from = cut(p, blockIdx.x - 1);
+      if (walk.t > 0 && from <= walk.pos + kMassUnitCost) {
+        const int row0 = walk.kt * kTile;
+        const int row_end = p.seq.start[walk.b] + p.seq.pre[walk.b + 1] - p.seq.pre[walk.b];
+        const int end = walk.pos + kMassUnitCost + walk.tiles(walk.token0());
+        d.at = ((int64_t)walk.b * p.H + walk.h) * p.S + row0;
+        d.rows = min(kTile, row_end - row0);
+        d.last = blockIdx.x;
+#pragma unroll 1
+        while (cut(p, d.last + 1) < end) ++d.last;
+        d.slot = from < walk.pos ? 1 : 0;
+      }
+      p.divided[blockIdx.x - 1] = d;
+    }
+    Ring<SM::kK> kr;
+    Ring<SM::kQ> qr;
+    uint32_t nk = 0, nq = 0, n_items = 0;
+    bool ok = true;
+    while (ok) {
+      MassItem it;
+      walk.next(&it);
+      if (n_items >= kItems)
+        ok = wait(at(ctl.item_empty[n_items % kItems]), (n_items / kItems - 1) & 1);
+      if (!ok) break;
+      if (on) {
+        ctl.item[n_items % kItems] = it;
+        bar_arrive(at(ctl.item_full[n_items % kItems]));
+      }
+      ++n_items;
+      if (it.n == 0) break;
+      if (nk >= SM::kK && !(ok = wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1))) break;
+      {
+        const uint32_t bar = at(ctl.k_full[kr.slot]), dst = base + kr.slot * SM::kSlot;
+        const int head = it.b * p.H + it.h, rows = min(kTile, it.row_end - it.row0);
+        const int pad = p.C & 1;  // zeros for the other half of the last contraction step
+        bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
+        if (rows == kTile) {
+          tma_load4(dst, &p.k_map, 0, it.row0 / p.k_rows, 0, head, bar, on);
+        } else {
+          const uint4* src = p.k + (int64_t)head * p.C * p.S + it.row0;
+#pragma unroll 1
+          for (int c = 0; c < p.C; ++c)
+            bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar, on);
+        }
+        if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar, on);
+        kr.next();
+        ++nk;
+      }
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j) {
+        if (nq >= SM::kQ && !(ok = wait(at(ctl.q_empty[qr.slot]), qr.turn ^ 1))) break;
+        const uint32_t bar = at(ctl.q_full[qr.slot]);
+        bar_expect(bar, (DP / 64) * 128 * used, on);
+        for (int half = 0; half < DP / 64; ++half)
+          tma_load4(base + SM::kQAt + qr.slot * SM::kSlot + half * (kTile * 128), &p.q_map,
+                    half * 64, 0, it.h, it.tok_at + it.tok0 + j * p.tile_tok, bar, on);
+        qr.next();
+        ++nq;
+      }
+    }
+    // No copy is left in flight, whichever warp gave up.
+#pragma unroll 1
+    for (uint32_t i = 0; i < SM::kK && i < nk; ++i)  // a slot's last use
+      bar_wait(at(ctl.k_full[i]), (nk - i - 1) / SM::kK & 1, kSpinLimit);
+#pragma unroll 1
+    for (uint32_t i = 0; i < SM::kQ && i < nq; ++i)
+      bar_wait(at(ctl.q_full[i]), (nq - i - 1) / SM::kQ & 1, kSpinLimit);
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---- products: S^T = K Q^T ----
+    const bool on = elect();
+    constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
+    constexpr uint32_t kIdesc = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(kTile >> 3) << 17 |
+                                (uint32_t)(kTile >> 4) << 24;
+    const int steps = (p.C + 1) / 2;
+    Ring<SM::kK> kr;
+    Ring<SM::kQ> qr;
+    Ring<SM::kS> sr;
+    uint32_t n_items = 0, ns = 0;
+    bool ok = true;
+    MassItem it;
+    while (ok && get_item(n_items, &it)) {
+      const int n = __shfl_sync(~0u, it.n, 0);
+      if (!(ok = wait(at(ctl.k_full[kr.slot]), kr.turn))) break;
+      const uint64_t kd = smem_desc(base + kr.slot * SM::kSlot, kTile * 16, 128, 0);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = wait(at(ctl.q_full[qr.slot]), qr.turn))) break;
+        if (ns >= SM::kS && !(ok = wait(at(ctl.s_empty[sr.slot]), sr.turn ^ 1))) break;
+        fence_after();
+        const uint64_t qd = smem_desc(base + SM::kQAt + qr.slot * SM::kSlot, 0, 1024, 2);
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s)
+          mma_ss(tmem + sr.slot * kTile, kd + s * (2 * kTile),
+                 qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kIdesc, s > 0, on && s < steps);
+        mma_commit(at(ctl.s_full[sr.slot]), on);
+        mma_commit(at(ctl.q_empty[qr.slot]), on);
+        qr.next();
+        sr.next();
+        ++ns;
+      }
+      mma_commit(at(ctl.k_empty[kr.slot]), on);
+      kr.next();
+      done_item(n_items++);
+    }
+    // the products in flight end before tensor memory is given back
+    mma_commit(at(ctl.drained), on);
+    bar_wait(at(ctl.drained), 0, kSpinLimit);
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---- lse of each tile's rows ----
+    Ring<SM::kL> lr;
+    uint32_t n_items = 0, nl = 0;
+    bool ok = true;
+    MassItem it;
+    while (ok && get_item(n_items, &it)) {
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j) {
+        const int tok = it.tok0 + j * p.tile_tok, cols = min(p.tile_tok, it.n_tok - tok) * p.G;
+        const float* const src = p.lse + ((int64_t)it.h * p.tokens + it.tok_at + tok) * p.G;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = lane + 32 * e < cols ? -src[lane + 32 * e] : -INFINITY;
+        if (nl >= SM::kL && !(ok = wait(at(ctl.lse_empty[lr.slot]), lr.turn ^ 1))) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ctl.lse[lr.slot][lane + 32 * e] = x[e];
+        __syncwarp();
+        if (lane == 0) bar_arrive(at(ctl.lse_full[lr.slot]));
+        lr.next();
+        ++nl;
+      }
+      done_item(n_items++);
+    }
+  } else {
+    // ---- sums: a key per thread, half of the columns ----
+    const int half = warp >> 2, r = threadIdx.x & (kTile - 1);
+    const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + half * (kTile / 2);
+    Ring<SM::kS> sr;
+    Ring<SM::kL> lr;
+    uint32_t item = 0;
+    bool ok = true;
+    MassItem it;
+    for (; ok && get_item(item, &it); ++item) {
+      const int row = it.row0 + r;
+      float* const mass = p.mass + ((int64_t)it.b * p.H + it.h) * p.S + row;
+      const bool write = half == 0 && row < it.row_end;
+      const float old = write && it.whole ? *mass : 0.f;
+      float total = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j) {
+        if (!(ok = wait(at(ctl.s_full[sr.slot]), sr.turn))) break;
+        fence_after();
+        uint32_t x[kTile / 2];
+        tmem_ld32(x, ts + sr.slot * kTile);
+        tmem_ld32(x + 32, ts + sr.slot * kTile + 32);
+        tmem_wait_ld();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(at(ctl.s_empty[sr.slot]));
+        sr.next();
+        if (!(ok = wait(at(ctl.lse_full[lr.slot]), lr.turn))) break;
+        const float4* const nl =
+            reinterpret_cast<const float4*>(ctl.lse[lr.slot] + half * (kTile / 2));
+        const int tok = it.tok0 + j * p.tile_tok, cols = min(p.tile_tok, it.n_tok - tok) * p.G;
+        float sum[4] = {};
+        if (cols == kTile && it.start + tok >= it.row0 + kTile - 1) {
+#pragma unroll
+          for (int e = 0; e < kTile / 2; e += 4) {
+            const float4 n4 = nl[e / 4];
+            float a = __uint_as_float(x[e]), b = __uint_as_float(x[e + 1]);
+            float c = __uint_as_float(x[e + 2]), d = __uint_as_float(x[e + 3]);
+            fma2(a, b, p.c, n4.x, n4.y);
+            fma2(c, d, p.c, n4.z, n4.w);
+            add2(sum[0], sum[1], ex2(a), ex2(b));
+            add2(sum[2], sum[3], ex2(c), ex2(d));
+          }
+        } else {
+          // columns [lo, hi): tokens from the key's own row on, up to the last (what is past
+          // them may hold anything)
+          const int lo = max(0, row - it.start - tok) * p.G - half * (kTile / 2);
+          const int hi = cols - half * (kTile / 2);
+#pragma unroll
+          for (int e = 0; e < kTile / 2; ++e) {
+            const float w =
+                ex2(fmaf(__uint_as_float(x[e]), p.c, reinterpret_cast<const float*>(nl)[e]));
+            if (e >= lo && e < hi) sum[e & 3] += w;
+          }
+        }
+        total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        __syncwarp();
+        if (lane == 0) bar_arrive(at(ctl.lse_empty[lr.slot]));
+        lr.next();
+      }
+      if (!ok) break;
+      const uint32_t x = item & 1, parity = item >> 1 & 1;
+      if (half == 1) {
+        if (item >= 2 && !(ok = wait(at(ctl.sum_empty[x]), parity ^ 1))) break;
+        ctl.sum[x][r] = total;
+        bar_arrive(at(ctl.sum_full[x]));
+      } else {
+        if (!(ok = wait(at(ctl.sum_full[x]), parity))) break;
+        total += ctl.sum[x][r];
+        bar_arrive(at(ctl.sum_empty[x]));
+        if (it.whole) {
+          if (write) *mass = old + total;
+        } else {
+          p.part[(int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kTile + r] = total;
+        }
+      }
+      done_item(item);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+// Adds the pieces of the unit that the cut after CTA blockIdx.x is the first to divide.
+__global__ __launch_bounds__(kTile) void mass_join_kernel(const MassDivided* divided,
+                                                          const float* part, float* mass) {
+  ops_pdl_enter();
+  const MassDivided d = divided[blockIdx.x];
+  const int r = threadIdx.x, i0 = blockIdx.x;
+  if (r >= d.rows) return;
+  float total = part[(int64_t)(2 * i0 + d.slot) * kTile + r];
+  for (int i = i0 + 1; i <= d.last; ++i) total += part[(int64_t)(2 * i) * kTile + r];
+  mass[d.at + r] += total;
+}
+
+// ---- few rows: from the scores that the attention kernel kept ----------------------
+
+template <int MAXB>
+struct FewParams {
+  const float* lse;
+  const float* scores;
+  float* mass;
+  int32_t H, G, S, tokens, last, chunks;
+  float c;
+  SeqTable<MAXB> seq;
+  int32_t block_pre[MAXB + 1];
+};
+
+// A thread per cache row; a CTA per (sequence, key head, kFewThreads rows).
+template <int MAXB>
+__global__ __launch_bounds__(kFewThreads) void few_kernel(
+    const __grid_constant__ FewParams<MAXB> p) {
+  ops_pdl_enter();
+  const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x - bh * p.chunks;
+  const int b = bh / p.H, h = bh - b * p.H;
+  const int start = p.seq.start[b], t0 = p.seq.pre[b], n = p.seq.pre[b + 1] - t0;
+  const int row = chunk * kFewThreads + threadIdx.x, row_end = start + n;
+  if (n == 0 || row >= row_end) return;
+  const int64_t pitch = (int64_t)((row_end + kTile - 1) / kTile) * kTile;
+  const float* s = p.scores + kTile * (int64_t)p.block_pre[b] * (p.H * p.G) +
+                   (int64_t)h * p.G * n * pitch + row;
+  const float* const lse = p.lse + ((int64_t)h * p.tokens + t0) * p.G;
+  const int first = first_token(start, n, p.last, row);
+  if (first >= n) return;
+  float sum = 0.f;
+  for (int g = 0; g < p.G; ++g)
+    for (int i = first; i < n; ++i)
+      sum += ex2(fmaf(s[(int64_t)(g * n + i) * pitch], p.c, -lse[i * p.G + g]));
+  p.mass[((int64_t)b * p.H + h) * p.S + row] += sum;
+}
+
+// ---- host ----------------------------------------------------------------------------
+
+size_t up32(size_t n) { return (n + 31) / 32 * 32; }
+
+// Whether the attention kernel keeps the scores: it runs one row tile a unit, of few rows.
+bool keeps_scores(const Plan& p, int group) {
+  return p.max_len <= kTile / group && p.max_len * group <= kFewRows &&
+         score_blocks(p, nullptr) <= INT32_MAX;
+}
+
+// The workspace behind the attention's own: lse, then the scores or the mass kernel's pieces.
+size_t lse_bytes(const Plan& p, int group) {
+  return up32((size_t)p.tokens * p.H * group * sizeof(float));
+}
+size_t scored_bytes(const Plan& p, int group) {
+  const size_t rest =
+      keeps_scores(p, group)
+          ? (size_t)score_blocks(p, nullptr) * p.H * group * kTile * sizeof(float)
+          : (size_t)sm_count() * (2 * kTile * sizeof(float) + sizeof(MassDivided));
+  return 32 + lse_bytes(p, group) + rest;
+}
+
+// Cost of the mass kernel's units, before each sequence in `pre`; in *tiles their tiles.
+int64_t mass_cost(const Plan& p, int tile_tok, int32_t last, int32_t* pre, int64_t* tiles) {
+  int64_t total = 0;
+  *tiles = 0;
+  for (int b = 0; b < p.B; ++b) {
+    if (pre) pre[b] = (int32_t)total;
+    const int n = p.seq_len[b], start = p.seq_start[b];
+    if (n == 0) continue;
+    const auto count = [&](int first) { return (n - first + tile_tok - 1) / tile_tok; };
+    // (the rows that all counted tokens attend: units of one cost)
+    const int c0 = first_counted(n, last);
+    int64_t units = (start + c0) / kTile + 1, t = units * count(c0);
+    for (int64_t row = units * kTile; row < (int64_t)start + n; row += kTile, ++units)
+      t += count(first_token(start, n, last, (int)row));
+    *tiles += t * p.H;
+    total += (t + units * kMassUnitCost) * p.H;
+  }
+  if (pre) pre[p.B] = (int32_t)total;
+  return total;
+}
+
+// Blocks of rows of a (sequence, key head) in few_kernel.
+int64_t few_chunks(const Plan& p) {
+  int64_t rows = 0;
+  for (int b = 0; b < p.B; ++b)
+    if (p.seq_len[b] > 0) rows = std::max<int64_t>(rows, (int64_t)p.seq_start[b] + p.seq_len[b]);
+  return (rows + kFewThreads - 1) / kFewThreads;
+}
+
+template <typename T, int DP, int MAXB>
+cudaError_t launch_mass(const MassParams<MAXB>& kp, int ctas, cudaStream_t stream) {
+  void (*const kernel)(MassParams<MAXB>) = mass_kernel<T, DP, MAXB>;
+  constexpr int kBytes = MassSmem<DP>::kBytes;
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (err != cudaSuccess) return err;
+  return ops_launch(kernel, dim3((unsigned)ctas), kMassThreads, kBytes, stream, kp);
+}
+
+template <typename T, int MAXB>
+dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t last, uint8_t* rest,
+                   cudaStream_t stream) {
+  const int group = q.q_heads / p.H;
+  if (x.scores) {
+    FewParams<MAXB> fp;
+    fp.lse = x.lse;
+    fp.scores = x.scores;
+    fp.mass = x.mass;
+    fp.H = p.H;
+    fp.G = group;
+    fp.S = p.S;
+    fp.tokens = (int32_t)p.tokens;
+    fp.last = last;
+    fp.c = q.scale * 1.4426950408889634f;
+    fill_table(p, &fp.seq);
+    score_blocks(p, fp.block_pre);
+    fp.chunks = (int32_t)few_chunks(p);
+    const cudaError_t err = ops_launch(few_kernel<MAXB>, dim3((unsigned)(fp.chunks * p.H * p.B)),
+                                       kFewThreads, 0, stream, fp);
+    return err == cudaSuccess ? DV_OK : cuda_fail(err, "scored attention's sums launch");
+  }
+  MassParams<MAXB> kp;
+  kp.tile_tok = kTile / group;
+  int64_t tiles = 0;
+  const int64_t total = mass_cost(p, kp.tile_tok, last, kp.cost_pre, &tiles);
+  int64_t ctas = sm_count();
+  if (ctas > tiles) ctas = tiles;
+  const void* k = static_cast<const uint4*>(p.k) + p.l0 * p.layer_chunks;
+  if (!encode_q(&kp.q_map, p, q, group, kp.tile_tok) ||
+      !encode_k(&kp.k_map, p, q.dtype == DV_DTYPE_FP16, k))
+    return fail(DV_ERR_CUDA, "cuTensorMapEncodeTiled refused the queries or the cache");
+  kp.k = static_cast<const uint4*>(k);
+  kp.lse = x.lse;
+  kp.mass = x.mass;
+  kp.part = reinterpret_cast<float*>(rest);
+  kp.divided = reinterpret_cast<MassDivided*>(rest + (size_t)ctas * 2 * kTile * sizeof(float));
+  kp.share = (int32_t)(total / ctas);
+  kp.extra = (int32_t)(total % ctas);
+  kp.H = p.H;
+  kp.G = group;
+  kp.C = p.C;
+  kp.S = p.S;
+  kp.k_rows = k_run(p);
+  kp.tokens = (int32_t)p.tokens;
+  kp.last = last;
+  kp.tries = attention_tries();
+  kp.c = q.scale * 1.4426950408889634f;
+  fill_table(p, &kp.seq);
+  cudaError_t err = p.D <= 64 ? launch_mass<T, 64, MAXB>(kp, (int)ctas, stream)
+                              : launch_mass<T, 128, MAXB>(kp, (int)ctas, stream);
+  if (err == cudaSuccess && ctas > 1)
+    err = ops_launch(mass_join_kernel, dim3((unsigned)ctas - 1), kTile, 0, stream,
+                     static_cast<const MassDivided*>(kp.divided),
+                     static_cast<const float*>(kp.part), kp.mass);
+  return err == cudaSuccess ? DV_OK : cuda_fail(err, "scored attention's sums launch");
+}
+
+}  // namespace
+}  // namespace dv
+
+extern "C" dv_status dv_scored_attention_workspace(const dv_cache* cache, const int32_t* seq_start,
+                                                   const int32_t* seq_end, int32_t q_heads,
+                                                   size_t* bytes) {
+  if (!bytes) return dv::fail(DV_ERR_INVALID_ARG, "bytes is NULL");
+  dv::Plan p;
+  dv_status st = dv::plan_ranges(cache, 0, 1, seq_start, seq_end, &p);
+  if (st != DV_OK) return st;
+  if ((st = dv::check_heads(cache, p, q_heads)) != DV_OK) return st;
+  const int group = q_heads / p.H;
+  *bytes = p.tokens == 0 ? 0
+                         : dv::schedule<dv::kScored>(p, group, {}, nullptr).bytes +
+                               dv::scored_bytes(p, group);
+  return DV_OK;
+}
+
+extern "C" dv_status dv_scored_attention(const dv_cache* cache, int32_t layer,
+                                         const int32_t* seq_start, const int32_t* seq_end,
+                                         const dv_queries* queries, int32_t last, float* mass,
+                                         void* workspace, size_t workspace_bytes,
+                                         dv_stream stream) {
+  dv::Trace trace("dv_scored_attention");
+  if (last < 0) return dv::fail(DV_ERR_INVALID_ARG, "the last %d tokens", last);
+  dv::Plan p;
+  dv_queries q;
+  dv::Extra x;
+  x.mass = mass;
+  uint8_t* ws = nullptr;
+  dv_status st = dv::check_call<dv::kScored>(cache, layer, seq_start, seq_end, queries, &x,
+                                             workspace, workspace_bytes, dv::scored_bytes, &p, &q,
+                                             &ws);
+  if (st != DV_OK || p.tokens == 0) return st;
+  const int group = q.q_heads / p.H;
+  uint8_t* const lse = ws + dv::up32(dv::schedule<dv::kScored>(p, group, x, nullptr).bytes);
+  uint8_t* const rest = lse + dv::lse_bytes(p, group);
+  x.lse = reinterpret_cast<float*>(lse);
+  int64_t tiles = 0, work = 0;
+  if (dv::keeps_scores(p, group)) {
+    x.scores = reinterpret_cast<float*>(rest);
+    work = dv::few_chunks(p) * p.H * p.B;
+  } else {
+    work = dv::mass_cost(p, dv::kTile / group, last, nullptr, &tiles);
+  }
+  if (work > INT32_MAX)
+    return dv::fail(DV_ERR_UNSUPPORTED, "%lld tiles of weights in one call", (long long)work);
+  if ((st = dv::run_call<dv::kScored>(p, q, x, ws, stream)) != DV_OK) return st;
+  const bool small = p.B <= dv::kSmallBatch;
+  if (q.dtype == DV_DTYPE_FP16)
+    return small ? dv::add_mass<__half, dv::kSmallBatch>(p, q, x, last, rest, stream)
+                 : dv::add_mass<__half, dv::kMaxBatch>(p, q, x, last, rest, stream);
+  return small ? dv::add_mass<__nv_bfloat16, dv::kSmallBatch>(p, q, x, last, rest, stream)
+               : dv::add_mass<__nv_bfloat16, dv::kMaxBatch>(p, q, x, last, rest, stream);
+}

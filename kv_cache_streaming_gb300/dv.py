@@ -137,6 +137,10 @@ _tree_attention = _sig("dv_tree_attention", [_CP, _I32, _I32P, _I32P, ctypes.POI
                                              _P, _P, _SZ, _P])
 _window_attention = _sig("dv_window_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
                                                  _I32, _I32, _P, _SZ, _P])
+_scored_attention = _sig("dv_scored_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
+                                                 _I32, _P, _P, _SZ, _P])
+_scored_workspace = _sig("dv_scored_attention_workspace", [_CP, _I32P, _I32P, _I32,
+                                                           ctypes.POINTER(_SZ)])
 _attention_check = _sig("dv_attention_check", [_P])
 _attention_tries = _sig("dv_debug_attention_tries", [_I32])
 _compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _I64, _P])
@@ -943,6 +947,39 @@ def dv_window_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, 
     w, wn = _buf(workspace)
     _check(_window_attention(cache.ref, layer, sp, ep, ctypes.byref(a), _int32(window, "window"),
                              _int32(sinks, "sinks"), w, wn, _stream(stream)))
+
+
+def _mass(t, name, shape):
+    """Address of a contiguous float32 tensor of ``shape``."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    if t.element_size() != 4 or not t.is_floating_point():
+        raise TypeError(f"{name} must hold float32 (got {t.dtype})")
+    if not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def dv_scored_attention_workspace(cache: Cache, seq_start, seq_end, q_heads) -> int:
+    s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
+    out = _SZ(0)
+    _check(_scored_workspace(cache.ref, sp, ep, q_heads, ctypes.byref(out)))
+    return out.value
+
+
+def dv_scored_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, mass,
+                        workspace=None, last=0, stream=None) -> None:
+    """As ``dv_prompt_attention`` (and for decode steps), and adds the weight
+    that each cache row receives from the last ``last`` new tokens of its
+    sequence (0: all) to ``mass``, the layer's float32 [batch, num_heads,
+    max_seq].  ``workspace``: of ``dv_scored_attention_workspace`` bytes."""
+    c = cache.c
+    s, e, sp, ep = _ranges(seq_start, seq_end, c.batch)
+    _, a = _queries(cache, q, out, scale)
+    m = _mass(mass, "mass", (c.batch, c.num_heads, c.max_seq))
+    w, wn = _buf(workspace)
+    _check(_scored_attention(cache.ref, layer, sp, ep, ctypes.byref(a), _int32(last, "last"), m, w, wn,
+                             _stream(stream)))
 
 
 def dv_attention_check(stream=None) -> None:

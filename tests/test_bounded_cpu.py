@@ -55,3 +55,61 @@ def test_window_refusals():
     n = np.zeros(2, np.int32).ctypes.data
     assert dv.lib.dv_window_attention(None, 0, n, n, None, 4, 1, None, 0, None) == dv.DV_ERR_INVALID_ARG
     assert dv.lib.dv_window_attention(_cache().ref, 0, n, n, None, 4, 1, None, 0, None) == dv.DV_ERR_INVALID_ARG
+
+
+def test_scored_refusals():
+    def call(c=None, layer=0, s=S2, e=E2, q=None, scale=0.125, heads=8, D=64, last=0, mass=None):
+        c = c or _cache()
+        q, o = _qo(int((np.asarray(e) - np.asarray(s)).sum()), heads, D) if q is None else q
+        mass = torch.zeros(2, 4, 32) if mass is None else mass
+        dv.dv_scored_attention(c, layer, s, e, q, o, scale, mass, None, last=last, stream=0)
+
+    for last in (-1, -2**31):
+        _refused(dv.DV_ERR_INVALID_ARG, lambda: call(last=last))
+    with pytest.raises(ValueError):
+        call(last=2**31)
+    for mass in (torch.zeros(2, 4, 31), torch.zeros(4, 32), torch.zeros(2, 2, 4, 32)):
+        with pytest.raises(ValueError):
+            call(mass=mass)
+    for mass in (torch.zeros(2, 4, 32, dtype=torch.float64), torch.zeros(2, 4, 32, dtype=F16),
+                 torch.zeros(2, 4, 32, dtype=torch.int32), torch.zeros(2, 4, 64)[..., ::2]):
+        with pytest.raises(TypeError):
+            call(mass=mass)
+    _refused(dv.DV_ERR_RANGE, lambda: call(layer=2))
+    _refused(dv.DV_ERR_RANGE, lambda: call(s=[4, 0], e=[33, 0]))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(heads=6))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(scale=math.nan))
+    _refused(dv.DV_ERR_UNSUPPORTED, lambda: call(c=_cache(D=136), D=136))
+    _refused(dv.DV_ERR_UNSUPPORTED, lambda: call(c=_cache(P=4)))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(q=_qo(n=4)))
+    _refused(dv.DV_ERR_BUFFER_TOO_SMALL, lambda: call())  # no workspace
+    call(s=[4, 3], e=[4, 3])
+    n = np.zeros(2, np.int32).ctypes.data
+    assert dv.lib.dv_scored_attention(None, 0, n, n, None, 0, None, None, 0, None) == dv.DV_ERR_INVALID_ARG
+
+
+def test_scored_refuses_weights_on_other_buffers():
+    K, V = (torch.zeros(2, 4 * 64 * 32, dtype=F16) for _ in range(2))
+    c = dv.Cache(2, 1, 4, 64, 32, 2, K, V)
+    s, e = np.array([4], np.int32), np.array([9], np.int32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    q, o = _qo(n=64, heads=4)
+    mass = torch.zeros(4 * 32)
+
+    def call(**kw):
+        a = dict(q=q[:5], out=o[:5], mass=mass, ws=ws) | kw
+        dv.dv_scored_attention(c, 1, s, e, a["q"], a["out"], 0.1, a["mass"].view(1, 4, 32), a["ws"], stream=0)
+
+    for kw in (dict(mass=K[1].view(torch.float32)[40:168]), dict(mass=V[1].view(torch.float32)[-128:]),
+               dict(mass=q.view(-1).view(torch.float32)[600:728]), dict(mass=o.view(-1).view(torch.float32)[:128]),
+               dict(mass=ws.view(torch.float32)[64:192])):
+        _refused(dv.DV_ERR_INVALID_ARG, lambda: call(**kw))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(out=q[4:9]))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(ws=(K.data_ptr(), 1 << 20)))
+
+
+def test_scored_workspace_refusals():
+    assert dv.dv_scored_attention_workspace(_cache(), S2, E2, 8) >= dv.dv_attention_workspace(_cache(), S2, E2, 8)
+    assert dv.dv_scored_attention_workspace(_cache(), [3, 3], [3, 3], 8) == 0
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: dv.dv_scored_attention_workspace(_cache(), S2, E2, 6))
+    _refused(dv.DV_ERR_RANGE, lambda: dv.dv_scored_attention_workspace(_cache(), [0, 0], [33, 0], 8))
