@@ -776,6 +776,26 @@ dv_status dv_kv_compact(const dv_cache* cache, int32_t l0, int32_t l1, const int
                         const int32_t* seq_end, const int32_t* keep, int64_t count,
                         dv_stream stream);
 
+/* Evicts, in layers [l0, l1), the rows that received least weight: of the rows[b] rows in use
+ * of sequence b, kept[b] stay (host arrays, 0 <= kept <= rows <= max_seq).  For each layer and
+ * key head by itself these are the first `sinks`, the last `recent`, and of those between them
+ * the ones with the largest `mass`; of equals the lowest rows, and NaN counts above every
+ * number.  They are moved together in place and in order (K, V and mass): row i gets what row
+ * keep[...] held.  Rows from kept[b] on keep their K and V; their mass, up to rows[b], is 0, as
+ * new tokens there need it.  kept[b] = rows[b] leaves a sequence as it is; else sinks + recent <=
+ * kept[b] (DV_ERR_INVALID_ARG).
+ *   mass, mass_out  [l1 - l0][batch][num_heads][max_seq] 32-bit floats (as dv_scored_attention
+ *                   adds up, layer by layer); the same buffer, or two that share no bytes.
+ *                   mass_out's rows from rows[b] on are left as they were.
+ *   keep            written: [l1 - l0][num_heads][sum of kept] int32, the sequences one after
+ *                   the other; `count` entries (else DV_ERR_INVALID_ARG).
+ * All device memory, 4-byte aligned, on none of the layers (else DV_ERR_INVALID_ARG).  Positions
+ * of the rows that stay are theirs still: tokens appended behind them are given theirs with
+ * dv_new_tokens.positions.  Any elem_bytes. */
+dv_status dv_kv_evict(const dv_cache* cache, int32_t l0, int32_t l1, const int32_t* rows,
+                      const int32_t* kept, int32_t sinks, int32_t recent, const float* mass,
+                      float* mass_out, int32_t* keep, int64_t count, dv_stream stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

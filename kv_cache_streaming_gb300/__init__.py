@@ -40,5 +40,5 @@ from .dv import (  # noqa: F401
     DV_ROPE_NONE, DV_ROPE_LINEAR, DV_ROPE_NTK, DV_ROPE_PARTS,
     Rope, dv_rope, dv_rope_init, dv_kv_append, dv_attention_workspace, dv_prompt_attention,
     dv_tree_attention, dv_window_attention, dv_scored_attention,
-    dv_scored_attention_workspace, dv_attention_check, dv_debug_attention_tries, dv_kv_compact,
+    dv_scored_attention_workspace, dv_attention_check, dv_debug_attention_tries, dv_kv_compact, dv_kv_evict,
 )

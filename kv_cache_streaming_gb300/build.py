@@ -28,7 +28,7 @@ LIB = PKG / "libdv.so"
 LIB_CHECKED = PKG / "libdv_checked.so"  # device-side bounds checks (debugging)
 SOURCES = ["dv_api.cu", "dv_replica.cu", "dv_sched.cu", "dv_hostmem.cu", "dv_kernels.cu",
            "dv_noalloc.cu", "dv_append.cu", "dv_compact.cu", "dv_attention.cu", "dv_window.cu",
-           "dv_scored.cu"]
+           "dv_scored.cu", "dv_evict.cu"]
 HEADERS = ["dv_plan.h", "dv_host.h", "dv_ops.h", "dv_attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

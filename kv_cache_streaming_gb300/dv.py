@@ -144,6 +144,7 @@ _scored_workspace = _sig("dv_scored_attention_workspace", [_CP, _I32P, _I32P, _I
 _attention_check = _sig("dv_attention_check", [_P])
 _attention_tries = _sig("dv_debug_attention_tries", [_I32])
 _compact = _sig("dv_kv_compact", [_CP, _I32, _I32, _I32P, _I32P, _P, _I64, _P])
+_evict = _sig("dv_kv_evict", [_CP, _I32, _I32, _I32P, _I32P, _I32, _I32, _P, _P, _P, _I64, _P])
 
 
 class DvError(RuntimeError):
@@ -1000,3 +1001,20 @@ def dv_kv_compact(cache: Cache, l0, l1, seq_start, seq_end, keep, stream=None) -
     s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
     _check(_compact(cache.ref, l0, l1, sp, ep, _words(keep, "keep", 4), keep.numel(),
                     _stream(stream)))
+
+
+def dv_kv_evict(cache: Cache, l0, l1, rows, kept, sinks, recent, mass, keep, mass_out=None,
+                stream=None) -> None:
+    """Of the ``rows[b]`` rows of each sequence ``kept[b]`` stay, by layer in
+    [l0, l1) and key head: the first ``sinks``, the last ``recent`` and those of
+    most ``mass`` (float32 [l1 - l0, batch, num_heads, max_seq]) between them,
+    moved together in place.  ``keep``: int32, l1 - l0 times num_heads times the
+    sum of ``kept``, gets the rows they were; ``mass_out`` (None: ``mass``
+    itself) the weights, moved likewise, and zeros behind them."""
+    c = cache.c
+    n, m, np_, mp = _ranges(rows, kept, c.batch)
+    shape = (l1 - l0, c.batch, c.num_heads, c.max_seq)
+    w = _mass(mass, "mass", shape)
+    o = w if mass_out is None else _mass(mass_out, "mass_out", shape)
+    _check(_evict(cache.ref, l0, l1, np_, mp, _int32(sinks, "sinks"), _int32(recent, "recent"), w, o,
+                  _words(keep, "keep", 4), keep.numel(), _stream(stream)))

@@ -84,3 +84,25 @@ def attend_ref(K, V, s, e, q, scale, window=1 << 40, sinks=0, last=0, mass=None)
                 m64[b, h, :z] += torch.where(seen, add, 0.0)
                 mtol[b, h, :z] = torch.where(seen, err + 2.0 ** -23 * m64[b, h, :z].abs(), 0.0)
     return out, tol, m64, mtol
+
+
+def evict_rows(mass, rows, kept, sinks, recent):
+    """The rows that stay of each (layer, head, sequence), [L][H][B] lists: a sort by (weight
+    from above, row), NaN above all numbers.  mass: [L, B, H, S], any device."""
+    m = mass.detach().cpu().double().numpy()
+    out = []
+    for l in range(m.shape[0]):
+        out.append([])
+        for h in range(m.shape[2]):
+            lists = []
+            for b, (n, k) in enumerate(zip(rows.tolist(), kept.tolist())):
+                if n == k:
+                    lists.append(list(range(n)))
+                    continue
+                x = m[l, b, h]
+                mid = sorted(range(sinks, n - recent), key=lambda i: (-math.inf if math.isnan(x[i]) else -x[i],
+                                                                      not math.isnan(x[i]), i))
+                top = sorted(mid[:k - sinks - recent])
+                lists.append(list(range(sinks)) + top + list(range(n - recent, n)))
+            out[-1].append(lists)
+    return out

@@ -113,3 +113,48 @@ def test_scored_workspace_refusals():
     assert dv.dv_scored_attention_workspace(_cache(), [3, 3], [3, 3], 8) == 0
     _refused(dv.DV_ERR_INVALID_ARG, lambda: dv.dv_scored_attention_workspace(_cache(), S2, E2, 6))
     _refused(dv.DV_ERR_RANGE, lambda: dv.dv_scored_attention_workspace(_cache(), [0, 0], [33, 0], 8))
+
+
+def test_evict_refusals():
+    def call(c=None, l0=0, l1=2, rows=(20, 32), kept=(10, 32), sinks=1, recent=2, mass=None, keep=None, out=None):
+        c = c or _cache()
+        mass = torch.zeros(max(0, l1 - l0), 2, 4, 32) if mass is None else mass
+        keep = torch.zeros(max(0, l1 - l0) * 4 * int(np.sum(kept)), dtype=torch.int32) if keep is None else keep
+        dv.dv_kv_evict(c, l0, l1, rows, kept, sinks, recent, mass, keep, mass_out=out, stream=0)
+
+    _refused(dv.DV_ERR_RANGE, lambda: call(l1=3))
+    _refused(dv.DV_ERR_RANGE, lambda: call(l0=-1, l1=1))
+    _refused(dv.DV_ERR_RANGE, lambda: call(rows=(20, 33), kept=(10, 10)))
+    _refused(dv.DV_ERR_RANGE, lambda: call(rows=(20, 9), kept=(10, 10)))
+    _refused(dv.DV_ERR_RANGE, lambda: call(kept=(-1, 10), keep=torch.zeros(72, dtype=torch.int32)))
+    for sinks, recent in ((-1, 0), (0, -1), (6, 5), (11, 0), (0, 11), (2**31 - 1, 2**31 - 1)):
+        _refused(dv.DV_ERR_INVALID_ARG, lambda: call(sinks=sinks, recent=recent))
+    for kw in (dict(sinks=2**31), dict(recent=2**32 + 1)):
+        with pytest.raises(ValueError):
+            call(**kw)
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(keep=torch.zeros(335, dtype=torch.int32)))
+    for bad in (torch.zeros(2, 2, 4, 31), torch.zeros(1, 2, 4, 32)):
+        with pytest.raises(ValueError):
+            call(mass=bad)
+        with pytest.raises(ValueError):
+            call(out=bad)
+    with pytest.raises(TypeError):
+        call(mass=torch.zeros(2, 2, 4, 32, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        call(keep=torch.zeros(336, dtype=torch.int64))
+    buf = torch.zeros(2 * 2 * 4 * 32 + 8)
+    a, b = buf[:512].view(2, 2, 4, 32), buf[4:516].view(2, 2, 4, 32)
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(mass=a, out=b))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(mass=a, keep=buf.view(torch.int32)[100:436]))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(out=a, keep=buf.view(torch.int32)[100:436]))
+    K, V = (torch.zeros(2, 2 * 4 * 64 * 32, dtype=F16) for _ in range(2))
+    c = dv.Cache(2, 2, 4, 64, 32, 2, K, V)
+    on = V[1].view(torch.float32)[16:272].view(1, 2, 4, 32)
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(c=c, l0=1, mass=on))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(c=c, l0=1, out=on))
+    _refused(dv.DV_ERR_INVALID_ARG, lambda: call(c=c, l0=1, keep=K[1].view(torch.int32)[:168]))
+    call(l0=1, l1=1)
+    call(rows=(0, 0), kept=(0, 0))
+    n = np.zeros(2, np.int32).ctypes.data
+    assert dv.lib.dv_kv_evict(None, 0, 1, n, n, 0, 0, None, None, None, 0, None) == dv.DV_ERR_INVALID_ARG
+    assert dv.lib.dv_kv_evict(_cache().ref, 0, 1, None, n, 0, 0, None, None, None, 0, None) == dv.DV_ERR_INVALID_ARG
