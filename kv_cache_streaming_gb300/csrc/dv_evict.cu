@@ -1,27 +1,36 @@
 // dv_kv_evict: of each (layer, sequence, key head) the rows that received most weight stay,
 // beside the first and the last ones, and are moved together in place.
 //
-// select_kernel finds a unit's rows: of the candidates, the rows between the first and the
-// last ones, those with the `need` largest weights.  A weight's bits, turned so that they order
-// as the numbers do, are looked at 8 at a time from the top: a histogram of the candidates that
-// agree with the border so far says which value the next 8 bits of the border have and how
-// many of the candidates at it still fit.  Then one pass in order of rows gives each kept row
-// its place (the kept ones before it: those above the border, and of those at it the first that
-// fit) and moves the weights.
+// One kernel, a CTA or a cluster of them for a (layer, sequence, key head): it finds the rows,
+// then copies them, so that some CTAs' search runs under others' copies.
 //
-// move_kernel is a pure copy of K and V rows, row i <- row keep[i] >= i.  A CTA takes a slice of
-// the 16-byte chunks of a (layer, K|V, sequence, key head)'s rows and walks the destinations
-// upwards; a step's reads come before its writes, and later steps read rows past what earlier
-// ones have written.  Bound by memory.
+// The search: of the candidates, the rows between the first and the last ones, those with the
+// `need` largest weights.  A weight's bits, turned so that they order as the numbers do, are
+// looked at 11 at a time from the top: a histogram of the candidates that agree with the border
+// so far says which value the next 11 bits of the border have and how many of the candidates at
+// it still fit; it ends early when all of them do.  Each kept row's place is the number of kept
+// ones before it, those above the border and of those at it the first that fit.  The weights
+// are read once and stay in shared memory; in a cluster each CTA takes a run of the rows, and
+// the histograms and counts are added through distributed shared memory.
+//
+// The copy: row i <- row keep[i] >= i, of K and V.  A CTA takes slices of the rows' 16-byte
+// chunks and walks the destinations upwards; a step's reads come before its writes, and later
+// steps read rows past what earlier ones have written.  Bound by memory.
+#include <algorithm>
+
 #include "dv_ops.h"
 
 namespace dv {
 namespace {
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveCells = 8;  // 16-byte chunks in flight per thread
+constexpr int kEvictThreads = 512;  // two CTAs an SM
+constexpr int kWarps = kEvictThreads / 32;
+constexpr int kCells = 8;           // 16-byte chunks in flight per thread
+constexpr int kBins = 2048;         // of 11 bits of a key
+constexpr int kMaxCluster = 8;      // CTAs of a unit
+constexpr int kHeld = 24 * 1024;    // weights of a CTA in shared memory, where two fit an SM
+constexpr int kMostHeld = 50 * 1024;
+constexpr int kLeastRun = 512;      // rows of a CTA below which a unit has no more of them
 
 template <int MAXB>
 struct EvictTable {
@@ -31,11 +40,16 @@ struct EvictTable {
 };
 
 template <int MAXB>
-struct SelectParams {
+struct EvictParams {
+  uint4* k;
+  uint4* v;
   const float* mass;
   float* mass_out;  // may be mass
   int32_t* keep;    // [layer][H][T]
-  int32_t H, S, sinks, recent;
+  int64_t layer_chunks;
+  int32_t l0, H, C, S, sinks, recent;
+  int32_t ctas;           // of a unit
+  int32_t slice, slices;  // chunks that a CTA copies at a time, slices of a row
   EvictTable<MAXB> seq;
 };
 
@@ -46,14 +60,46 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u ^ ((u >> 31) ? ~0u : 0x80000000u);
 }
 
-template <int MAXB>
-__global__ __launch_bounds__(kSelectThreads) void select_kernel(
-    const __grid_constant__ SelectParams<MAXB> p) {
-  __shared__ uint32_t hist[256];
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at the same place in another CTA's shared memory.
+__device__ __forceinline__ uint32_t remote_word(const uint32_t* mine, int rank) {
+  uint32_t addr, x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(addr)
+               : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+  return x;
+}
+
+// A 16-byte load whose miss fetches 64 bytes from memory: of K's chunk rows a few scattered
+// chunks are read.
+__device__ __forceinline__ uint4 load_sparse(const uint4* src) {
+  uint4 x;
+  asm volatile("ld.global.cg.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(src)
+               : "memory");
+  return x;
+}
+
+// HELD: the weights are in shared memory (else there is one CTA a unit, which reads them from
+// memory each time).
+template <int MAXB, bool HELD>
+__global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
+    const __grid_constant__ EvictParams<MAXB> p) {
+  extern __shared__ float held[];
+  __shared__ uint32_t hist[kBins];
   __shared__ uint32_t border[3];  // the bits found, how many at them fit, how many there are
-  __shared__ uint2 totals[2][kSelectWarps];
+  __shared__ uint32_t sums[kWarps];
+  __shared__ uint2 totals[2][kWarps];
+  __shared__ uint32_t counts[2];  // of this CTA: rows above the border and at it
   ops_pdl_enter();
-  const int B = p.seq.batch, b = blockIdx.x % B, lh = blockIdx.x / B;
+  const int ctas = p.ctas, rank = HELD ? (int)(blockIdx.x % ctas) : 0;
+  const int unit = HELD ? blockIdx.x / ctas : blockIdx.x;
+  const int B = p.seq.batch, b = unit % B, lh = unit / B;
   const int l = lh / p.H, h = lh - l * p.H;
   const int n = p.seq.rows[b], m = p.seq.pre[b + 1] - p.seq.pre[b];
   const int64_t at = (((int64_t)l * B + b) * p.H + h) * p.S;
@@ -61,39 +107,69 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(
   float* const out = p.mass_out + at;
   int32_t* const keep = p.keep + (int64_t)lh * p.seq.pre[B] + p.seq.pre[b];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (n == m) {
-    for (int i = tid; i < n; i += kSelectThreads) {
+  const auto sync = [&]() {
+    if (HELD && ctas > 1) cluster_sync(); else __syncthreads();
+  };
+  // this CTA's rows [lo, hi)
+  const int run = (n + ctas - 1) / ctas, lo = min(rank * run, n), hi = min(lo + run, n);
+  if (n == m) {  // (the same for every CTA of the cluster)
+    for (int i = lo + tid; i < hi; i += kEvictThreads) {
       keep[i] = i;
       out[i] = mass[i];
     }
     return;
   }
+  if (HELD) {
+#pragma unroll 8
+    for (int i = lo + tid; i < hi; i += kEvictThreads) held[i - lo] = mass[i];
+    __syncthreads();
+  }
+  const auto weight = [&](int i) { return HELD ? held[i - lo] : mass[i]; };
+
+  // ---- the border ----
   const int c0 = p.sinks, c1 = n - p.recent;
   uint32_t need = m - p.sinks - p.recent, bits = 0, mask = 0;
   if (need == 0) {
     bits = mask = ~0u;
   } else {
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+    for (int shift = 21;; shift = shift == 21 ? 10 : 0) {  // 11, 11 and the last 10 bits
+      const uint32_t field = shift == 0 ? 1023u : 2047u;
+#pragma unroll
+      for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = c0 + tid; i < c1; i += kSelectThreads) {
-        const uint32_t key = order_key(mass[i]);
-        if ((key & mask) == bits) atomicAdd(&hist[key >> shift & 255], 1u);
+#pragma unroll 4
+      for (int i = max(lo, c0) + tid; i < min(hi, c1); i += kEvictThreads) {
+        const uint32_t key = order_key(weight(i));
+        if ((key & mask) == bits) atomicAdd(&hist[key >> shift & field], 1u);
       }
-      __syncthreads();
-      if (warp == 0) {  // a lane's eight values, the largest first
-        uint32_t mine[8], sum = 0;
-        for (int e = 0; e < 8; ++e) sum += mine[e] = hist[255 - 8 * lane - e];
-        uint32_t before = sum;
-        for (int d = 1; d < 32; d *= 2) {
-          const uint32_t x = __shfl_up_sync(~0u, before, d);
-          if (lane >= d) before += x;
-        }
-        before -= sum;
-        for (int e = 0; e < 8; ++e) {
+      sync();
+      // four bins a thread, the largest first
+      uint32_t mine[4] = {}, sum = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t* const bin = &hist[kBins - 1 - 4 * tid - e];
+        if (HELD && ctas > 1)
+          for (int r = 0; r < ctas; ++r) mine[e] += remote_word(bin, r);
+        else
+          mine[e] = *bin;
+        sum += mine[e];
+      }
+      uint32_t before = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const uint32_t x = __shfl_up_sync(~0u, before, d);
+        if (lane >= d) before += x;
+      }
+      if (lane == 31) sums[warp] = before;
+      sync();  // (the histograms have been read)
+      before -= sum;
+      for (int w = 0; w < warp; ++w) before += sums[w];
+      if (before < need && need <= before + sum) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
           if (before < need && need <= before + mine[e]) {
-            border[0] = 255 - 8 * lane - e;
+            border[0] = kBins - 1 - 4 * tid - e;
             border[1] = need - before;
             border[2] = mine[e];
           }
@@ -102,101 +178,141 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(
       }
       __syncthreads();
       bits |= border[0] << shift;
-      mask |= 255u << shift;
+      mask |= field << shift;
       need = border[1];
-      if (border[2] == need) break;  // all of them fit
+      if (shift == 0 || border[2] == need) break;  // (then all of them fit)
     }
   }
-  // Places: kept rows before this one.
-  uint32_t above = 0, level = 0;  // above the border (or first, or last), and at it, so far
-  for (int base = 0, turn = 0; base < n; base += kSelectThreads, turn ^= 1) {
-    const int i = base + tid;
-    const float x = i < n ? mass[i] : 0.f;
+
+  // ---- places: kept rows before each one ----
+  const auto side = [&](int i, int end, float x, bool* above, bool* level) {
     const uint32_t key = order_key(x) & mask;
     const bool candidate = i >= c0 && i < c1;
-    const bool hi = i < n && (!candidate || key > bits), eq = candidate && key == bits;
-    const uint32_t his = __ballot_sync(~0u, hi), eqs = __ballot_sync(~0u, eq);
-    if (lane == 0) totals[turn][warp] = make_uint2(__popc(his), __popc(eqs));
+    *above = i < end && (!candidate || key > bits);
+    *level = i < end && candidate && key == bits;
+  };
+  const uint32_t lower = (1u << lane) - 1;
+  if constexpr (HELD) {
+    // a warp's rows [w0, w1)
+    const int part = ((run + kWarps - 1) / kWarps + 31) & ~31;
+    const int w0 = min(lo + warp * part, hi), w1 = min(w0 + part, hi);
+    uint32_t a = 0, e = 0;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+      bool up, eq;
+      side(i0 + lane, w1, i0 + lane < w1 ? weight(i0 + lane) : 0.f, &up, &eq);
+      a += __popc(__ballot_sync(~0u, up));
+      e += __popc(__ballot_sync(~0u, eq));
+    }
+    if (lane == 0) totals[0][warp] = make_uint2(a, e);
     __syncthreads();
-    uint32_t a = above, e = level;
-    for (int w = 0; w < kSelectWarps; ++w) {
-      const uint2 t = totals[turn][w];
+    a = e = 0;
+    uint32_t all_a = 0, all_e = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      const uint2 t = totals[0][w];
       if (w < warp) {
         a += t.x;
         e += t.y;
       }
-      above += t.x;
-      level += t.y;
+      all_a += t.x;
+      all_e += t.y;
     }
-    a += __popc(his & ((1u << lane) - 1));
-    e += __popc(eqs & ((1u << lane) - 1));
-    if (hi || (eq && e < need)) {
-      const uint32_t to = a + min(e, need);
-      keep[to] = i;
-      out[to] = x;
+    if (ctas > 1) {
+      if (tid == 0) {
+        counts[0] = all_a;
+        counts[1] = all_e;
+      }
+      cluster_sync();
+      for (int r = 0; r < rank; ++r) {
+        a += remote_word(&counts[0], r);
+        e += remote_word(&counts[1], r);
+      }
     }
-  }
-  __syncthreads();
-  for (int i = m + tid; i < n; i += kSelectThreads) out[i] = 0.f;
-}
-
-template <int MAXB>
-struct MoveParams {
-  uint4* k;
-  uint4* v;
-  const int32_t* keep;
-  int64_t layer_chunks;
-  int32_t l0, H, C, S;
-  int32_t slice, slices;  // chunks of a CTA, slices of a row
-  EvictTable<MAXB> seq;
-};
-
-template <int MAXB>
-__global__ __launch_bounds__(kMoveThreads) void move_kernel(
-    const __grid_constant__ MoveParams<MAXB> p) {
-  ops_pdl_enter();
-  // block = (((layer * 2 + kv) * batch + b) * H + h) * slices + slice
-  int64_t x = blockIdx.x;
-  const int slice = (int)(x % p.slices);
-  x /= p.slices;
-  const int h = (int)(x % p.H);
-  x /= p.H;
-  const int b = (int)(x % p.seq.batch);
-  x /= p.seq.batch;
-  const bool is_k = (x & 1) == 0;
-  const int l = (int)(x >> 1);
-  const int n = p.seq.rows[b], m = p.seq.pre[b + 1] - p.seq.pre[b];
-  if (n == m) return;
-  const int c0 = slice * p.slice, cw = min(p.slice, p.C - c0);
-  uint4* const base = (is_k ? p.k : p.v) + (p.l0 + l) * p.layer_chunks +
-                      ((int64_t)b * p.H + h) * p.C * p.S;
-  const int32_t* const keep =
-      p.keep + ((int64_t)l * p.H + h) * p.seq.pre[p.seq.batch] + p.seq.pre[b];
-  const int step = kMoveThreads * kMoveCells / cw;
-  for (int i0 = 0; i0 < m; i0 += step) {
-    const int rows = min(step, m - i0), cells = rows * cw;
-    uint4 y[kMoveCells];
-    int64_t to[kMoveCells];
-#pragma unroll
-    for (int u = 0; u < kMoveCells; ++u) {
-      const int j = u * kMoveThreads + threadIdx.x;
-      to[u] = -1;
-      if (j < cells) {
-        // K: a thread per row, then the next chunk; V: a row's chunks side by side
-        const int outer = is_k ? j / rows : j / cw, inner = j - outer * (is_k ? rows : cw);
-        const int dst = i0 + (is_k ? inner : outer), c = c0 + (is_k ? outer : inner);
-        const int src = keep[dst];
-        if (src > dst) {
-          const int64_t row = is_k ? (int64_t)c * p.S : c, pitch = is_k ? 1 : p.C;
-          y[u] = base[row + src * pitch];
-          to[u] = row + dst * pitch;
+    // (every weight has been read from memory: they may be overwritten)
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+      const int i = i0 + lane;
+      const float x = i < w1 ? weight(i) : 0.f;
+      bool up, eq;
+      side(i, w1, x, &up, &eq);
+      const uint32_t ups = __ballot_sync(~0u, up), eqs = __ballot_sync(~0u, eq);
+      const uint32_t at_i = e + __popc(eqs & lower);
+      if (up || (eq && at_i < need)) {
+        const uint32_t to = a + __popc(ups & lower) + min(at_i, need);
+        keep[to] = i;
+        out[to] = x;
+      }
+      a += __popc(ups);
+      e += __popc(eqs);
+    }
+  } else {
+    // in order of rows, so that none is overwritten before it is read
+    uint32_t above = 0, level = 0;
+    for (int base = 0, turn = 0; base < n; base += kEvictThreads, turn ^= 1) {
+      const int i = base + tid;
+      const float x = i < n ? mass[i] : 0.f;
+      bool up, eq;
+      side(i, n, x, &up, &eq);
+      const uint32_t ups = __ballot_sync(~0u, up), eqs = __ballot_sync(~0u, eq);
+      if (lane == 0) totals[turn][warp] = make_uint2(__popc(ups), __popc(eqs));
+      __syncthreads();
+      uint32_t a = above, e = level;
+      for (int w = 0; w < kWarps; ++w) {
+        const uint2 t = totals[turn][w];
+        if (w < warp) {
+          a += t.x;
+          e += t.y;
         }
+        above += t.x;
+        level += t.y;
+      }
+      a += __popc(ups & lower);
+      e += __popc(eqs & lower);
+      if (up || (eq && e < need)) {
+        const uint32_t to = a + min(e, need);
+        keep[to] = i;
+        out[to] = x;
       }
     }
     __syncthreads();
+  }
+  for (int i = max(m, lo) + tid; i < hi; i += kEvictThreads) out[i] = 0.f;
+  sync();  // the list is complete (and no CTA leaves while others read its counts)
+
+  // ---- the copy ----
+#pragma unroll 1
+  for (int part = rank; part < 2 * p.slices; part += ctas) {
+    const bool is_k = part < p.slices;
+    const int c0 = (is_k ? part : part - p.slices) * p.slice, cw = min(p.slice, p.C - c0);
+    uint4* const base = (is_k ? p.k : p.v) + (p.l0 + l) * p.layer_chunks +
+                        ((int64_t)b * p.H + h) * p.C * p.S;
+    const int step = kEvictThreads * kCells / cw;
+#pragma unroll 1
+    for (int i0 = 0; i0 < m; i0 += step) {
+      const int rows = min(step, m - i0), cells = rows * cw;
+      // K: a thread per row, then the next chunk; V: a row's chunks side by side.  The quotient
+      // by a multiplication (exact: the cells and the divisor are at most 2^12).
+      const uint32_t inner = is_k ? rows : cw, inv = (uint32_t)(((1ull << 32) + inner - 1) / inner);
+      uint4 y[kCells];
+      int64_t to[kCells];
 #pragma unroll
-    for (int u = 0; u < kMoveCells; ++u)
-      if (to[u] >= 0) base[to[u]] = y[u];
+      for (int u = 0; u < kCells; ++u) {
+        const uint32_t j = u * kEvictThreads + tid;
+        to[u] = -1;
+        if (j < (uint32_t)cells) {
+          const int outer = inner == 1 ? (int)j : (int)__umulhi(j, inv), rest = (int)(j - outer * inner);
+          const int dst = i0 + (is_k ? rest : outer), c = c0 + (is_k ? outer : rest);
+          const int src = keep[dst];
+          if (src > dst) {
+            const int64_t row = is_k ? (int64_t)c * p.S : c, pitch = is_k ? 1 : p.C;
+            y[u] = is_k ? load_sparse(base + row + src) : base[row + src * pitch];
+            to[u] = row + dst * pitch;
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kCells; ++u)
+        if (to[u] >= 0) base[to[u]] = y[u];
+    }
   }
 }
 
@@ -210,38 +326,66 @@ void fill_table(const Plan& p, EvictTable<MAXB>* t) {  // the plan's ranges: [ke
   }
 }
 
+template <int MAXB, bool HELD>
+cudaError_t launch_kernel(const EvictParams<MAXB>& kp, int64_t units, size_t smem,
+                          cudaStream_t stream) {
+  void (*const kernel)(EvictParams<MAXB>) = evict_kernel<MAXB, HELD>;
+  cudaError_t err = cudaSuccess;
+  if (HELD)
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * kp.ctas));
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)kp.ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kp.ctas > 1 ? 2 : 1;
+  err = cudaLaunchKernelEx(&cfg, kernel, kp);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 template <int MAXB>
 cudaError_t launch_evict(const Plan& p, int32_t sinks, int32_t recent, const float* mass,
                          float* mass_out, int32_t* keep, cudaStream_t stream) {
-  SelectParams<MAXB> sp;
-  sp.mass = mass;
-  sp.mass_out = mass_out;
-  sp.keep = keep;
-  sp.H = p.H;
-  sp.S = p.S;
-  sp.sinks = sinks;
-  sp.recent = recent;
-  fill_table(p, &sp.seq);
+  EvictParams<MAXB> kp;
+  kp.k = static_cast<uint4*>(p.k);
+  kp.v = static_cast<uint4*>(p.v);
+  kp.mass = mass;
+  kp.mass_out = mass_out;
+  kp.keep = keep;
+  kp.layer_chunks = p.layer_chunks;
+  kp.l0 = p.l0;
+  kp.H = p.H;
+  kp.C = p.C;
+  kp.S = p.S;
+  kp.sinks = sinks;
+  kp.recent = recent;
+  fill_table(p, &kp.seq);
+  // As many CTAs a unit as hold its weights, and where there are few units as fill the SMs
+  // with runs of kLeastRun rows.
   const int64_t units = (int64_t)(p.l1 - p.l0) * p.H * p.B;
-  cudaError_t err = ops_launch(select_kernel<MAXB>, dim3((unsigned)units), kSelectThreads, 0,
-                               stream, sp);
-  if (err != cudaSuccess || p.tokens == 0) return err;  // no row goes: none is moved
-  MoveParams<MAXB> mp;
-  mp.k = static_cast<uint4*>(p.k);
-  mp.v = static_cast<uint4*>(p.v);
-  mp.keep = keep;
-  mp.layer_chunks = p.layer_chunks;
-  mp.l0 = p.l0;
-  mp.H = p.H;
-  mp.C = p.C;
-  mp.S = p.S;
-  mp.seq = sp.seq;
-  int slice = p.C < 16 ? p.C : 16;
-  while (slice > 2 && 2 * units * ((p.C + slice - 1) / slice) < 152 * 6) slice = (slice + 1) / 2;
-  mp.slice = slice;
-  mp.slices = (p.C + slice - 1) / slice;
-  return ops_launch(move_kernel<MAXB>, dim3((unsigned)(2 * units * mp.slices)), kMoveThreads, 0,
-                    stream, mp);
+  int32_t most = 0;
+  for (int b = 0; b < p.B; ++b) most = std::max(most, kp.seq.rows[b]);
+  int ctas = 1;
+  while (ctas < kMaxCluster && (most > ctas * kHeld || (most > ctas * kLeastRun &&
+                                                        units * ctas * 2 <= 2 * 152)))
+    ctas *= 2;
+  const int64_t run = ((int64_t)most + ctas - 1) / ctas;
+  const bool held = run <= kMostHeld;
+  kp.ctas = held ? ctas : 1;
+  // Each CTA copies a slice of K and one of V, of 32 to 256 bytes a row.
+  int slices = std::max((p.C + 15) / 16, kp.ctas);
+  kp.slice = std::max((p.C + slices - 1) / slices, std::min(2, p.C));
+  kp.slices = (p.C + kp.slice - 1) / kp.slice;
+  return held ? launch_kernel<MAXB, true>(kp, units, (size_t)run * 4, stream)
+              : launch_kernel<MAXB, false>(kp, units, 0, stream);
 }
 
 }  // namespace
@@ -267,7 +411,7 @@ extern "C" dv_status dv_kv_evict(const dv_cache* cache, int32_t l0, int32_t l1,
     used += (int64_t)p.seq_start[b] + p.seq_len[b];
   }
   const int64_t heads = (int64_t)(l1 - l0) * p.H;
-  if (heads > INT32_MAX / p.B || heads * p.B > INT32_MAX / (2 * ((p.C + 1) / 2)) ||
+  if (heads > INT32_MAX / p.B || heads * p.B > INT32_MAX / (2 * std::max(dv::kMaxCluster, (p.C + 1) / 2)) ||
       total > INT32_MAX)
     return dv::fail(DV_ERR_UNSUPPORTED, "%d layers, %d sequences, %d heads of %d chunks, %lld rows",
                     l1 - l0, p.B, p.H, p.C, (long long)total);

@@ -15,9 +15,9 @@
 // (token, head of the group) rows that attend some of them, in tiles of 128.  The units form
 // one line, each as long as its tiles and unit cost, cut into equal stretches, one a CTA (one
 // CTA an SM); a unit that a cut divides leaves partial sums, which mass_join_kernel adds in
-// order (no atomics: the same bits each time).  Warps 0-7 sum, two to a quarter of the rows with
-// half of the columns each; 8 loads (and walks over the units), 9 issues the products into four
-// buffers of tensor memory, 10 fetches lse.
+// order (no atomics: the same bits each time).  Warps 0-7 sum one tile, two to a quarter of the
+// rows with half of the columns each, 8-15 the next; 16 loads (and walks over the units), 17
+// issues the products into four buffers of tensor memory, 18 fetches lse.
 //
 // Every wait gives up after a number of tries, as in the attention kernel.
 #include <algorithm>
@@ -34,9 +34,10 @@ namespace {
 
 // Rows (new tokens x heads of a group) up to which the scores are kept.
 constexpr int kFewRows = 16;
-constexpr int kFewThreads = 256;
-constexpr int kMassThreads = 352;
-constexpr int kSumWarps = 8;
+constexpr int kFewThreads = 256, kFewPer = 4;
+constexpr int kTileWarps = 8;   // that sum a tile: a quarter of the rows, half of the columns each
+constexpr int kSumWarps = 16;   // two such sets, for every other tile
+constexpr int kMassThreads = 32 * (kSumWarps + 3);
 // What a unit costs besides its tiles (its keys' fetch, the sums' exchange), in tiles.
 constexpr int kMassUnitCost = 1;
 
@@ -92,7 +93,7 @@ struct MassSmem {
   static constexpr int kCtl = kQAt + kQ * kSlot;
   struct Ctl {
     float lse[kL][kTile];  // negative
-    float sum[2][kTile];   // of the second half of the columns
+    float sum[2][3][kTile];  // of the other halves and sets
     uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ], s_full[kS], s_empty[kS];
     uint64_t lse_full[kL], lse_empty[kL], sum_full[2], sum_empty[2];
     uint64_t item_full[kItems], item_empty[kItems], drained;
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
   const auto at = [&](const uint64_t& bar) {
     return base + (uint32_t)(reinterpret_cast<const uint8_t*>(&bar) - sm);
   };
-  if (warp == 8) {
+  if (warp == kSumWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      base + (uint32_t)(reinterpret_cast<uint8_t*>(&ctl.tmem) - sm)),
                  "r"(512u));
@@ -220,14 +221,14 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     }
     for (int i = 0; i < SM::kS; ++i) {
       bar_init(at(ctl.s_full[i]), 1);
-      bar_init(at(ctl.s_empty[i]), kSumWarps);
+      bar_init(at(ctl.s_empty[i]), kTileWarps);
     }
     for (int i = 0; i < SM::kL; ++i) {
       bar_init(at(ctl.lse_full[i]), 1);
-      bar_init(at(ctl.lse_empty[i]), kSumWarps);
+      bar_init(at(ctl.lse_empty[i]), kTileWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(at(ctl.sum_full[i]), kTile);
+      bar_init(at(ctl.sum_full[i]), 3 * kTile);
       bar_init(at(ctl.sum_empty[i]), kTile);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     if (lane == 0) bar_arrive(at(ctl.item_empty[k % kItems]));
   };
 
-  if (warp == 8) {
+  if (warp == kSumWarps) {
     // ---- the walk, and loads ----
     const bool on = elect();
     MassWalk<MassParams<MAXB>> walk(p, cut(p, blockIdx.x), cut(p, blockIdx.x + 1));
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     for (uint32_t i = 0; i < SM::kQ && i < nq; ++i)
       bar_wait(at(ctl.q_full[i]), (nq - i - 1) / SM::kQ & 1, kSpinLimit);
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kSumWarps + 1) {
     // ---- products: S^T = K Q^T ----
     const bool on = elect();
     constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
@@ -371,7 +372,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     mma_commit(at(ctl.drained), on);
     bar_wait(at(ctl.drained), 0, kSpinLimit);
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == kSumWarps + 2) {
     // ---- lse of each tile's rows ----
     Ring<SM::kL> lr;
     uint32_t n_items = 0, nl = 0;
@@ -397,22 +398,24 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       done_item(n_items++);
     }
   } else {
-    // ---- sums: a key per thread, half of the columns ----
-    const int half = warp >> 2, r = threadIdx.x & (kTile - 1);
+    // ---- sums: a key per thread, half of the columns, of every other tile ----
+    const int half = warp >> 2 & 1, set = warp >> 3, part = warp >> 2;
+    const int r = threadIdx.x & (kTile - 1);
     const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + half * (kTile / 2);
     Ring<SM::kS> sr;
     Ring<SM::kL> lr;
-    uint32_t item = 0;
+    uint32_t item = 0, tiles = 0;  // tiles of the items before
     bool ok = true;
     MassItem it;
     for (; ok && get_item(item, &it); ++item) {
       const int row = it.row0 + r;
       float* const mass = p.mass + ((int64_t)it.b * p.H + it.h) * p.S + row;
-      const bool write = half == 0 && row < it.row_end;
+      const bool write = part == 0 && row < it.row_end;
       const float old = write && it.whole ? *mass : 0.f;
       float total = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < it.n; ++j) {
+      for (int j = 0; j < it.n; ++j, ++tiles, sr.next(), lr.next()) {
+        if ((int)(tiles & 1) != set) continue;
         if (!(ok = wait(at(ctl.s_full[sr.slot]), sr.turn))) break;
         fence_after();
         uint32_t x[kTile / 2];
@@ -422,7 +425,6 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(at(ctl.s_empty[sr.slot]));
-        sr.next();
         if (!(ok = wait(at(ctl.lse_full[lr.slot]), lr.turn))) break;
         const float4* const nl =
             reinterpret_cast<const float4*>(ctl.lse[lr.slot] + half * (kTile / 2));
@@ -454,17 +456,16 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
         total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         __syncwarp();
         if (lane == 0) bar_arrive(at(ctl.lse_empty[lr.slot]));
-        lr.next();
       }
       if (!ok) break;
       const uint32_t x = item & 1, parity = item >> 1 & 1;
-      if (half == 1) {
+      if (part > 0) {
         if (item >= 2 && !(ok = wait(at(ctl.sum_empty[x]), parity ^ 1))) break;
-        ctl.sum[x][r] = total;
+        ctl.sum[x][part - 1][r] = total;
         bar_arrive(at(ctl.sum_full[x]));
       } else {
         if (!(ok = wait(at(ctl.sum_full[x]), parity))) break;
-        total += ctl.sum[x][r];
+        total += ctl.sum[x][0][r] + (ctl.sum[x][1][r] + ctl.sum[x][2][r]);
         bar_arrive(at(ctl.sum_empty[x]));
         if (it.whole) {
           if (write) *mass = old + total;
@@ -478,7 +479,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 8)
+  if (warp == kSumWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
@@ -507,7 +508,8 @@ struct FewParams {
   int32_t block_pre[MAXB + 1];
 };
 
-// A thread per cache row; a CTA per (sequence, key head, kFewThreads rows).
+// kFewPer cache rows a thread, kFewThreads apart, whose loads are in flight together; a CTA per
+// (sequence, key head, kFewThreads * kFewPer rows).
 template <int MAXB>
 __global__ __launch_bounds__(kFewThreads) void few_kernel(
     const __grid_constant__ FewParams<MAXB> p) {
@@ -515,19 +517,32 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(
   const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x - bh * p.chunks;
   const int b = bh / p.H, h = bh - b * p.H;
   const int start = p.seq.start[b], t0 = p.seq.pre[b], n = p.seq.pre[b + 1] - t0;
-  const int row = chunk * kFewThreads + threadIdx.x, row_end = start + n;
-  if (n == 0 || row >= row_end) return;
+  const int row0 = chunk * (kFewThreads * kFewPer) + threadIdx.x, row_end = start + n;
+  if (n == 0 || row0 >= row_end) return;
   const int64_t pitch = (int64_t)((row_end + kTile - 1) / kTile) * kTile;
   const float* s = p.scores + kTile * (int64_t)p.block_pre[b] * (p.H * p.G) +
-                   (int64_t)h * p.G * n * pitch + row;
+                   (int64_t)h * p.G * n * pitch + row0;
   const float* const lse = p.lse + ((int64_t)h * p.tokens + t0) * p.G;
-  const int first = first_token(start, n, p.last, row);
-  if (first >= n) return;
-  float sum = 0.f;
-  for (int g = 0; g < p.G; ++g)
-    for (int i = first; i < n; ++i)
-      sum += ex2(fmaf(s[(int64_t)(g * n + i) * pitch], p.c, -lse[i * p.G + g]));
-  p.mass[((int64_t)b * p.H + h) * p.S + row] += sum;
+  float* const mass = p.mass + ((int64_t)b * p.H + h) * p.S + row0;
+  const int c0 = first_counted(n, p.last);
+  float old[kFewPer], sum[kFewPer] = {};
+#pragma unroll
+  for (int e = 0; e < kFewPer; ++e)
+    old[e] = row0 + e * kFewThreads < row_end ? mass[e * kFewThreads] : 0.f;
+  for (int g = 0; g < p.G; ++g) {
+#pragma unroll 2
+    for (int i = c0; i < n; ++i) {
+      const float* const x = s + (int64_t)(g * n + i) * pitch;
+      const float nl = -lse[i * p.G + g];
+      const int end = start + i + 1;  // of the rows that the token attends
+#pragma unroll
+      for (int e = 0; e < kFewPer; ++e)
+        if (row0 + e * kFewThreads < end) sum[e] += ex2(fmaf(x[e * kFewThreads], p.c, nl));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kFewPer; ++e)
+    if (row0 + e * kFewThreads < row_end) mass[e * kFewThreads] = old[e] + sum[e];
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -578,7 +593,7 @@ int64_t few_chunks(const Plan& p) {
   int64_t rows = 0;
   for (int b = 0; b < p.B; ++b)
     if (p.seq_len[b] > 0) rows = std::max<int64_t>(rows, (int64_t)p.seq_start[b] + p.seq_len[b]);
-  return (rows + kFewThreads - 1) / kFewThreads;
+  return (rows + kFewThreads * kFewPer - 1) / (kFewThreads * kFewPer);
 }
 
 template <typename T, int DP, int MAXB>
