@@ -64,13 +64,25 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The word at the same place in another CTA's shared memory.
+// The word (four words) at the same place in another CTA's shared memory.
 __device__ __forceinline__ uint32_t remote_word(const uint32_t* mine, int rank) {
   uint32_t addr, x;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                : "=r"(addr)
                : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint4 remote_words(const uint32_t* mine, int rank) {
+  uint32_t addr;
+  uint4 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(addr)
+               : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(addr)
+               : "memory");
   return x;
 }
 
@@ -91,7 +103,7 @@ template <int MAXB, bool HELD>
 __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
     const __grid_constant__ EvictParams<MAXB> p) {
   extern __shared__ float held[];
-  __shared__ uint32_t hist[kBins];
+  __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ uint32_t border[3];  // the bits found, how many at them fit, how many there are
   __shared__ uint32_t sums[kWarps];
   __shared__ uint2 totals[2][kWarps];
@@ -145,16 +157,21 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
       }
       sync();
       // four bins a thread, the largest first
-      uint32_t mine[4] = {}, sum = 0;
+      const uint32_t* const bins = &hist[kBins - 4 - 4 * tid];
+      uint4 four = make_uint4(0, 0, 0, 0);
+      if (HELD && ctas > 1) {
+        uint4 of[kMaxCluster];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t* const bin = &hist[kBins - 1 - 4 * tid - e];
-        if (HELD && ctas > 1)
-          for (int r = 0; r < ctas; ++r) mine[e] += remote_word(bin, r);
-        else
-          mine[e] = *bin;
-        sum += mine[e];
+        for (int r = 0; r < kMaxCluster; ++r)
+          of[r] = r < ctas ? remote_words(bins, r) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          four = make_uint4(four.x + of[r].x, four.y + of[r].y, four.z + of[r].z, four.w + of[r].w);
+      } else {
+        four = *reinterpret_cast<const uint4*>(bins);
       }
+      const uint32_t mine[4] = {four.w, four.z, four.y, four.x};
+      const uint32_t sum = (four.x + four.y) + (four.z + four.w);
       uint32_t before = sum;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -164,7 +181,8 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
       if (lane == 31) sums[warp] = before;
       sync();  // (the histograms have been read)
       before -= sum;
-      for (int w = 0; w < warp; ++w) before += sums[w];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) before += w < warp ? sums[w] : 0;
       if (before < need && need <= before + sum) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -192,11 +210,13 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
     *level = i < end && candidate && key == bits;
   };
   const uint32_t lower = (1u << lane) - 1;
+  const bool listed = ctas == 1 && m <= kBins;  // the list is kept in place of the histogram too
   if constexpr (HELD) {
     // a warp's rows [w0, w1)
     const int part = ((run + kWarps - 1) / kWarps + 31) & ~31;
     const int w0 = min(lo + warp * part, hi), w1 = min(w0 + part, hi);
     uint32_t a = 0, e = 0;
+#pragma unroll 4
     for (int i0 = w0; i0 < w1; i0 += 32) {
       bool up, eq;
       side(i0 + lane, w1, i0 + lane < w1 ? weight(i0 + lane) : 0.f, &up, &eq);
@@ -238,6 +258,7 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
       if (up || (eq && at_i < need)) {
         const uint32_t to = a + __popc(ups & lower) + min(at_i, need);
         keep[to] = i;
+        if (listed) hist[to] = i;
         out[to] = x;
       }
       a += __popc(ups);
@@ -269,6 +290,7 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
       if (up || (eq && e < need)) {
         const uint32_t to = a + min(e, need);
         keep[to] = i;
+        if (listed) hist[to] = i;
         out[to] = x;
       }
     }
@@ -300,7 +322,7 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
         if (j < (uint32_t)cells) {
           const int outer = inner == 1 ? (int)j : (int)__umulhi(j, inv), rest = (int)(j - outer * inner);
           const int dst = i0 + (is_k ? rest : outer), c = c0 + (is_k ? outer : rest);
-          const int src = keep[dst];
+          const int src = listed ? (int)hist[dst] : keep[dst];
           if (src > dst) {
             const int64_t row = is_k ? (int64_t)c * p.S : c, pitch = is_k ? 1 : p.C;
             y[u] = is_k ? load_sparse(base + row + src) : base[row + src * pitch];

@@ -98,7 +98,7 @@ CASES = [
     (1, 1, 2, 128, 40000, 2, [39999], [5000], 4, 1000, "few"),
     (1, 2, 1, 64, 9000, 2, [8999, 8192], [8998, 100], 4, 0, "ties"),
     (1, 2, 2, 128, 30000, 2, [29999, 20000], [5000, 19999], 4, 1000, "ties"),
-    (1, 1, 1, 16, 420000, 2, [419999], [2000], 4, 100, "few"),   # more than a cluster's shared memory holds
+    (1, 1, 1, 16, 420000, 2, [419999], [2000], 4, 100, "few"), 
     (8, 4, 40, 64, 200, 2, [200, 150, 199, 60], [100, 60, 198, 60], 4, 16, "few"),
 ]
 
