@@ -11,13 +11,14 @@
 //     that a thread that owns a key sums along its row of tensor memory and nothing is reduced
 //     across threads.
 //
-// mass_kernel: a unit of work is 128 cache rows of a (sequence, key head), against the counted
-// (token, head of the group) rows that attend some of them, in tiles of 128.  The units form
-// one line, each as long as its tiles and unit cost, cut into equal stretches, one a CTA (one
-// CTA an SM); a unit that a cut divides leaves partial sums, which mass_join_kernel adds in
-// order (no atomics: the same bits each time).  Warps 0-7 sum one tile, two to a quarter of the
-// rows with half of the columns each, 8-15 the next; 16 loads (and walks over the units), 17
-// issues the products into four buffers of tensor memory, 18 fetches lse.
+// mass_kernel: a unit of work is 256 cache rows of a (sequence, key head), two tiles of keys,
+// against the counted (token, head of the group) rows that attend some of them, in tiles of
+// 128: with one tile of keys, fetching the queries again for each bound it by L2.  The units
+// form one line, each as long as its tiles and unit cost, cut into equal stretches, one a CTA
+// (one CTA an SM); a unit that a cut divides leaves partial sums, which mass_join_kernel adds in
+// order (no atomics: the same bits each time).  Warps 0-3 and 4-7 sum the unit's two tiles of
+// keys, a key a thread; 8 loads (and walks over the units), 9 issues the products into two
+// buffers of tensor memory for each tile, 10 fetches lse.
 //
 // Every wait gives up after a number of tries, as in the attention kernel.
 #include <algorithm>
@@ -35,8 +36,8 @@ namespace {
 // Rows (new tokens x heads of a group) up to which the scores are kept.
 constexpr int kFewRows = 16;
 constexpr int kFewThreads = 256, kFewPer = 4;
-constexpr int kTileWarps = 8;   // that sum a tile: a quarter of the rows, half of the columns each
-constexpr int kSumWarps = 16;   // two such sets, for every other tile
+constexpr int kUnit = 2 * kTile;  // rows of a unit of mass_kernel
+constexpr int kSumWarps = 8;
 constexpr int kMassThreads = 32 * (kSumWarps + 3);
 // What a unit costs besides its tiles (its keys' fetch, the sums' exchange), in tiles.
 constexpr int kMassUnitCost = 1;
@@ -55,7 +56,7 @@ struct MassParams {
   const uint4* k;
   const float* lse;  // [H][T][G]
   float* mass;       // [B][H][S]
-  float* part;       // two slots of kTile sums a CTA
+  float* part;       // two slots of kUnit sums a CTA
   MassDivided* divided;
   int32_t share, extra;
   int32_t H, G, C, S;
@@ -78,7 +79,7 @@ __host__ __device__ __forceinline__ int first_token(int start, int n, int last, 
 }
 
 struct MassItem {
-  int b, h, row0;   // the unit's rows [row0, row0 + kTile)
+  int b, h, row0;   // the unit's rows [row0, row0 + kUnit)
   int row_end;      // of the sequence
   int tok0, n;      // the piece's first token; its tiles of tokens (0: no more items)
   int whole;
@@ -88,14 +89,14 @@ struct MassItem {
 template <int DP>
 struct MassSmem {
   static constexpr int kSlot = kTile * DP * 2;
-  static constexpr int kK = 2, kQ = 4, kS = 4, kL = 8;  // tiles of K and Q, sums, lse
+  static constexpr int kK = 4, kQ = DP == 128 ? 3 : 6;  // tiles of K and Q held
+  static constexpr int kS = 2, kL = 4;  // sums of each tile of keys, lse
   static constexpr int kQAt = kK * kSlot;
   static constexpr int kCtl = kQAt + kQ * kSlot;
   struct Ctl {
     float lse[kL][kTile];  // negative
-    float sum[2][3][kTile];  // of the other halves and sets
-    uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ], s_full[kS], s_empty[kS];
-    uint64_t lse_full[kL], lse_empty[kL], sum_full[2], sum_empty[2];
+    uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ];
+    uint64_t s_full[2][kS], s_empty[2][kS], lse_full[kL], lse_empty[kL];
     uint64_t item_full[kItems], item_empty[kItems], drained;
     MassItem item[kItems];
     uint32_t tmem;
@@ -114,7 +115,7 @@ struct MassWalk {
     return (p.seq.pre[b + 1] - p.seq.pre[b] - first + p.tile_tok - 1) / p.tile_tok;
   }
   __device__ int token0() const {
-    return first_token(p.seq.start[b], p.seq.pre[b + 1] - p.seq.pre[b], p.last, kt * kTile);
+    return first_token(p.seq.start[b], p.seq.pre[b + 1] - p.seq.pre[b], p.last, kt * kUnit);
   }
 
   __device__ MassWalk(const P& p_, int lo, int hi) : p(p_), pos(lo), end(hi) {
@@ -133,7 +134,7 @@ struct MassWalk {
     rem -= h * head;
     // the rows that every counted token attends: units of one cost
     const int c0 = first_counted(p.seq.pre[b + 1] - p.seq.pre[b], p.last);
-    const int flat = (p.seq.start[b] + c0) / kTile + 1, cost0 = kMassUnitCost + tiles(c0);
+    const int flat = (p.seq.start[b] + c0) / kUnit + 1, cost0 = kMassUnitCost + tiles(c0);
     kt = min(rem / cost0, flat);
     rem -= kt * cost0;
     if (kt == flat)
@@ -157,7 +158,7 @@ struct MassWalk {
     if (n <= 0) return;
     it->b = b;
     it->h = h;
-    it->row0 = kt * kTile;
+    it->row0 = kt * kUnit;
     it->row_end = start + n_tok;
     it->tok0 = first + t * p.tile_tok;
     it->n = n;
@@ -167,7 +168,7 @@ struct MassWalk {
     it->tok_at = at;
     pos += kMassUnitCost + cnt;
     t = 0;
-    if (++kt * kTile >= it->row_end) {
+    if (++kt * kUnit >= it->row_end) {
       kt = 0;
       if (++h == p.H) {
         h = 0;
@@ -176,6 +177,14 @@ struct MassWalk {
     }
   }
 };
+
+// The item's first tile of tokens of which some attend the unit's second tile of keys.
+template <typename P>
+__device__ __forceinline__ int second_from(const P& p, const MassItem& it) {
+  // tile j's last token is tok0 + (j + 1) tile_tok - 1, at most n_tok - 1
+  const int hidden = it.row0 + kTile - it.start - it.tok0;  // tokens before the first that does
+  return max(0, min(hidden / p.tile_tok, it.n - 1));
+}
 
 // (a, b) = (a, b) * c + (d, e)
 __device__ __forceinline__ void fma2(float& a, float& b, float c, float d, float e) {
@@ -219,17 +228,13 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       bar_init(at(ctl.q_full[i]), 1);
       bar_init(at(ctl.q_empty[i]), 1);
     }
-    for (int i = 0; i < SM::kS; ++i) {
-      bar_init(at(ctl.s_full[i]), 1);
-      bar_init(at(ctl.s_empty[i]), kTileWarps);
+    for (int i = 0; i < 2 * SM::kS; ++i) {
+      bar_init(at(ctl.s_full[i / SM::kS][i % SM::kS]), 1);
+      bar_init(at(ctl.s_empty[i / SM::kS][i % SM::kS]), 4);
     }
     for (int i = 0; i < SM::kL; ++i) {
       bar_init(at(ctl.lse_full[i]), 1);
-      bar_init(at(ctl.lse_empty[i]), kTileWarps);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(at(ctl.sum_full[i]), 3 * kTile);
-      bar_init(at(ctl.sum_empty[i]), kTile);
+      bar_init(at(ctl.lse_empty[i]), kSumWarps);
     }
     for (int i = 0; i < kItems; ++i) {
       bar_init(at(ctl.item_full[i]), 1);
@@ -265,11 +270,11 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       MassDivided d = {};
       const int from = cut(p, blockIdx.x - 1);
       if (walk.t > 0 && from <= walk.pos + kMassUnitCost) {
-        const int row0 = walk.kt * kTile;
+        const int row0 = walk.kt * kUnit;
         const int row_end = p.seq.start[walk.b] + p.seq.pre[walk.b + 1] - p.seq.pre[walk.b];
         const int end = walk.pos + kMassUnitCost + walk.tiles(walk.token0());
         d.at = ((int64_t)walk.b * p.H + walk.h) * p.S + row0;
-        d.rows = min(kTile, row_end - row0);
+        d.rows = min(kUnit, row_end - row0);
         d.last = blockIdx.x;
 #pragma unroll 1
         while (cut(p, d.last + 1) < end) ++d.last;
@@ -293,16 +298,17 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       }
       ++n_items;
       if (it.n == 0) break;
-      if (nk >= SM::kK && !(ok = wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1))) break;
-      {
+#pragma unroll 1
+      for (int row0 = it.row0; row0 < min(it.row0 + kUnit, it.row_end); row0 += kTile) {
+        if (nk >= SM::kK && !(ok = wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1))) break;
         const uint32_t bar = at(ctl.k_full[kr.slot]), dst = base + kr.slot * SM::kSlot;
-        const int head = it.b * p.H + it.h, rows = min(kTile, it.row_end - it.row0);
+        const int head = it.b * p.H + it.h, rows = min(kTile, it.row_end - row0);
         const int pad = p.C & 1;  // zeros for the other half of the last contraction step
         bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
         if (rows == kTile) {
-          tma_load4(dst, &p.k_map, 0, it.row0 / p.k_rows, 0, head, bar, on);
+          tma_load4(dst, &p.k_map, 0, row0 / p.k_rows, 0, head, bar, on);
         } else {
-          const uint4* src = p.k + (int64_t)head * p.C * p.S + it.row0;
+          const uint4* src = p.k + (int64_t)head * p.C * p.S + row0;
 #pragma unroll 1
           for (int c = 0; c < p.C; ++c)
             bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar, on);
@@ -311,6 +317,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
         kr.next();
         ++nk;
       }
+      if (!ok) break;
 #pragma unroll 1
       for (int j = 0; j < it.n; ++j) {
         if (nq >= SM::kQ && !(ok = wait(at(ctl.q_empty[qr.slot]), qr.turn ^ 1))) break;
@@ -340,32 +347,42 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     const int steps = (p.C + 1) / 2;
     Ring<SM::kK> kr;
     Ring<SM::kQ> qr;
-    Ring<SM::kS> sr;
-    uint32_t n_items = 0, ns = 0;
+    Ring<SM::kS> sr[2];
+    uint32_t n_items = 0, ns[2] = {};
     bool ok = true;
     MassItem it;
     while (ok && get_item(n_items, &it)) {
-      const int n = __shfl_sync(~0u, it.n, 0);
-      if (!(ok = wait(at(ctl.k_full[kr.slot]), kr.turn))) break;
-      const uint64_t kd = smem_desc(base + kr.slot * SM::kSlot, kTile * 16, 128, 0);
+      const int n = __shfl_sync(~0u, it.n, 0), row0 = __shfl_sync(~0u, it.row0, 0);
+      const int keys = __shfl_sync(~0u, it.row_end, 0) - row0 > kTile ? 2 : 1;
+      // the first tile of tokens that attends the second tile of keys
+      const int second = keys < 2 ? n : second_from(p, it);
+      Ring<SM::kK> kt[2] = {kr, kr};
+      kt[1].next();
+      for (int i = 0; i < keys; ++i) kr.next();
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         if (!(ok = wait(at(ctl.q_full[qr.slot]), qr.turn))) break;
-        if (ns >= SM::kS && !(ok = wait(at(ctl.s_empty[sr.slot]), sr.turn ^ 1))) break;
-        fence_after();
         const uint64_t qd = smem_desc(base + SM::kQAt + qr.slot * SM::kSlot, 0, 1024, 2);
 #pragma unroll
-        for (int s = 0; s < DP / 16; ++s)
-          mma_ss(tmem + sr.slot * kTile, kd + s * (2 * kTile),
-                 qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kIdesc, s > 0, on && s < steps);
-        mma_commit(at(ctl.s_full[sr.slot]), on);
+        for (int i = 0; i < 2; ++i) {
+          if (i == 1 && j < second) break;
+          if (j == (i ? second : 0) && !(ok = wait(at(ctl.k_full[kt[i].slot]), kt[i].turn))) break;
+          if (ns[i] >= SM::kS && !(ok = wait(at(ctl.s_empty[i][sr[i].slot]), sr[i].turn ^ 1))) break;
+          fence_after();
+          const uint64_t kd = smem_desc(base + kt[i].slot * SM::kSlot, kTile * 16, 128, 0);
+#pragma unroll
+          for (int s = 0; s < DP / 16; ++s)
+            mma_ss(tmem + (i * SM::kS + sr[i].slot) * kTile, kd + s * (2 * kTile),
+                   qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kIdesc, s > 0, on && s < steps);
+          mma_commit(at(ctl.s_full[i][sr[i].slot]), on);
+          sr[i].next();
+          ++ns[i];
+        }
+        if (!ok) break;
         mma_commit(at(ctl.q_empty[qr.slot]), on);
         qr.next();
-        sr.next();
-        ++ns;
       }
-      mma_commit(at(ctl.k_empty[kr.slot]), on);
-      kr.next();
+      for (int i = 0; i < keys; ++i) mma_commit(at(ctl.k_empty[kt[i].slot]), on);
       done_item(n_items++);
     }
     // the products in flight end before tensor memory is given back
@@ -398,81 +415,77 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       done_item(n_items++);
     }
   } else {
-    // ---- sums: a key per thread, half of the columns, of every other tile ----
-    const int half = warp >> 2 & 1, set = warp >> 3, part = warp >> 2;
-    const int r = threadIdx.x & (kTile - 1);
-    const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + half * (kTile / 2);
+    // ---- sums: a key per thread ----
+    const int set = warp >> 2, r = threadIdx.x & (kUnit - 1);
+    const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + set * SM::kS * kTile;
     Ring<SM::kS> sr;
     Ring<SM::kL> lr;
-    uint32_t item = 0, tiles = 0;  // tiles of the items before
+    uint32_t item = 0;
     bool ok = true;
     MassItem it;
     for (; ok && get_item(item, &it); ++item) {
       const int row = it.row0 + r;
       float* const mass = p.mass + ((int64_t)it.b * p.H + it.h) * p.S + row;
-      const bool write = part == 0 && row < it.row_end;
-      const float old = write && it.whole ? *mass : 0.f;
+      const float old = row < it.row_end && it.whole ? *mass : 0.f;
+      const int from = set == 0 ? 0 : it.row_end - it.row0 > kTile ? second_from(p, it) : it.n;
       float total = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < it.n; ++j, ++tiles, sr.next(), lr.next()) {
-        if ((int)(tiles & 1) != set) continue;
-        if (!(ok = wait(at(ctl.s_full[sr.slot]), sr.turn))) break;
-        fence_after();
-        uint32_t x[kTile / 2];
-        tmem_ld32(x, ts + sr.slot * kTile);
-        tmem_ld32(x + 32, ts + sr.slot * kTile + 32);
-        tmem_wait_ld();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(at(ctl.s_empty[sr.slot]));
+      for (int j = 0; j < it.n; ++j, lr.next()) {
         if (!(ok = wait(at(ctl.lse_full[lr.slot]), lr.turn))) break;
-        const float4* const nl =
-            reinterpret_cast<const float4*>(ctl.lse[lr.slot] + half * (kTile / 2));
-        const int tok = it.tok0 + j * p.tile_tok, cols = min(p.tile_tok, it.n_tok - tok) * p.G;
-        float sum[4] = {};
-        if (cols == kTile && it.start + tok >= it.row0 + kTile - 1) {
-#pragma unroll
-          for (int e = 0; e < kTile / 2; e += 4) {
-            const float4 n4 = nl[e / 4];
-            float a = __uint_as_float(x[e]), b = __uint_as_float(x[e + 1]);
-            float c = __uint_as_float(x[e + 2]), d = __uint_as_float(x[e + 3]);
-            fma2(a, b, p.c, n4.x, n4.y);
-            fma2(c, d, p.c, n4.z, n4.w);
-            add2(sum[0], sum[1], ex2(a), ex2(b));
-            add2(sum[2], sum[3], ex2(c), ex2(d));
-          }
-        } else {
+        if (j >= from) {
+          if (!(ok = wait(at(ctl.s_full[set][sr.slot]), sr.turn))) break;
+          fence_after();
+          const uint32_t s0 = ts + sr.slot * kTile;
+          const int tok = it.tok0 + j * p.tile_tok, cols = min(p.tile_tok, it.n_tok - tok) * p.G;
+          const bool all = cols == kTile && it.start + tok >= it.row0 + set * kTile + kTile - 1;
           // columns [lo, hi): tokens from the key's own row on, up to the last (what is past
           // them may hold anything)
-          const int lo = max(0, row - it.start - tok) * p.G - half * (kTile / 2);
-          const int hi = cols - half * (kTile / 2);
+          const int lo = max(0, row - it.start - tok) * p.G;
+          float sum[4] = {};
+          uint32_t x[2][32];
+          tmem_ld32(x[0], s0);
 #pragma unroll
-          for (int e = 0; e < kTile / 2; ++e) {
-            const float w =
-                ex2(fmaf(__uint_as_float(x[e]), p.c, reinterpret_cast<const float*>(nl)[e]));
-            if (e >= lo && e < hi) sum[e & 3] += w;
+          for (int k = 0; k < 4; ++k) {  // 32 columns' exponentials under the next ones' load
+            tmem_wait_ld();
+            if (k < 3) tmem_ld32(x[k + 1 & 1], s0 + 32 * (k + 1));
+            else {
+              fence_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(at(ctl.s_empty[set][sr.slot]));
+            }
+            const uint32_t* const y = x[k & 1];
+            const float4* const nl = reinterpret_cast<const float4*>(ctl.lse[lr.slot] + 32 * k);
+            if (all) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 n4 = nl[e / 4];
+                float a = __uint_as_float(y[e]), b = __uint_as_float(y[e + 1]);
+                float c = __uint_as_float(y[e + 2]), d = __uint_as_float(y[e + 3]);
+                fma2(a, b, p.c, n4.x, n4.y);
+                fma2(c, d, p.c, n4.z, n4.w);
+                add2(sum[0], sum[1], ex2(a), ex2(b));
+                add2(sum[2], sum[3], ex2(c), ex2(d));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float w =
+                    ex2(fmaf(__uint_as_float(y[e]), p.c, reinterpret_cast<const float*>(nl)[e]));
+                if (32 * k + e >= lo && 32 * k + e < cols) sum[e & 3] += w;
+              }
+            }
           }
+          sr.next();
+          total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         __syncwarp();
         if (lane == 0) bar_arrive(at(ctl.lse_empty[lr.slot]));
       }
       if (!ok) break;
-      const uint32_t x = item & 1, parity = item >> 1 & 1;
-      if (part > 0) {
-        if (item >= 2 && !(ok = wait(at(ctl.sum_empty[x]), parity ^ 1))) break;
-        ctl.sum[x][part - 1][r] = total;
-        bar_arrive(at(ctl.sum_full[x]));
-      } else {
-        if (!(ok = wait(at(ctl.sum_full[x]), parity))) break;
-        total += ctl.sum[x][0][r] + (ctl.sum[x][1][r] + ctl.sum[x][2][r]);
-        bar_arrive(at(ctl.sum_empty[x]));
-        if (it.whole) {
-          if (write) *mass = old + total;
-        } else {
-          p.part[(int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kTile + r] = total;
-        }
-      }
+      if (!it.whole)
+        p.part[(int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kUnit + r] = total;
+      else if (row < it.row_end)
+        *mass = old + total;
       done_item(item);
     }
   }
@@ -484,14 +497,14 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
 }
 
 // Adds the pieces of the unit that the cut after CTA blockIdx.x is the first to divide.
-__global__ __launch_bounds__(kTile) void mass_join_kernel(const MassDivided* divided,
+__global__ __launch_bounds__(kUnit) void mass_join_kernel(const MassDivided* divided,
                                                           const float* part, float* mass) {
   ops_pdl_enter();
   const MassDivided d = divided[blockIdx.x];
   const int r = threadIdx.x, i0 = blockIdx.x;
   if (r >= d.rows) return;
-  float total = part[(int64_t)(2 * i0 + d.slot) * kTile + r];
-  for (int i = i0 + 1; i <= d.last; ++i) total += part[(int64_t)(2 * i) * kTile + r];
+  float total = part[(int64_t)(2 * i0 + d.slot) * kUnit + r];
+  for (int i = i0 + 1; i <= d.last; ++i) total += part[(int64_t)(2 * i) * kUnit + r];
   mass[d.at + r] += total;
 }
 
@@ -563,7 +576,7 @@ size_t scored_bytes(const Plan& p, int group) {
   const size_t rest =
       keeps_scores(p, group)
           ? (size_t)score_blocks(p, nullptr) * p.H * group * kTile * sizeof(float)
-          : (size_t)sm_count() * (2 * kTile * sizeof(float) + sizeof(MassDivided));
+          : (size_t)sm_count() * (2 * kUnit * sizeof(float) + sizeof(MassDivided));
   return 32 + lse_bytes(p, group) + rest;
 }
 
@@ -578,8 +591,8 @@ int64_t mass_cost(const Plan& p, int tile_tok, int32_t last, int32_t* pre, int64
     const auto count = [&](int first) { return (n - first + tile_tok - 1) / tile_tok; };
     // (the rows that all counted tokens attend: units of one cost)
     const int c0 = first_counted(n, last);
-    int64_t units = (start + c0) / kTile + 1, t = units * count(c0);
-    for (int64_t row = units * kTile; row < (int64_t)start + n; row += kTile, ++units)
+    int64_t units = (start + c0) / kUnit + 1, t = units * count(c0);
+    for (int64_t row = units * kUnit; row < (int64_t)start + n; row += kUnit, ++units)
       t += count(first_token(start, n, last, (int)row));
     *tiles += t * p.H;
     total += (t + units * kMassUnitCost) * p.H;
@@ -642,7 +655,7 @@ dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t l
   kp.lse = x.lse;
   kp.mass = x.mass;
   kp.part = reinterpret_cast<float*>(rest);
-  kp.divided = reinterpret_cast<MassDivided*>(rest + (size_t)ctas * 2 * kTile * sizeof(float));
+  kp.divided = reinterpret_cast<MassDivided*>(rest + (size_t)ctas * 2 * kUnit * sizeof(float));
   kp.share = (int32_t)(total / ctas);
   kp.extra = (int32_t)(total % ctas);
   kp.H = p.H;
@@ -658,7 +671,7 @@ dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t l
   cudaError_t err = p.D <= 64 ? launch_mass<T, 64, MAXB>(kp, (int)ctas, stream)
                               : launch_mass<T, 128, MAXB>(kp, (int)ctas, stream);
   if (err == cudaSuccess && ctas > 1)
-    err = ops_launch(mass_join_kernel, dim3((unsigned)ctas - 1), kTile, 0, stream,
+    err = ops_launch(mass_join_kernel, dim3((unsigned)ctas - 1), kUnit, 0, stream,
                      static_cast<const MassDivided*>(kp.divided),
                      static_cast<const float*>(kp.part), kp.mass);
   return err == cudaSuccess ? DV_OK : cuda_fail(err, "scored attention's sums launch");
