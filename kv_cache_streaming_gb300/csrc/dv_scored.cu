@@ -437,7 +437,6 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
           fence_after();
           const uint32_t s0 = ts + sr.slot * kTile;
           const int tok = it.tok0 + j * p.tile_tok, cols = min(p.tile_tok, it.n_tok - tok) * p.G;
-          const bool all = cols == kTile && it.start + tok >= it.row0 + set * kTile + kTile - 1;
           // columns [lo, hi): tokens from the key's own row on, up to the last (what is past
           // them may hold anything)
           const int lo = max(0, row - it.start - tok) * p.G;
@@ -455,7 +454,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
             }
             const uint32_t* const y = x[k & 1];
             const float4* const nl = reinterpret_cast<const float4*>(ctl.lse[lr.slot] + 32 * k);
-            if (all) {
+            if (__all_sync(~0u, lo <= 32 * k && cols >= 32 * k + 32)) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 const float4 n4 = nl[e / 4];
@@ -466,7 +465,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
                 add2(sum[0], sum[1], ex2(a), ex2(b));
                 add2(sum[2], sum[3], ex2(c), ex2(d));
               }
-            } else {
+            } else if (__any_sync(~0u, lo < 32 * k + 32 && cols > 32 * k)) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const float w =
