@@ -16,9 +16,9 @@
 // 128: with one tile of keys, fetching the queries again for each bound it by L2.  The units
 // form one line, each as long as its tiles and unit cost, cut into equal stretches, one a CTA
 // (one CTA an SM); a unit that a cut divides leaves partial sums, which mass_join_kernel adds in
-// order (no atomics: the same bits each time).  Warps 0-3 and 4-7 sum the unit's two tiles of
-// keys, a key a thread; 8 loads (and walks over the units), 9 issues the products into two
-// buffers of tensor memory for each tile, 10 fetches lse.
+// order (no atomics: the same bits each time).  Warps 0-7 and 8-15 sum the unit's two tiles of
+// keys, two to a quarter of the rows with half of the columns each; 16 loads (and walks over the
+// units), 17 issues the products into two buffers of tensor memory for each tile, 18 fetches lse.
 //
 // Every wait gives up after a number of tries, as in the attention kernel.
 #include <algorithm>
@@ -37,16 +37,15 @@ namespace {
 constexpr int kFewRows = 16;
 constexpr int kFewThreads = 256, kFewPer = 4;
 constexpr int kUnit = 2 * kTile;  // rows of a unit of mass_kernel
-constexpr int kSumWarps = 8;
+constexpr int kSumWarps = 16;
 constexpr int kMassThreads = 32 * (kSumWarps + 3);
 // What a unit costs besides its tiles (its keys' fetch, the sums' exchange), in tiles.
-constexpr int kMassUnitCost = 1;
+constexpr int kMassUnitCost = 2;
 
 struct MassDivided {
   int64_t at;    // of the unit's first row in mass
   int32_t rows;  // of the unit (0: none here)
-  int32_t last, slot;  // the last CTA with a piece; the first piece's slot
-  int32_t pad[3];
+  int32_t last;  // the last CTA with a piece
 };
 
 template <int MAXB>
@@ -56,7 +55,7 @@ struct MassParams {
   const uint4* k;
   const float* lse;  // [H][T][G]
   float* mass;       // [B][H][S]
-  float* part;       // two slots of kUnit sums a CTA
+  float* part;       // two slots of kUnit sums a CTA: of the piece it goes on with, and begins
   MassDivided* divided;
   int32_t share, extra;
   int32_t H, G, C, S;
@@ -82,7 +81,7 @@ struct MassItem {
   int b, h, row0;   // the unit's rows [row0, row0 + kUnit)
   int row_end;      // of the sequence
   int tok0, n;      // the piece's first token; its tiles of tokens (0: no more items)
-  int whole;
+  int whole, first;  // the piece is the whole unit; is the unit's first
   int start, n_tok, tok_at;
 };
 
@@ -90,14 +89,15 @@ template <int DP>
 struct MassSmem {
   static constexpr int kSlot = kTile * DP * 2;
   static constexpr int kK = 4, kQ = DP == 128 ? 3 : 6;  // tiles of K and Q held
-  static constexpr int kS = 2, kL = 4;  // sums of each tile of keys, lse
+  static constexpr int kS = 2, kL = 2;  // sums of each tile of keys, lse
   static constexpr int kQAt = kK * kSlot;
   static constexpr int kCtl = kQAt + kQ * kSlot;
   struct Ctl {
     float lse[kL][kTile];  // negative
+    float sum[kUnit];      // of the second half of the columns
     uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ];
     uint64_t s_full[2][kS], s_empty[2][kS], lse_full[kL], lse_empty[kL];
-    uint64_t item_full[kItems], item_empty[kItems], drained;
+    uint64_t sum_full, sum_empty, item_full[kItems], item_empty[kItems], drained;
     MassItem item[kItems];
     uint32_t tmem;
   };
@@ -111,11 +111,32 @@ struct MassWalk {
   int pos, end;     // as in Walk
   int b, h, kt, t;  // the next piece: its unit and first tile of tokens
 
+  __device__ int tokens() const { return p.seq.pre[b + 1] - p.seq.pre[b]; }
   __device__ int tiles(int first) const {  // of tokens, from `first` on
-    return (p.seq.pre[b + 1] - p.seq.pre[b] - first + p.tile_tok - 1) / p.tile_tok;
+    return (tokens() - first + p.tile_tok - 1) / p.tile_tok;
   }
   __device__ int token0() const {
-    return first_token(p.seq.start[b], p.seq.pre[b + 1] - p.seq.pre[b], p.last, kt * kUnit);
+    return first_token(p.seq.start[b], tokens(), p.last, kt * kUnit);
+  }
+  // Tiles of keys of the unit, what each of its tiles of tokens costs.
+  __device__ int keys() const {
+    return p.seq.start[b] + tokens() - kt * kUnit > kTile ? 2 : 1;
+  }
+  // The unit's tiles of tokens before place x of the line (whichever CTA asks).
+  __device__ int before(int x, int cnt) const {
+    const int w = keys();
+    return max(0, min(cnt, (x - pos - kMassUnitCost + w - 1) / w));
+  }
+  __device__ void next_unit(int cnt) {
+    pos += kMassUnitCost + cnt * keys();
+    t = 0;
+    if (++kt * kUnit >= p.seq.start[b] + tokens()) {
+      kt = 0;
+      if (++h == p.H) {
+        h = 0;
+        if (pos < end) do ++b; while (p.seq.pre[b + 1] == p.seq.pre[b]);
+      }
+    }
   }
 
   __device__ MassWalk(const P& p_, int lo, int hi) : p(p_), pos(lo), end(hi) {
@@ -132,49 +153,42 @@ struct MassWalk {
     const int head = (p.cost_pre[b + 1] - p.cost_pre[b]) / p.H;
     h = rem / head;
     rem -= h * head;
-    // the rows that every counted token attends: units of one cost
-    const int c0 = first_counted(p.seq.pre[b + 1] - p.seq.pre[b], p.last);
-    const int flat = (p.seq.start[b] + c0) / kUnit + 1, cost0 = kMassUnitCost + tiles(c0);
+    // the rows that every counted token attends, but for the last unit of them: of one cost
+    const int c0 = first_counted(tokens(), p.last);
+    const int flat = (p.seq.start[b] + c0) / kUnit, cost0 = kMassUnitCost + 2 * tiles(c0);
     kt = min(rem / cost0, flat);
     rem -= kt * cost0;
+    int cnt = tiles(token0());
     if (kt == flat)
 #pragma unroll 1
-      for (;;) {
-        const int cost = kMassUnitCost + tiles(token0());
-        if (rem < cost) break;
-        rem -= cost;
+      while (rem >= kMassUnitCost + cnt * keys()) {
+        rem -= kMassUnitCost + cnt * keys();
         ++kt;
+        cnt = tiles(token0());
       }
     pos = lo - rem;
-    t = max(0, rem - kMassUnitCost);
+    t = before(lo, cnt);
+    if (t == cnt) next_unit(cnt);  // (the stretch starts inside its last tile, which is not its own)
   }
 
   __device__ void next(MassItem* it) {
     it->n = 0;
     if (pos >= end) return;
-    const int start = p.seq.start[b], at = p.seq.pre[b], n_tok = p.seq.pre[b + 1] - at;
     const int first = token0(), cnt = tiles(first);
-    const int n = min(cnt, end - pos - kMassUnitCost) - t;
+    const int n = before(end, cnt) - t;
     if (n <= 0) return;
     it->b = b;
     it->h = h;
     it->row0 = kt * kUnit;
-    it->row_end = start + n_tok;
+    it->row_end = p.seq.start[b] + tokens();
     it->tok0 = first + t * p.tile_tok;
     it->n = n;
-    it->whole = t == 0 && n == cnt;
-    it->start = start;
-    it->n_tok = n_tok;
-    it->tok_at = at;
-    pos += kMassUnitCost + cnt;
-    t = 0;
-    if (++kt * kUnit >= it->row_end) {
-      kt = 0;
-      if (++h == p.H) {
-        h = 0;
-        if (pos < end) do ++b; while (p.seq.pre[b + 1] == p.seq.pre[b]);
-      }
-    }
+    it->whole = n == cnt;
+    it->first = t == 0;
+    it->start = p.seq.start[b];
+    it->n_tok = tokens();
+    it->tok_at = p.seq.pre[b];
+    next_unit(cnt);
   }
 };
 
@@ -230,7 +244,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     }
     for (int i = 0; i < 2 * SM::kS; ++i) {
       bar_init(at(ctl.s_full[i / SM::kS][i % SM::kS]), 1);
-      bar_init(at(ctl.s_empty[i / SM::kS][i % SM::kS]), 4);
+      bar_init(at(ctl.s_empty[i / SM::kS][i % SM::kS]), kSumWarps / 2);
     }
     for (int i = 0; i < SM::kL; ++i) {
       bar_init(at(ctl.lse_full[i]), 1);
@@ -240,6 +254,8 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       bar_init(at(ctl.item_full[i]), 1);
       bar_init(at(ctl.item_empty[i]), kSumWarps + 2);
     }
+    bar_init(at(ctl.sum_full), kUnit);
+    bar_init(at(ctl.sum_empty), kUnit);
     bar_init(at(ctl.drained), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -268,17 +284,14 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     MassWalk<MassParams<MAXB>> walk(p, cut(p, blockIdx.x), cut(p, blockIdx.x + 1));
     if (blockIdx.x > 0 && on) {
       MassDivided d = {};
-      const int from = cut(p, blockIdx.x - 1);
-      if (walk.t > 0 && from <= walk.pos + kMassUnitCost) {
-        const int row0 = walk.kt * kUnit;
-        const int row_end = p.seq.start[walk.b] + p.seq.pre[walk.b + 1] - p.seq.pre[walk.b];
-        const int end = walk.pos + kMassUnitCost + walk.tiles(walk.token0());
+      if (walk.t > 0 && cut(p, blockIdx.x - 1) <= walk.pos + kMassUnitCost) {
+        const int row0 = walk.kt * kUnit, cnt = walk.tiles(walk.token0());
+        const int row_end = p.seq.start[walk.b] + walk.tokens();
         d.at = ((int64_t)walk.b * p.H + walk.h) * p.S + row0;
         d.rows = min(kUnit, row_end - row0);
         d.last = blockIdx.x;
 #pragma unroll 1
-        while (cut(p, d.last + 1) < end) ++d.last;
-        d.slot = from < walk.pos ? 1 : 0;
+        while (walk.before(cut(p, d.last + 1), cnt) < cnt) ++d.last;
       }
       p.divided[blockIdx.x - 1] = d;
     }
@@ -415,8 +428,8 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       done_item(n_items++);
     }
   } else {
-    // ---- sums: a key per thread ----
-    const int set = warp >> 2, r = threadIdx.x & (kUnit - 1);
+    // ---- sums: a key per thread, half of the columns ----
+    const int set = warp >> 3, half = warp >> 2 & 1, r = set * kTile + (threadIdx.x & (kTile - 1));
     const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + set * SM::kS * kTile;
     Ring<SM::kS> sr;
     Ring<SM::kL> lr;
@@ -426,7 +439,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     for (; ok && get_item(item, &it); ++item) {
       const int row = it.row0 + r;
       float* const mass = p.mass + ((int64_t)it.b * p.H + it.h) * p.S + row;
-      const float old = row < it.row_end && it.whole ? *mass : 0.f;
+      const float old = half == 0 && row < it.row_end && it.whole ? *mass : 0.f;
       const int from = set == 0 ? 0 : it.row_end - it.row0 > kTile ? second_from(p, it) : it.n;
       float total = 0.f;
 #pragma unroll 1
@@ -442,22 +455,23 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
           const int lo = max(0, row - it.start - tok) * p.G;
           float sum[4] = {};
           uint32_t x[2][32];
-          tmem_ld32(x[0], s0);
+          tmem_ld32(x[0], s0 + half * (kTile / 2));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 32 columns' exponentials under the next ones' load
+          for (int e32 = 0; e32 < 2; ++e32) {  // 32 columns' exponentials under the next ones' load
+            const int k = 2 * half + e32;
+            const uint32_t* const y = x[e32];
             tmem_wait_ld();
-            if (k < 3) tmem_ld32(x[k + 1 & 1], s0 + 32 * (k + 1));
+            if (e32 == 0) tmem_ld32(x[1], s0 + 32 * (k + 1));
             else {
               fence_before();
               __syncwarp();
               if (lane == 0) bar_arrive(at(ctl.s_empty[set][sr.slot]));
             }
-            const uint32_t* const y = x[k & 1];
-            const float4* const nl = reinterpret_cast<const float4*>(ctl.lse[lr.slot] + 32 * k);
+            const float* const nl = ctl.lse[lr.slot] + 32 * k;
             if (__all_sync(~0u, lo <= 32 * k && cols >= 32 * k + 32)) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const float4 n4 = nl[e / 4];
+                const float4 n4 = *reinterpret_cast<const float4*>(nl + e);
                 float a = __uint_as_float(y[e]), b = __uint_as_float(y[e + 1]);
                 float c = __uint_as_float(y[e + 2]), d = __uint_as_float(y[e + 3]);
                 fma2(a, b, p.c, n4.x, n4.y);
@@ -468,8 +482,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
             } else if (__any_sync(~0u, lo < 32 * k + 32 && cols > 32 * k)) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float w =
-                    ex2(fmaf(__uint_as_float(y[e]), p.c, reinterpret_cast<const float*>(nl)[e]));
+                const float w = ex2(fmaf(__uint_as_float(y[e]), p.c, nl[e]));
                 if (32 * k + e >= lo && 32 * k + e < cols) sum[e & 3] += w;
               }
             }
@@ -481,10 +494,19 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
         if (lane == 0) bar_arrive(at(ctl.lse_empty[lr.slot]));
       }
       if (!ok) break;
-      if (!it.whole)
-        p.part[(int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kUnit + r] = total;
-      else if (row < it.row_end)
-        *mass = old + total;
+      if (half == 1) {
+        if (item > 0 && !(ok = wait(at(ctl.sum_empty), (item - 1) & 1))) break;
+        ctl.sum[r] = total;
+        bar_arrive(at(ctl.sum_full));
+      } else {
+        if (!(ok = wait(at(ctl.sum_full), item & 1))) break;
+        total += ctl.sum[r];
+        bar_arrive(at(ctl.sum_empty));
+        if (!it.whole)
+          p.part[(int64_t)(blockIdx.x * 2 + (it.first ? 1 : 0)) * kUnit + r] = total;
+        else if (row < it.row_end)
+          *mass = old + total;
+      }
       done_item(item);
     }
   }
@@ -502,7 +524,7 @@ __global__ __launch_bounds__(kUnit) void mass_join_kernel(const MassDivided* div
   const MassDivided d = divided[blockIdx.x];
   const int r = threadIdx.x, i0 = blockIdx.x;
   if (r >= d.rows) return;
-  float total = part[(int64_t)(2 * i0 + d.slot) * kUnit + r];
+  float total = part[(int64_t)(2 * i0 + 1) * kUnit + r];
   for (int i = i0 + 1; i <= d.last; ++i) total += part[(int64_t)(2 * i) * kUnit + r];
   mass[d.at + r] += total;
 }
@@ -588,11 +610,11 @@ int64_t mass_cost(const Plan& p, int tile_tok, int32_t last, int32_t* pre, int64
     const int n = p.seq_len[b], start = p.seq_start[b];
     if (n == 0) continue;
     const auto count = [&](int first) { return (n - first + tile_tok - 1) / tile_tok; };
-    // (the rows that all counted tokens attend: units of one cost)
+    // (the rows that all counted tokens attend, but for the last unit of them: of one cost)
     const int c0 = first_counted(n, last);
-    int64_t units = (start + c0) / kUnit + 1, t = units * count(c0);
+    int64_t units = (start + c0) / kUnit, t = units * 2 * count(c0);
     for (int64_t row = units * kUnit; row < (int64_t)start + n; row += kUnit, ++units)
-      t += count(first_token(start, n, last, (int)row));
+      t += count(first_token(start, n, last, (int)row)) * ((int64_t)start + n - row > kTile ? 2 : 1);
     *tiles += t * p.H;
     total += (t + units * kMassUnitCost) * p.H;
   }
@@ -645,7 +667,7 @@ dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t l
   int64_t tiles = 0;
   const int64_t total = mass_cost(p, kp.tile_tok, last, kp.cost_pre, &tiles);
   int64_t ctas = sm_count();
-  if (ctas > tiles) ctas = tiles;
+  if (ctas > tiles / 2) ctas = std::max<int64_t>(1, tiles / 2);  // (two tiles of keys a CTA at least)
   const void* k = static_cast<const uint4*>(p.k) + p.l0 * p.layer_chunks;
   if (!encode_q(&kp.q_map, p, q, group, kp.tile_tok) ||
       !encode_k(&kp.k_map, p, q.dtype == DV_DTYPE_FP16, k))
