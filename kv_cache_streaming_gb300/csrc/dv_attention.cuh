@@ -339,8 +339,8 @@ struct Item {
   int bad;      // non-finite values were taken out of V
 };
 struct WindowItem : Item {  // tiles are counted as in Span, `masked` too
-  int base, sinks;
-  int clear;    // the last row outside the window of the unit's last token
+  int sinks, skip;
+  int clear;  // the last row outside the window of the unit's last token
 };
 constexpr int kItems = 4;
 
@@ -381,12 +381,13 @@ struct Ring {
 
 // ---- the walk over units ---------------------------------------------------------
 
-// Tiles of the rows that some row of a unit attends.  kWindow: `sinks` tiles of the first
-// rows, then tiles from row `base` on, the window of the unit's first token; one run from
-// row 0 where that takes no more tiles.  A window starts where it does, not at a multiple of
-// a tile, so that few rows beside it are read (`base`: at a run of the K copies).
+// The rows that some row of a unit attends, one after the other in tiles.  kWindow: the first
+// rows, rounded up to `sinks`, a multiple of 32, then those `skip` rows later, from the start of the
+// unit's first token's window on; one run from row 0 where that takes no more tiles.  A
+// window starts where it does (at a run of the K copies), not at a multiple of a tile, and the
+// first rows share its first tile, so that few rows beside it are read and few tiles begun.
 struct Span {
-  int row_end, base, sinks, tiles;
+  int row_end, sinks, skip, tiles;
 };
 template <int FORM, typename P>
 __host__ __device__ __forceinline__ Span unit_span(const P& p, int start, int n, int tok0) {
@@ -394,18 +395,16 @@ __host__ __device__ __forceinline__ Span unit_span(const P& p, int start, int n,
   const int left = n - tok0;  // (tok0 + unit_tok may pass 2^31)
   s.row_end = start + (p.is_tree || left <= p.unit_tok ? n : tok0 + p.unit_tok);
   s.tiles = (int)(((uint32_t)s.row_end + kTile - 1) / kTile);
-  s.base = s.sinks = 0;
+  s.sinks = s.skip = 0;
   if constexpr (FORM == kWindow) {
     const int first = start + tok0 - p.window + 1;
-    if (first > 0) {
-      const int base = first & -p.k_rows;  // (a power of two)
-      const int sinks = (int)(((uint32_t)p.sinks + kTile - 1) / kTile);
-      const int tiles = sinks + (int)((uint32_t)(s.row_end - base + kTile - 1) / kTile);
-      if (p.sinks < base && tiles < s.tiles) {
-        s.base = base;
-        s.sinks = sinks;
-        s.tiles = tiles;
-      }
+    const int sinks = (int)(((uint32_t)p.sinks + 31) & ~31u);
+    const int skip = (first > 0 ? first & -p.k_rows : 0) - sinks;  // (k_rows: a power of two)
+    const int tiles = (int)((uint32_t)(s.row_end - skip + kTile - 1) / kTile);
+    if (skip > 0 && tiles < s.tiles) {
+      s.sinks = sinks;
+      s.skip = skip;
+      s.tiles = tiles;
     }
   }
   return s;
@@ -467,17 +466,17 @@ struct Walk {
     it->n_tok = n_tok;
     it->tok_at = at;
     it->bad = 0;
-    it->masked = (p.is_tree ? start : start + tok0 + 1 - sp.base) / kTile + sp.sinks;
+    it->masked = (p.is_tree ? start : start + tok0 + 1 - sp.skip) / kTile;
     if constexpr (FORM == kWindow) {
-      it->base = sp.base;
       it->sinks = sp.sinks;
+      it->skip = sp.skip;
       it->clear = row_end - 1 - p.window;
     }
     if (PAIR) {
       // chain 0's row tile may end earlier, chain 1's may be empty
       const int tok1 = tok0 + p.tile_tok;
       const int rows0 = p.is_tree ? row_end : start + min(tok1, n_tok);
-      it->nt0 = max(0, min(t + n, (rows0 - sp.base + kTile - 1) / kTile + sp.sinks) - t);
+      it->nt0 = max(0, min(t + n, (rows0 - sp.skip + kTile - 1) / kTile) - t);
       it->nt1 = tok1 < n_tok ? n : 0;
     } else {
       it->nt0 = (n + 1) / 2;
@@ -600,25 +599,34 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     *it = ctl.item[k % kItems];
     return __all_sync(~0u, it->n > 0) != 0;
   };
-  // Of an item's tile i: its first row, the end of its rows that some row attends, and whether
+  // Of an item's tile i: the row in its place r (of 32 from a multiple of 32 on, all rows come
+  // one after the other), its rows, how many of them are first rows, rounded up, and whether
   // it hides one of them from some row.
-  const auto tile_row = [&](const ItemT& it, int i) {
+  const auto tile_row = [&](const ItemT& it, int i, int r) {
+    const int at_r = i * kTile + r;
     if constexpr (FORM == kWindow)
-      return i < it.sinks ? i * kTile : it.base + (i - it.sinks) * kTile;
+      return at_r < it.sinks ? at_r : at_r + it.skip;
     else
-      return i * kTile;
+      return at_r;
   };
-  const auto tile_end = [&](const ItemT& it, int i) {
+  const auto tile_rows = [&](const ItemT& it, int i) {
     if constexpr (FORM == kWindow)
-      return i < it.sinks ? p.sinks : it.row_end;
+      return min(kTile, it.row_end - it.skip - i * kTile);
     else
-      return it.row_end;
+      return min(kTile, it.row_end - i * kTile);
+  };
+  const auto tile_sinks = [&](const ItemT& it, int i) {
+    if constexpr (FORM == kWindow)
+      return max(0, min(kTile, it.sinks - i * kTile));
+    else
+      return 0;
   };
   // (kWindow: `clear`, the last row outside the last token's window)
   const auto before_window = [&](const ItemT& it, int i, int clear) {
     if constexpr (FORM == kWindow) {
-      const int row = tile_row(it, i);
-      return p.sinks - row < kTile && (i < it.sinks || row <= clear);
+      const int n = tile_sinks(it, i), row = i * kTile;
+      return (n > 0 && row + n > p.sinks) ||
+             (n < kTile && row + n + it.skip <= clear && row + it.skip + kTile > p.sinks);
     } else {
       return false;
     }
@@ -684,7 +692,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                       x.tok_at + x.tok0 + i * p.tile_tok, bar, on);
         };
         // In the order K0 V0 K1 V1 ...; a unit's queries before its first K.
-        int j = 0, head = 0, v_row = 0, v_rows = 0;  // the V tile that is due (none: v_rows 0)
+        // The V tile that is due (none: v_rows 0): its first v_sinks rows from v_row on, the others
+        // v_skip rows later.
+        int j = 0, head = 0, v_row = 0, v_rows = 0, v_sinks = 0, v_skip = 0;
         bool fetch = true, step = true;  // the next unit is to be published; to be begun
 #pragma unroll 1
         while (ok) {
@@ -694,14 +704,16 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             // a whole tile in one copy a half, else in boxes of 32 rows
             const uint32_t bar = at(ctl.v_full[vr.slot]);
             const uint32_t dst = base + SM::kVAt + vr.slot * SM::kSlot;
-            const int boxes = (v_rows + 31) / 32, copies = boxes == 4 ? 1 : boxes;
-            const CUtensorMap* const map = boxes == 4 ? &p.v_map : &p.v_part;
+            const int boxes = (v_rows + 31) / 32;
+            const bool one = boxes == 4 && (v_sinks == 0 || v_sinks == kTile);
+            const int copies = one ? 1 : boxes;
+            const CUtensorMap* const map = one ? &p.v_map : &p.v_part;
             bar_expect(bar, boxes * (DP / 64) * 4096, on);
 #pragma unroll 1
             for (int x = 0; x < copies; ++x)
               for (int half = 0; half < DP / 64; ++half)
-                tma_load3(dst + half * (kTile * 128) + x * 4096, map, half * 64, v_row + x * 32,
-                          head, bar, on);
+                tma_load3(dst + half * (kTile * 128) + x * 4096, map, half * 64,
+                          v_row + x * 32 + (x * 32 < v_sinks ? 0 : v_skip), head, bar, on);
             vr.next();
             ++nv;
             v_rows = 0;
@@ -725,26 +737,35 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 if ((i ? it.nt1 : it.nt0) > 0) load_q(it, i);
           }
           if (!ok) break;
-          const int row = tile_row(it, it.t0 + j), rows = min(kTile, tile_end(it, it.t0 + j) - row);
+          const int tile = it.t0 + j, rows = tile_rows(it, tile), sinks = tile_sinks(it, tile);
           if (nk >= SM::kK) ok = wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1);
           if (!ok) break;
           const uint32_t bar = at(ctl.k_full[kr.slot]);
           const uint32_t dst = base + SM::kKAt + kr.slot * SM::kSlot;
           const int pad = p.C & 1;  // zeros for the other half of the last contraction step
           bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
-          if (rows == kTile) {
-            tma_load4(dst, &p.k_map, 0, row / p.k_rows, 0, head, bar, on);
+          if (rows == kTile && (sinks == 0 || sinks == kTile)) {
+            tma_load4(dst, &p.k_map, 0, tile_row(it, tile, 0) / p.k_rows, 0, head, bar, on);
           } else {
-            const uint4* src = p.k + (int64_t)head * p.C * p.S + row;
+            const uint4* src = p.k + (int64_t)head * p.C * p.S;
 #pragma unroll 1
-            for (int c = 0; c < p.C; ++c)
-              bulk_load(dst + c * (kTile * 16), src + (int64_t)c * p.S, rows * 16, bar, on);
+            for (int c = 0; c < p.C; ++c, src += p.S) {
+              if (FORM == kWindow && sinks > 0)
+                bulk_load(dst + c * (kTile * 16), src + tile * kTile, sinks * 16, bar, on);
+              if (FORM != kWindow || sinks < rows)
+                bulk_load(dst + (c * kTile + sinks) * 16, src + tile_row(it, tile, sinks),
+                          (rows - sinks) * 16, bar, on);
+            }
           }
           if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar, on);
           kr.next();
           ++nk;
-          v_row = row;
+          v_row = tile * kTile;
           v_rows = rows;
+          if constexpr (FORM == kWindow) {
+            v_sinks = sinks;
+            v_skip = it.skip;
+          }
           fetch = j == 0;
           step = ++j == it.n;
         }
@@ -781,8 +802,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           it.row_end = __shfl_sync(~0u, it.row_end, 0);
           it.masked = __shfl_sync(~0u, it.masked, 0);
           if constexpr (FORM == kWindow) {
-            it.base = __shfl_sync(~0u, it.base, 0);
             it.sinks = __shfl_sync(~0u, it.sinks, 0);
+            it.skip = __shfl_sync(~0u, it.skip, 0);
             it.clear = __shfl_sync(~0u, it.clear, 0);
           }
           const int nt_other = __shfl_sync(~0u, i ? it.nt0 : it.nt1, 0);
@@ -852,7 +873,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 const uint64_t vd =
                     smem_desc(base + SM::kVAt + vr.slot * SM::kSlot, kTile * 128, 1024, 2);
                 const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
-                const int rows = min(kTile, tile_end(it, t0 + jv) - tile_row(it, t0 + jv));
+                const int rows = tile_rows(it, t0 + jv);
                 const bool more = v_mine > 0;
                 if (!wait(at(ctl.p_half[i]), p_count & 1)) return false;
                 fence_after();
@@ -899,12 +920,15 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll 1
         for (int j = 0; j < it.n; ++j, vr.next()) {
           if (!(ok = wait(at(ctl.v_full[vr.slot]), vr.turn))) break;
-          const int row0 = tile_row(it, it.t0 + j), row_end = tile_end(it, it.t0 + j);
-          if (hides(it, it.t0 + j)) {
+          const int tile = it.t0 + j, rows = tile_rows(it, tile);
+          if (hides(it, tile)) {
 #pragma unroll 1
             for (int r = lane; r < kTile; r += 32) {
               uint4* const vrow = reinterpret_cast<uint4*>(sm + SM::kVAt + vr.slot * SM::kSlot + r * 128);
-              if (row0 + r >= row_end) {
+              bool none = r >= rows;
+              if constexpr (FORM == kWindow)
+                none |= r < tile_sinks(it, tile) && tile * kTile + r >= p.sinks;
+              if (none) {
 #pragma unroll
                 for (int c = 0; c < DP / 8; ++c)
                   vrow[(c >> 3) * (kTile * 8) + ((c + r) & 7)] = make_uint4(0, 0, 0, 0);
@@ -964,7 +988,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       int masked = p.is_tree ? it.masked : (it.start + tile_tok0 + 1) / kTile;
       int clear = 0;
       if constexpr (FORM == kWindow) {
-        masked = (it.start + tile_tok0 + 1 - it.base) / kTile + it.sinks;
+        masked = (it.start + tile_tok0 + 1 - it.skip) / kTile;
         clear = it.start + min(tile_tok0 + p.tile_tok, it.n_tok) - 1 - p.window;
       }
       if (!PAIR && item > 0) {  // the other chain has read this chain's last O
@@ -1007,7 +1031,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           if (tile >= masked || before_window(it, tile, clear)) {
 #pragma unroll 1
             for (int k = 0; k < kTile; k += 32) {
-              const int col = tile_row(it, tile) + k;
+              const int col = tile_row(it, tile, k);
               uint32_t w = p.is_tree ? tree_mask(bits, col - it.start)
                                      : causal_mask(it.start + tok - col);
               if constexpr (FORM == kWindow)
@@ -1187,9 +1211,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll 1
         for (int tile = it.t0; tile < it.t0 + it.n; ++tile) {
           if (!hides(it, tile)) continue;
-          const int row1 = min(tile_end(it, tile), tile_row(it, tile) + kTile);
+          const int rows = tile_rows(it, tile);
 #pragma unroll 1
-          for (int row = tile_row(it, tile); row < row1; ++row) {
+          for (int x = 0; x < rows; ++x) {
+            const int row = tile_row(it, tile, x);
             if (row >= it.start &&
                 !(p.is_tree ? (bits >> (row - it.start) & 1) != 0 : row <= it.start + tok))
               continue;
