@@ -89,14 +89,14 @@ template <int DP>
 struct MassSmem {
   static constexpr int kSlot = kTile * DP * 2;
   static constexpr int kK = 4, kQ = DP == 128 ? 3 : 6;  // tiles of K and Q held
-  static constexpr int kS = 2, kL = 2;  // sums of each tile of keys, lse
+  static constexpr int kS = 2, kL = 3;  // sums of each tile of keys, lse
   static constexpr int kQAt = kK * kSlot;
   static constexpr int kCtl = kQAt + kQ * kSlot;
   struct Ctl {
     float lse[kL][kTile];  // negative
     float sum[kUnit];      // of the second half of the columns
     uint64_t k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ];
-    uint64_t s_full[2][kS], s_empty[2][kS], lse_full[kL], lse_empty[kL];
+    uint64_t s_full[2][kS], s_empty[2][kS], lse_full[kL];
     uint64_t sum_full, sum_empty, item_full[kItems], item_empty[kItems], drained;
     MassItem item[kItems];
     uint32_t tmem;
@@ -243,13 +243,10 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       bar_init(at(ctl.q_empty[i]), 1);
     }
     for (int i = 0; i < 2 * SM::kS; ++i) {
-      bar_init(at(ctl.s_full[i / SM::kS][i % SM::kS]), 1);
+      bar_init(at(ctl.s_full[i / SM::kS][i % SM::kS]), 2);  // the products, and who issued them
       bar_init(at(ctl.s_empty[i / SM::kS][i % SM::kS]), kSumWarps / 2);
     }
-    for (int i = 0; i < SM::kL; ++i) {
-      bar_init(at(ctl.lse_full[i]), 1);
-      bar_init(at(ctl.lse_empty[i]), kSumWarps);
-    }
+    for (int i = 0; i < SM::kL; ++i) bar_init(at(ctl.lse_full[i]), 1);
     for (int i = 0; i < kItems; ++i) {
       bar_init(at(ctl.item_full[i]), 1);
       bar_init(at(ctl.item_empty[i]), kSumWarps + 2);
@@ -360,8 +357,9 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
     const int steps = (p.C + 1) / 2;
     Ring<SM::kK> kr;
     Ring<SM::kQ> qr;
-    Ring<SM::kS> sr[2];
-    uint32_t n_items = 0, ns[2] = {};
+    Ring<SM::kS> sr;
+    Ring<SM::kL> lr;
+    uint32_t n_items = 0;
     bool ok = true;
     MassItem it;
     while (ok && get_item(n_items, &it)) {
@@ -375,25 +373,28 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         if (!(ok = wait(at(ctl.q_full[qr.slot]), qr.turn))) break;
+        // (lse is written once the sums that were in the buffers have been read)
+        if (!(ok = wait(at(ctl.lse_full[lr.slot]), lr.turn))) break;
         const uint64_t qd = smem_desc(base + SM::kQAt + qr.slot * SM::kSlot, 0, 1024, 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (i == 1 && j < second) break;
-          if (j == (i ? second : 0) && !(ok = wait(at(ctl.k_full[kt[i].slot]), kt[i].turn))) break;
-          if (ns[i] >= SM::kS && !(ok = wait(at(ctl.s_empty[i][sr[i].slot]), sr[i].turn ^ 1))) break;
-          fence_after();
-          const uint64_t kd = smem_desc(base + kt[i].slot * SM::kSlot, kTile * 16, 128, 0);
+          if (i == 0 || j >= second) {
+            if (j == (i ? second : 0) && !(ok = wait(at(ctl.k_full[kt[i].slot]), kt[i].turn))) break;
+            fence_after();
+            const uint64_t kd = smem_desc(base + kt[i].slot * SM::kSlot, kTile * 16, 128, 0);
 #pragma unroll
-          for (int s = 0; s < DP / 16; ++s)
-            mma_ss(tmem + (i * SM::kS + sr[i].slot) * kTile, kd + s * (2 * kTile),
-                   qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kIdesc, s > 0, on && s < steps);
-          mma_commit(at(ctl.s_full[i][sr[i].slot]), on);
-          sr[i].next();
-          ++ns[i];
+            for (int s = 0; s < DP / 16; ++s)
+              mma_ss(tmem + (i * SM::kS + sr.slot) * kTile, kd + s * (2 * kTile),
+                     qd + (s >> 2) * (kTile * 8) + (s & 3) * 2, kIdesc, s > 0, on && s < steps);
+          }
+          mma_commit(at(ctl.s_full[i][sr.slot]), on);
+          if (on) bar_arrive(at(ctl.s_full[i][sr.slot]));
         }
         if (!ok) break;
         mma_commit(at(ctl.q_empty[qr.slot]), on);
         qr.next();
+        sr.next();
+        lr.next();
       }
       for (int i = 0; i < keys; ++i) mma_commit(at(ctl.k_empty[kt[i].slot]), on);
       done_item(n_items++);
@@ -405,6 +406,7 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
   } else if (warp == kSumWarps + 2) {
     // ---- lse of each tile's rows ----
     Ring<SM::kL> lr;
+    Ring<SM::kS> sr;
     uint32_t n_items = 0, nl = 0;
     bool ok = true;
     MassItem it;
@@ -417,12 +419,17 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           x[e] = lane + 32 * e < cols ? -src[lane + 32 * e] : -INFINITY;
-        if (nl >= SM::kL && !(ok = wait(at(ctl.lse_empty[lr.slot]), lr.turn ^ 1))) break;
+        // Once the sums of the tile before the last have been read, a warp is through with the
+        // tile before that one, whose place this is.
+        if (nl >= SM::kS)
+          if (!(ok = wait(at(ctl.s_empty[0][sr.slot]), sr.turn ^ 1) &&
+                     wait(at(ctl.s_empty[1][sr.slot]), sr.turn ^ 1))) break;
 #pragma unroll
         for (int e = 0; e < 4; ++e) ctl.lse[lr.slot][lane + 32 * e] = x[e];
         __syncwarp();
         if (lane == 0) bar_arrive(at(ctl.lse_full[lr.slot]));
         lr.next();
+        sr.next();
         ++nl;
       }
       done_item(n_items++);
@@ -430,7 +437,8 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
   } else {
     // ---- sums: a key per thread, half of the columns ----
     const int set = warp >> 3, half = warp >> 2 & 1, r = set * kTile + (threadIdx.x & (kTile - 1));
-    const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + set * SM::kS * kTile;
+    const uint32_t ts =
+        tmem + ((uint32_t)(warp & 3) << 21) + set * SM::kS * kTile + half * (kTile / 2);
     Ring<SM::kS> sr;
     Ring<SM::kL> lr;
     uint32_t item = 0;
@@ -443,55 +451,65 @@ __global__ __launch_bounds__(kMassThreads, 1) void mass_kernel(
       const int from = set == 0 ? 0 : it.row_end - it.row0 > kTile ? second_from(p, it) : it.n;
       float total = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < it.n; ++j, lr.next()) {
-        if (!(ok = wait(at(ctl.lse_full[lr.slot]), lr.turn))) break;
-        if (j >= from) {
-          if (!(ok = wait(at(ctl.s_full[set][sr.slot]), sr.turn))) break;
-          fence_after();
-          const uint32_t s0 = ts + sr.slot * kTile;
-          const int tok = it.tok0 + j * p.tile_tok, cols = min(p.tile_tok, it.n_tok - tok) * p.G;
+      for (int j = 0, tok = it.tok0; j < it.n; ++j, tok += p.tile_tok, sr.next(), lr.next()) {
+        if (!(ok = wait(at(ctl.s_full[set][sr.slot]), sr.turn))) break;
+        fence_after();
+        const auto read = [&]() {  // the tile's scores: its buffer is free
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(at(ctl.s_empty[set][sr.slot]));
+        };
+        if (j < from) {
+          read();
+          continue;
+        }
+        const uint32_t s0 = ts + sr.slot * kTile;
+        const float* const nl = ctl.lse[lr.slot] + half * (kTile / 2);
+        const int cols = min(p.tile_tok, it.n_tok - tok) * p.G;
+        const int lead = it.row0 + set * kTile - it.start - tok;  // (the first key's own token)
+        float sum[4] = {};
+        uint32_t x[2][32];
+        tmem_ld32(x[0], s0);
+        tmem_wait_ld();
+        tmem_ld32(x[1], s0 + 32);  // under the first exponentials
+        const auto add = [&](int i) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * i + e);
+            float a = __uint_as_float(x[i][e]), b = __uint_as_float(x[i][e + 1]);
+            float c = __uint_as_float(x[i][e + 2]), d = __uint_as_float(x[i][e + 3]);
+            fma2(a, b, p.c, n4.x, n4.y);
+            fma2(c, d, p.c, n4.z, n4.w);
+            add2(sum[0], sum[1], ex2(a), ex2(b));
+            add2(sum[2], sum[3], ex2(c), ex2(d));
+          }
+        };
+        if (cols == kTile && lead <= 1 - kTile) {  // every key's token comes before the tile
+          add(0);
+          tmem_wait_ld();
+          read();
+          add(1);
+        } else {
+          tmem_wait_ld();
+          read();
           // columns [lo, hi): tokens from the key's own row on, up to the last (what is past
           // them may hold anything)
-          const int lo = max(0, row - it.start - tok) * p.G;
-          float sum[4] = {};
-          uint32_t x[2][32];
-          tmem_ld32(x[0], s0 + half * (kTile / 2));
+          const int lo = max(0, lead + (threadIdx.x & (kTile - 1))) * p.G - half * (kTile / 2);
+          const int hi = cols - half * (kTile / 2);
 #pragma unroll
-          for (int e32 = 0; e32 < 2; ++e32) {  // 32 columns' exponentials under the next ones' load
-            const int k = 2 * half + e32;
-            const uint32_t* const y = x[e32];
-            tmem_wait_ld();
-            if (e32 == 0) tmem_ld32(x[1], s0 + 32 * (k + 1));
-            else {
-              fence_before();
-              __syncwarp();
-              if (lane == 0) bar_arrive(at(ctl.s_empty[set][sr.slot]));
-            }
-            const float* const nl = ctl.lse[lr.slot] + 32 * k;
-            if (__all_sync(~0u, lo <= 32 * k && cols >= 32 * k + 32)) {
+          for (int i = 0; i < 2; ++i) {
+            if (__all_sync(~0u, lo <= 32 * i && hi >= 32 * i + 32)) {
+              add(i);
+            } else if (__any_sync(~0u, lo < 32 * i + 32 && hi > 32 * i)) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 n4 = *reinterpret_cast<const float4*>(nl + e);
-                float a = __uint_as_float(y[e]), b = __uint_as_float(y[e + 1]);
-                float c = __uint_as_float(y[e + 2]), d = __uint_as_float(y[e + 3]);
-                fma2(a, b, p.c, n4.x, n4.y);
-                fma2(c, d, p.c, n4.z, n4.w);
-                add2(sum[0], sum[1], ex2(a), ex2(b));
-                add2(sum[2], sum[3], ex2(c), ex2(d));
-              }
-            } else if (__any_sync(~0u, lo < 32 * k + 32 && cols > 32 * k)) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float w = ex2(fmaf(__uint_as_float(y[e]), p.c, nl[e]));
-                if (32 * k + e >= lo && 32 * k + e < cols) sum[e & 3] += w;
+              for (int e = 32 * i; e < 32 * i + 32; ++e) {
+                const float w = ex2(fmaf(__uint_as_float(x[i][e - 32 * i]), p.c, nl[e]));
+                if (e >= lo && e < hi) sum[e & 3] += w;
               }
             }
           }
-          sr.next();
-          total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(at(ctl.lse_empty[lr.slot]));
+        total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
       if (!ok) break;
       if (half == 1) {
