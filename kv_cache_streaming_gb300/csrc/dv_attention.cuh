@@ -1261,21 +1261,18 @@ struct JoinParams {
   int32_t tokens;
 };
 
-// Adds up the pieces of the unit that the cut after CTA blockIdx.x is the
-// first to divide:
+// Adds up the pieces of the unit that the cut after CTA i0 is the first to divide (block y of ny):
 //   out = sum_i f_i O_i / sum_i f_i l_i,  f_i = exp2(m_i - max m).
 // Bound by latency (a launch of a few microseconds): a thread per 4 output
 // values, with no load waiting for another but for the unit's description.
 template <typename T, int FORM>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constant__ JoinParams p) {
-  ops_pdl_enter();
-  const int i0 = blockIdx.x;
+__device__ __forceinline__ void join(const JoinParams& p, int i0, int y, int ny) {
   const Divided d = p.divided[i0];
   const int d4 = p.D / 4, n = d.tokens * p.G * d4, pieces = d.last - i0 + 1;
   const int64_t slot = (int64_t)p.rows * (p.D + 2);
   const auto piece = [&](int i) { return p.part + slot * (2 * (i0 + i) + (i == 0 ? d.slot : 0)); };
 #pragma unroll 1
-  for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < n; e += gridDim.y * kJoinThreads) {
+  for (int e = y * kJoinThreads + threadIdx.x; e < n; e += ny * kJoinThreads) {
     const int q = e / d4, c = e - q * d4;
     const int tok = q / p.G, g = q - tok * p.G;
     const int tile = tok / p.tile_tok;
@@ -1325,6 +1322,12 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constan
   }
 }
 
+template <typename T, int FORM>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constant__ JoinParams p) {
+  ops_pdl_enter();
+  join<T, FORM>(p, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
 // ---- host ---------------------------------------------------------------------------
 
 // How a call is cut into units and CTAs.
@@ -1346,6 +1349,7 @@ struct Extra {
   float* mass = nullptr;           // kScored: the layer's
   float* lse = nullptr;            // from the workspace
   float* scores = nullptr;
+  bool join_later = false;  // by the kernel that adds up the scores
 };
 
 inline int sm_count() {
@@ -1470,6 +1474,27 @@ inline bool encode_k(CUtensorMap* map, const Plan& p, bool fp16, const void* k) 
   return encode(map, fp16, 4, k, dims, strides, box, false);
 }
 
+inline JoinParams join_params(const Plan& p, const dv_queries& q, const Schedule& s,
+                              const Extra& x, const float* part) {
+  JoinParams jp;
+  jp.out = static_cast<uint16_t*>(q.out);
+  jp.part = part;
+  jp.divided = reinterpret_cast<const Divided*>(reinterpret_cast<const uint8_t*>(part) + s.part_bytes);
+  jp.out_stride = q.out_stride;
+  jp.G = q.q_heads / p.H;
+  jp.D = p.D;
+  jp.tile_tok = s.tile_tok;
+  jp.rows = (s.pair ? 2 : 1) * kTile;
+  jp.lse = x.lse;
+  jp.tokens = (int32_t)p.tokens;
+  return jp;
+}
+// Blocks that join a unit.
+inline unsigned join_blocks(const Plan& p, const dv_queries& q, const Schedule& s) {
+  const int unit = (s.unit_tok < p.max_len ? s.unit_tok : p.max_len) * (q.q_heads / p.H) * (p.D / 4);
+  return (unsigned)((unit + kJoinThreads - 1) / kJoinThreads);
+}
+
 template <typename T, int DP, bool PAIR, int MAXB, int FORM>
 cudaError_t launch_kernel(const AttnParams<MAXB, FORM>& kp, int ctas, cudaStream_t stream) {
   void (*const kernel)(AttnParams<MAXB, FORM>) = attention_kernel<T, DP, PAIR, MAXB, FORM>;
@@ -1538,20 +1563,9 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, const Extra& x, f
     err = s.pair ? launch_kernel<T, 128, true, MAXB, FORM>(kp, s.ctas, stream)
                  : launch_kernel<T, 128, false, MAXB, FORM>(kp, s.ctas, stream);
   if (err != cudaSuccess) return cuda_fail(err, "attention launch");
-  if (s.ctas > 1) {
-    JoinParams jp;
-    jp.out = kp.out;
-    jp.part = part;
-    jp.divided = kp.divided;
-    jp.out_stride = kp.out_stride;
-    jp.G = group;
-    jp.D = p.D;
-    jp.tile_tok = s.tile_tok;
-    jp.rows = (s.pair ? 2 : 1) * kTile;
-    jp.lse = x.lse;
-    jp.tokens = (int32_t)p.tokens;
-    const int unit = (s.unit_tok < p.max_len ? s.unit_tok : p.max_len) * group * (p.D / 4);
-    err = ops_launch(join_kernel<T, FORM>, dim3((unsigned)s.ctas - 1, (unit + kJoinThreads - 1) / kJoinThreads),
+  if (s.ctas > 1 && !x.join_later) {
+    const JoinParams jp = join_params(p, q, s, x, part);
+    err = ops_launch(join_kernel<T, FORM>, dim3((unsigned)s.ctas - 1, join_blocks(p, q, s)),
                      kJoinThreads, 0, stream, jp);
     if (err != cudaSuccess) return cuda_fail(err, "attention join launch");
   }

@@ -35,7 +35,12 @@ namespace {
 
 // Rows (new tokens x heads of a group) up to which the scores are kept.
 constexpr int kFewRows = 16;
-constexpr int kFewThreads = 256, kFewPer = 4;
+constexpr int kFewThreads = kJoinThreads, kFewPer = 4;
+// Blocks of the sums up to which they also join what the cuts divided: 8 an SM.  One launch less
+// (8 short sequences, 25 heads of 64: 17.4 us, 20.3 with two), but every block of a divided
+// unit goes through its pieces' statistics (two contexts of 115000, 8 key heads: 165 us, 160 with
+// two launches; 32 sequences, 112 heads: 309 and 304).
+constexpr int kFewWave = 8 * 152;
 constexpr int kUnit = 2 * kTile;  // rows of a unit of mass_kernel
 constexpr int kSumWarps = 16;
 constexpr int kMassThreads = 32 * (kSumWarps + 3);
@@ -551,41 +556,99 @@ __global__ __launch_bounds__(kUnit) void mass_join_kernel(const MassDivided* div
 
 template <int MAXB>
 struct FewParams {
-  const float* lse;
+  JoinParams join;
   const float* scores;
   float* mass;
-  int32_t H, G, S, tokens, last, chunks;
+  int32_t H, S, last, chunks;
+  int32_t join_ctas, join_blocks;  // blocks that join pieces of outputs: a unit's, of each cut
+  int32_t ctas, share, extra, unit_cost;  // of the attention kernel
   float c;
   SeqTable<MAXB> seq;
   int32_t block_pre[MAXB + 1];
+  int32_t cost_pre[MAXB + 1];
 };
 
-// kFewPer cache rows a thread, kFewThreads apart, whose loads are in flight together; a CTA per
-// (sequence, key head, kFewThreads * kFewPer rows).
-template <int MAXB>
+// The CTA whose stretch holds place x of the line.
+template <typename P>
+__device__ __forceinline__ int owner(const P& p, int x) {
+  const int longer = p.extra * (p.share + 1);
+  return x < longer ? x / (p.share + 1) : p.extra + (x - longer) / p.share;
+}
+
+// -lse of row r of a unit that the cuts may have divided: from the attention kernel, or from
+// its pieces' statistics.
+template <typename T, typename P>
+__device__ __forceinline__ float row_lse(const P& p, int b, int h, int r) {
+  const int n = p.seq.pre[b + 1] - p.seq.pre[b], G = p.join.G;
+  const int tiles = (p.seq.start[b] + n + kTile - 1) / kTile;
+  const int pos = p.cost_pre[b] + h * (p.unit_cost + tiles);
+  const int i0 = owner(p, pos + p.unit_cost), i1 = owner(p, pos + p.unit_cost + tiles - 1);
+  if (i0 == i1) return -p.join.lse[((int64_t)h * p.join.tokens + p.seq.pre[b]) * G + r];
+  const int64_t slot = (int64_t)p.join.rows * (p.join.D + 2);
+  const int first = cut(p, i0) < pos ? 1 : 0;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int i = i0; i <= i1; i += 4) {
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      ml[k] = i + k <= i1
+                  ? reinterpret_cast<const float2*>(
+                        p.join.part + slot * (2 * (i + k) + (i + k == i0 ? first : 0)) +
+                        (int64_t)p.join.rows * p.join.D)[r]
+                  : make_float2(-INFINITY, 0.f);
+    const float m_new =
+        fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+    l *= m == -INFINITY ? 0.f : ex2(m - m_new);
+    m = m_new;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k <= i1)  // (a piece of NaN scores alone has m = -inf and l = NaN)
+        l += (ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - m)) * ml[k].y;
+  }
+  return (std::is_same<T, __half>::value ? kHalfUp : 0.f) - (m + log2f(l));
+}
+
+// Blocks that join the pieces of divided outputs (where that is left to them), then those that sum: kFewPer cache rows a
+// thread, kFewThreads apart, whose loads are in flight together; a block for each (sequence,
+// key head, kFewThreads * kFewPer rows).
+// JOIN: it joins; else lse is complete.
+template <typename T, int MAXB, bool JOIN>
 __global__ __launch_bounds__(kFewThreads) void few_kernel(
     const __grid_constant__ FewParams<MAXB> p) {
+  __shared__ float nlse[kFewRows];
   ops_pdl_enter();
-  const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x - bh * p.chunks;
+  const int joins = JOIN ? p.join_ctas * p.join_blocks : 0;
+  if (JOIN && (int)blockIdx.x < joins) {
+    const int i0 = blockIdx.x / p.join_blocks;
+    join<T, kPlain>(p.join, i0, blockIdx.x - i0 * p.join_blocks, p.join_blocks);
+    return;
+  }
+  const int id = blockIdx.x - joins, bh = id / p.chunks, chunk = id - bh * p.chunks;
   const int b = bh / p.H, h = bh - b * p.H;
-  const int start = p.seq.start[b], t0 = p.seq.pre[b], n = p.seq.pre[b + 1] - t0;
-  const int row0 = chunk * (kFewThreads * kFewPer) + threadIdx.x, row_end = start + n;
-  if (n == 0 || row0 >= row_end) return;
+  const int start = p.seq.start[b], n = p.seq.pre[b + 1] - p.seq.pre[b], G = p.join.G;
+  const int row_end = start + n;
+  if (n == 0 || chunk * (kFewThreads * kFewPer) >= row_end) return;  // (the whole block)
+  const int row0 = chunk * (kFewThreads * kFewPer) + threadIdx.x;
   const int64_t pitch = (int64_t)((row_end + kTile - 1) / kTile) * kTile;
-  const float* s = p.scores + kTile * (int64_t)p.block_pre[b] * (p.H * p.G) +
-                   (int64_t)h * p.G * n * pitch + row0;
-  const float* const lse = p.lse + ((int64_t)h * p.tokens + t0) * p.G;
+  const float* s = p.scores + kTile * (int64_t)p.block_pre[b] * (p.H * G) +
+                   (int64_t)h * G * n * pitch + row0;
   float* const mass = p.mass + ((int64_t)b * p.H + h) * p.S + row0;
   const int c0 = first_counted(n, p.last);
   float old[kFewPer], sum[kFewPer] = {};
 #pragma unroll
   for (int e = 0; e < kFewPer; ++e)
     old[e] = row0 + e * kFewThreads < row_end ? mass[e * kFewThreads] : 0.f;
-  for (int g = 0; g < p.G; ++g) {
+  const float* const lse = p.join.lse + ((int64_t)h * p.join.tokens + p.seq.pre[b]) * G;
+  if constexpr (JOIN) {
+    if ((int)threadIdx.x < n * G) nlse[threadIdx.x] = row_lse<T>(p, b, h, threadIdx.x);
+    __syncthreads();
+  }
+  for (int g = 0; g < G; ++g) {
 #pragma unroll 2
     for (int i = c0; i < n; ++i) {
       const float* const x = s + (int64_t)(g * n + i) * pitch;
-      const float nl = -lse[i * p.G + g];
+      const float nl = JOIN ? nlse[i * G + g] : -lse[i * G + g];
       const int end = start + i + 1;  // of the rows that the token attends
 #pragma unroll
       for (int e = 0; e < kFewPer; ++e)
@@ -659,25 +722,33 @@ cudaError_t launch_mass(const MassParams<MAXB>& kp, int ctas, cudaStream_t strea
 }
 
 template <typename T, int MAXB>
-dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t last, uint8_t* rest,
-                   cudaStream_t stream) {
+dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t last, uint8_t* ws,
+                   uint8_t* rest, cudaStream_t stream) {
   const int group = q.q_heads / p.H;
   if (x.scores) {
     FewParams<MAXB> fp;
-    fp.lse = x.lse;
+    const Schedule sch = schedule<kScored>(p, group, x, fp.cost_pre);
+    fp.join = join_params(p, q, sch, x, reinterpret_cast<const float*>(ws));
+    fp.join_ctas = x.join_later ? sch.ctas - 1 : 0;
+    fp.join_blocks = (int32_t)join_blocks(p, q, sch);
+    fp.ctas = sch.ctas;
+    fp.share = (int32_t)(sch.total / sch.ctas);
+    fp.extra = (int32_t)(sch.total % sch.ctas);
+    fp.unit_cost = sch.unit_cost;
     fp.scores = x.scores;
     fp.mass = x.mass;
     fp.H = p.H;
-    fp.G = group;
     fp.S = p.S;
-    fp.tokens = (int32_t)p.tokens;
     fp.last = last;
     fp.c = q.scale * 1.4426950408889634f;
     fill_table(p, &fp.seq);
     score_blocks(p, fp.block_pre);
     fp.chunks = (int32_t)few_chunks(p);
-    const cudaError_t err = ops_launch(few_kernel<MAXB>, dim3((unsigned)(fp.chunks * p.H * p.B)),
-                                       kFewThreads, 0, stream, fp);
+    const unsigned blocks = (unsigned)(fp.join_ctas * fp.join_blocks + fp.chunks * p.H * p.B);
+    const cudaError_t err =
+        x.join_later
+            ? ops_launch(few_kernel<T, MAXB, true>, dim3(blocks), kFewThreads, 0, stream, fp)
+            : ops_launch(few_kernel<T, MAXB, false>, dim3(blocks), kFewThreads, 0, stream, fp);
     return err == cudaSuccess ? DV_OK : cuda_fail(err, "scored attention's sums launch");
   }
   MassParams<MAXB> kp;
@@ -758,6 +829,7 @@ extern "C" dv_status dv_scored_attention(const dv_cache* cache, int32_t layer,
   if (dv::keeps_scores(p, group)) {
     x.scores = reinterpret_cast<float*>(rest);
     work = dv::few_chunks(p) * p.H * p.B;
+    x.join_later = work <= dv::kFewWave;
   } else {
     work = dv::mass_cost(p, dv::kTile / group, last, nullptr, &tiles);
   }
@@ -766,8 +838,8 @@ extern "C" dv_status dv_scored_attention(const dv_cache* cache, int32_t layer,
   if ((st = dv::run_call<dv::kScored>(p, q, x, ws, stream)) != DV_OK) return st;
   const bool small = p.B <= dv::kSmallBatch;
   if (q.dtype == DV_DTYPE_FP16)
-    return small ? dv::add_mass<__half, dv::kSmallBatch>(p, q, x, last, rest, stream)
-                 : dv::add_mass<__half, dv::kMaxBatch>(p, q, x, last, rest, stream);
-  return small ? dv::add_mass<__nv_bfloat16, dv::kSmallBatch>(p, q, x, last, rest, stream)
-               : dv::add_mass<__nv_bfloat16, dv::kMaxBatch>(p, q, x, last, rest, stream);
+    return small ? dv::add_mass<__half, dv::kSmallBatch>(p, q, x, last, ws, rest, stream)
+                 : dv::add_mass<__half, dv::kMaxBatch>(p, q, x, last, ws, rest, stream);
+  return small ? dv::add_mass<__nv_bfloat16, dv::kSmallBatch>(p, q, x, last, ws, rest, stream)
+               : dv::add_mass<__nv_bfloat16, dv::kMaxBatch>(p, q, x, last, ws, rest, stream);
 }
