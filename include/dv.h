@@ -607,6 +607,9 @@ void dv_delta_streamer_destroy(dv_delta_streamer* ds);
 
 typedef enum { DV_DTYPE_FP16 = 0, DV_DTYPE_BF16 = 1 } dv_dtype;
 
+/* dv_window_attention, dv_scored_attention and dv_kv_evict: max_seq at most 2^31 - 16385, else
+ * DV_ERR_UNSUPPORTED. */
+
 #define DV_MAX_ROT 256   /* rotated elements of a head */
 #define DV_MAX_TREE 64   /* drafted tokens of a sequence in one dv_tree_attention */
 #define DV_MAX_GROUP 128 /* query heads that share a key head */

@@ -419,7 +419,8 @@ extern "C" dv_status dv_kv_evict(const dv_cache* cache, int32_t l0, int32_t l1,
                                  int64_t count, dv_stream stream) {
   dv::Trace trace("dv_kv_evict");
   dv::Plan p;  // of the rows that go, in number: [kept, rows)
-  dv_status st = dv::plan_ranges(cache, l0, l1, kept, rows, &p);
+  dv_status st = dv::check_max_seq(cache);
+  if (st == DV_OK) st = dv::plan_ranges(cache, l0, l1, kept, rows, &p);
   if (st != DV_OK) return st;
   if (sinks < 0 || recent < 0)
     return dv::fail(DV_ERR_INVALID_ARG, "%d first and %d last rows", sinks, recent);

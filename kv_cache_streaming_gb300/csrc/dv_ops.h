@@ -142,6 +142,13 @@ inline dv_status resolve_layers(Plan* p) {
   return DV_OK;
 }
 
+// Rows are counted in 32 bits, in steps of some thousand.
+inline dv_status check_max_seq(const dv_cache* c) {
+  if (c && c->max_seq > INT32_MAX - 16384)
+    return fail(DV_ERR_UNSUPPORTED, "max_seq %d is more than %d", c->max_seq, INT32_MAX - 16384);
+  return DV_OK;
+}
+
 inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && x < y + nb && y < x + na;

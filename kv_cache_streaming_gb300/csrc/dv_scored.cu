@@ -812,14 +812,15 @@ extern "C" dv_status dv_scored_attention(const dv_cache* cache, int32_t layer,
                                          dv_stream stream) {
   dv::Trace trace("dv_scored_attention");
   if (last < 0) return dv::fail(DV_ERR_INVALID_ARG, "the last %d tokens", last);
+  dv_status st = dv::check_max_seq(cache);
+  if (st != DV_OK) return st;
   dv::Plan p;
   dv_queries q;
   dv::Extra x;
   x.mass = mass;
   uint8_t* ws = nullptr;
-  dv_status st = dv::check_call<dv::kScored>(cache, layer, seq_start, seq_end, queries, &x,
-                                             workspace, workspace_bytes, dv::scored_bytes, &p, &q,
-                                             &ws);
+  st = dv::check_call<dv::kScored>(cache, layer, seq_start, seq_end, queries, &x, workspace,
+                                   workspace_bytes, dv::scored_bytes, &p, &q, &ws);
   if (st != DV_OK || p.tokens == 0) return st;
   const int group = q.q_heads / p.H;
   uint8_t* const lse = ws + dv::up32(dv::schedule<dv::kScored>(p, group, x, nullptr).bytes);

@@ -19,6 +19,8 @@ extern "C" dv_status dv_window_attention(const dv_cache* cache, int32_t layer,
   if (!cache) return dv::fail(DV_ERR_INVALID_ARG, "cache is NULL");
   if (window < 1 || sinks < 0)
     return dv::fail(DV_ERR_INVALID_ARG, "a window of %d rows and %d first ones", window, sinks);
+  const dv_status st = dv::check_max_seq(cache);
+  if (st != DV_OK) return st;
   dv::Extra x;  // (more rows than there are: all of them)
   x.window = window < cache->max_seq ? window : cache->max_seq;
   x.sinks = sinks < cache->max_seq ? sinks : cache->max_seq;

@@ -158,3 +158,15 @@ def test_evict_refusals():
     n = np.zeros(2, np.int32).ctypes.data
     assert dv.lib.dv_kv_evict(None, 0, 1, n, n, 0, 0, None, None, None, 0, None) == dv.DV_ERR_INVALID_ARG
     assert dv.lib.dv_kv_evict(_cache().ref, 0, 1, None, n, 0, 0, None, None, None, 0, None) == dv.DV_ERR_INVALID_ARG
+
+
+def test_rows_that_32_bits_hardly_count_are_refused():
+    S = 2**31 - 16384
+    c = dv.Cache(1, 1, 1, 8, S, 2, 0x1000, 0x2000)
+    q, o = _qo(n=1, heads=1, D=8)
+    n = np.zeros(1, np.int32).ctypes.data
+    _refused(dv.DV_ERR_UNSUPPORTED, lambda: dv.dv_window_attention(c, 0, [S - 1], [S], q, o, 0.1, 4, 1, None, stream=0))
+    a = dv.dv.dv_queries(dv.DV_DTYPE_FP16, 1, 0, None, 8, None, 8, 0.1)
+    import ctypes
+    assert dv.lib.dv_scored_attention(c.ref, 0, n, n, ctypes.byref(a), 0, None, None, 0, None) == dv.DV_ERR_UNSUPPORTED
+    assert dv.lib.dv_kv_evict(c.ref, 0, 1, n, n, 0, 0, None, None, None, 0, None) == dv.DV_ERR_UNSUPPORTED
