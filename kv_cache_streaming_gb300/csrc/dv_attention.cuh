@@ -25,6 +25,11 @@
 //   SPLIT  one row tile, the even K/V tiles on one chain and the odd ones on
 //          the other, joined at the end: decode steps and small trees, bound
 //          by reading K and V once.
+//   HEADS  (kWindow and kScored) two key heads of the same tokens, the K/V tiles of one on
+//          one chain and of the other on the other: one head's filling and draining under the
+//          other's tiles, no join at the end.  Many units of few rows: a decode step of 32
+//          sequences through a window of 512, 112 heads, 150 us where SPLIT takes 164; over 64
+//          to 1791 rows, scored, 284 and 289.
 // PAIR where some sequence has more rows than a row tile, SPLIT otherwise, one
 // form for a call.  PAIR and SPLIT, us: 8 prompts of 1000, 25 heads of 64, 51 and
 // 65, of 129 to 384 within 6% either way; 32 prompts of 256, 40 heads of 128, 67
@@ -85,11 +90,13 @@ namespace dv {
 namespace {
 
 enum Form { kPlain = 0, kWindow = 1, kScored = 2 };
+enum Mode { kSplit = 0, kPair = 1, kHeads = 2 };
 
 constexpr int kTile = 128;        // rows of Q and of K/V in a tile
 constexpr int kThreadsAttn = 384;  // two softmax warpgroups, and one of the other warps
 constexpr uint32_t kSpinLimit = 1u << 22;
 constexpr int kJoinThreads = 256;
+constexpr int kHeadRows = 64;      // HEADS: rows of a head at most, and in a piece's slot
 constexpr int kTurnPolls = 32;     // of another chain's progress, a preference (about 1 us)
 constexpr float kLazy = 8.f;       // log2 of the growth that is left to the old maximum
 // fp16 holds weights to 2^-25 of the largest and loses bits of those below 2^-14: log2 of a
@@ -107,7 +114,8 @@ __device__ uint4 g_zero_rows[kTile];
 struct Divided {
   int32_t tok, head, tokens;  // first token and query head of its output; tokens (0: none here)
   int32_t last, slot;         // the last CTA with a piece; the first piece's slot
-  int32_t pad[3];
+  int32_t heads;              // HEADS: key heads of the unit
+  int32_t pad[2];
 };
 
 template <int MAXB>
@@ -410,12 +418,15 @@ __host__ __device__ __forceinline__ Span unit_span(const P& p, int start, int n,
   return s;
 }
 
-template <typename P, int FORM>
+template <typename P, int FORM, int MODE>
 struct Walk {
   using ItemT = typename Smem<64, FORM>::ItemT;
   const P& p;
   int pos, end;       // where the unit starts on the line of costs; where the CTA's stretch ends
   int b, h, tok0, t;  // the next piece: its unit and first tile
+
+  // Units of the same tokens: key heads, HEADS pairs of them.
+  __device__ int heads() const { return MODE == kHeads ? (p.H + 1) / 2 : p.H; }
 
   __device__ Walk(const P& p_, int lo, int hi) : p(p_), pos(lo), end(hi) {
     b = h = tok0 = t = 0;
@@ -428,7 +439,7 @@ struct Walk {
     }
     b = x;
     int rem = lo - p.cost_pre[b];
-    const int head = (p.cost_pre[b + 1] - p.cost_pre[b]) / p.H;
+    const int head = (p.cost_pre[b + 1] - p.cost_pre[b]) / heads();
     h = rem / head;
     rem -= h * head;
 #pragma unroll 1
@@ -446,7 +457,6 @@ struct Walk {
     return unit_span<FORM>(p, p.seq.start[b], p.seq.pre[b + 1] - p.seq.pre[b], tok0);
   }
 
-  template <bool PAIR>
   __device__ void next(ItemT* it) {
     it->n = 0;
     if (pos >= end) return;
@@ -456,7 +466,7 @@ struct Walk {
     const int n = min(cnt, end - pos - p.unit_cost) - t;
     if (n <= 0) return;
     it->b = b;
-    it->h = h;
+    it->h = MODE == kHeads ? 2 * h : h;
     it->tok0 = tok0;
     it->row_end = row_end;
     it->t0 = t;
@@ -472,7 +482,10 @@ struct Walk {
       it->skip = sp.skip;
       it->clear = row_end - 1 - p.window;
     }
-    if (PAIR) {
+    if (MODE == kHeads) {
+      it->nt0 = n;
+      it->nt1 = 2 * h + 1 < p.H ? n : 0;
+    } else if (MODE == kPair) {
       // chain 0's row tile may end earlier, chain 1's may be empty
       const int tok1 = tok0 + p.tile_tok;
       const int rows0 = p.is_tree ? row_end : start + min(tok1, n_tok);
@@ -487,7 +500,7 @@ struct Walk {
     tok0 += p.unit_tok;
     if (tok0 >= n_tok) {
       tok0 = 0;
-      if (++h == p.H) {
+      if (++h == heads()) {
         h = 0;
         if (pos < end) do ++b; while (p.seq.pre[b + 1] == p.seq.pre[b]);
       }
@@ -528,9 +541,10 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
       : "f"(c), "f"(d));
 }
 
-template <typename T, int DP, bool PAIR, int MAXB, int FORM>
+template <typename T, int DP, int MODE, int MAXB, int FORM>
 __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     const __grid_constant__ AttnParams<MAXB, FORM> p) {
+  constexpr bool HEADS = MODE == kHeads, PAIR = MODE != kSplit;  // PAIR: a chain's rows are its own
   using SM = Smem<DP, FORM>;
   using ItemT = typename SM::ItemT;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -631,6 +645,13 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       return false;
     }
   };
+  // HEADS: an item's tiles of keys come in turn, a head's and the other's.  Their number, and
+  // the tile of rows and the head of the j-th.
+  const auto all_tiles = [&](const ItemT& it) { return HEADS ? it.nt0 + it.nt1 : it.n; };
+  const auto tile_of = [&](const ItemT& it, int j) {
+    return it.t0 + (HEADS && it.nt1 > 0 ? j >> 1 : j);
+  };
+  const auto head_of = [&](const ItemT& it, int j) { return HEADS && it.nt1 > 0 ? j & 1 : 0; };
   const auto hides = [&](const ItemT& it, int i) {
     if constexpr (FORM == kWindow)
       return i >= it.masked || before_window(it, i, it.clear);
@@ -644,8 +665,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       // ---- the walk, and loads ----
       {
         const bool on = elect();
-        Walk<AttnParams<MAXB, FORM>, FORM> walk(p, cut(p, blockIdx.x),
-                                    cut(p, blockIdx.x + 1));
+        Walk<AttnParams<MAXB, FORM>, FORM, MODE> walk(p, cut(p, blockIdx.x),
+                                                      cut(p, blockIdx.x + 1));
         ops_pdl_enter();
         if (blockIdx.x > 0 && on) {
           Divided d = {};
@@ -654,7 +675,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             const int n_tok = p.seq.pre[walk.b + 1] - p.seq.pre[walk.b] - walk.tok0;
             const int end = walk.pos + p.unit_cost + walk.span().tiles;
             d.tok = p.seq.pre[walk.b] + walk.tok0;
-            d.head = walk.h * p.G;
+            d.head = walk.h * (HEADS ? 2 : 1) * p.G;
+            d.heads = HEADS ? min(2, p.H - 2 * walk.h) : 1;
             d.tokens = min(n_tok, p.unit_tok);
             d.last = blockIdx.x;
 #pragma unroll 1
@@ -688,13 +710,14 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           const uint32_t bar = at(ctl.q_full[qb]);
           bar_expect(bar, (DP / 64) * 128 * p.G * p.tile_tok, on);
           for (int half = 0; half < DP / 64; ++half)
-            tma_load4(base + qb * SM::kQ + half * (kTile * 128), &p.q_map, half * 64, 0, x.h,
-                      x.tok_at + x.tok0 + i * p.tile_tok, bar, on);
+            tma_load4(base + qb * SM::kQ + half * (kTile * 128), &p.q_map, half * 64, 0,
+                      x.h + (HEADS ? i : 0), x.tok_at + x.tok0 + (HEADS ? 0 : i * p.tile_tok), bar,
+                      on);
         };
         // In the order K0 V0 K1 V1 ...; a unit's queries before its first K.
         // The V tile that is due (none: v_rows 0): its first v_sinks rows from v_row on, the others
         // v_skip rows later.
-        int j = 0, head = 0, v_row = 0, v_rows = 0, v_sinks = 0, v_skip = 0;
+        int j = 0, head = 0, v_head = 0, v_row = 0, v_rows = 0, v_sinks = 0, v_skip = 0;
         bool fetch = true, step = true;  // the next unit is to be published; to be begun
 #pragma unroll 1
         while (ok) {
@@ -713,13 +736,14 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             for (int x = 0; x < copies; ++x)
               for (int half = 0; half < DP / 64; ++half)
                 tma_load3(dst + half * (kTile * 128) + x * 4096, map, half * 64,
-                          v_row + x * 32 + (x * 32 < v_sinks ? 0 : v_skip), head, bar, on);
+                          v_row + x * 32 + (x * 32 < v_sinks ? 0 : v_skip), HEADS ? v_head : head, bar,
+                          on);
             vr.next();
             ++nv;
             v_rows = 0;
           }
           if (fetch) {  // ahead of need, under a unit's first loads: the next unit, SPLIT its queries
-            walk.template next<PAIR>(&after);
+            walk.next(&after);
             publish(after);
             if (!PAIR && ok && after.n > 0) load_q(after, 0);
             fetch = false;
@@ -737,7 +761,8 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 if ((i ? it.nt1 : it.nt0) > 0) load_q(it, i);
           }
           if (!ok) break;
-          const int tile = it.t0 + j, rows = tile_rows(it, tile), sinks = tile_sinks(it, tile);
+          const int tile = tile_of(it, j), rows = tile_rows(it, tile), sinks = tile_sinks(it, tile);
+          const int k_head = head + head_of(it, j);
           if (nk >= SM::kK) ok = wait(at(ctl.k_empty[kr.slot]), kr.turn ^ 1);
           if (!ok) break;
           const uint32_t bar = at(ctl.k_full[kr.slot]);
@@ -745,9 +770,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           const int pad = p.C & 1;  // zeros for the other half of the last contraction step
           bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
           if (rows == kTile && (sinks == 0 || sinks == kTile)) {
-            tma_load4(dst, &p.k_map, 0, tile_row(it, tile, 0) / p.k_rows, 0, head, bar, on);
+            tma_load4(dst, &p.k_map, 0, tile_row(it, tile, 0) / p.k_rows, 0, k_head, bar, on);
           } else {
-            const uint4* src = p.k + (int64_t)head * p.C * p.S;
+            const uint4* src = p.k + (int64_t)k_head * p.C * p.S;
 #pragma unroll 1
             for (int c = 0; c < p.C; ++c, src += p.S) {
               if (FORM == kWindow && sinks > 0)
@@ -760,6 +785,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           if (pad) bulk_load(dst + p.C * (kTile * 16), g_zero_rows, kTile * 16, bar, on);
           kr.next();
           ++nk;
+          v_head = k_head;
           v_row = tile * kTile;
           v_rows = rows;
           if constexpr (FORM == kWindow) {
@@ -767,7 +793,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             v_skip = it.skip;
           }
           fetch = j == 0;
-          step = ++j == it.n;
+          step = ++j == all_tiles(it);
         }
         // No copy is left in flight, whichever warp gave up: nobody else may have waited for it.
 #pragma unroll 1
@@ -797,7 +823,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         bool ok = true;
         ItemT it;
         while (ok && get_item(n_items, &it)) {
-          const int n = __shfl_sync(~0u, it.n, 0), t0 = __shfl_sync(~0u, it.t0, 0);
+          const int n = __shfl_sync(~0u, all_tiles(it), 0);
+          it.t0 = __shfl_sync(~0u, it.t0, 0);
+          if (HEADS) it.nt1 = __shfl_sync(~0u, it.nt1, 0);
           const int nt = __shfl_sync(~0u, i ? it.nt1 : it.nt0, 0);
           it.row_end = __shfl_sync(~0u, it.row_end, 0);
           it.masked = __shfl_sync(~0u, it.masked, 0);
@@ -814,7 +842,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             if (!(ok = wait(at(ctl.q_full[qb]), q_parity))) break;
             if (on) bar_arrive(at(ctl.q_empty[qb]));
           }
-          const auto mine = [&](int j) { return PAIR ? j < nt : (j & 1) == i; };
+          const auto mine = [&](int j) {
+            return HEADS ? head_of(it, j) == i : PAIR ? j < nt : (j & 1) == i;
+          };
           int jk = 0, jv = 0, k_mine = 0, v_mine = 0;
           // Both chains go through every K and V tile in order; one that is not the chain's is
           // let go.  Neither ring is followed past the other (V_j is loaded after K_j+1 and not
@@ -828,7 +858,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
               if (!wait(at(ctl.k_full[kr.slot]), kr.turn)) return false;
               if (own) {
                 if (k_mine == 0 && !wait(at(ctl.q_full[qb]), q_parity)) return false;
-                if (PAIR && !hides(it, t0 + jk)) {
+                if (MODE == kPair && !hides(it, it.t0 + jk)) {
                   // The chains take turns: a chain's scores are computed once the other's softmax
                   // is at its exponentials, so that one's products run under the other's
                   // softmax (in step, both compete for the one and then for the other: 15% slower
@@ -866,14 +896,14 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             while (jv < jk) {
               const bool own = mine(jv);
               // (hidden rows have been looked at where the tile has any)
-              if (!wait(at(own && hides(it, t0 + jv) ? ctl.v_ok[vr.slot] : ctl.v_full[vr.slot]),
+              if (!wait(at(own && hides(it, tile_of(it, jv)) ? ctl.v_ok[vr.slot] : ctl.v_full[vr.slot]),
                             vr.turn))
                 return false;
               if (own) {
                 const uint64_t vd =
                     smem_desc(base + SM::kVAt + vr.slot * SM::kSlot, kTile * 128, 1024, 2);
                 const uint32_t o = tmem + 2 * kTile + i * kTile, s0 = tmem + i * kTile;
-                const int rows = tile_rows(it, t0 + jv);
+                const int rows = tile_rows(it, tile_of(it, jv));
                 const bool more = v_mine > 0;
                 if (!wait(at(ctl.p_half[i]), p_count & 1)) return false;
                 fence_after();
@@ -918,9 +948,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       bool ok = true;
       for (uint32_t k = 0; ok && get_item(k, &it); ++k) {
 #pragma unroll 1
-        for (int j = 0; j < it.n; ++j, vr.next()) {
+        for (int j = 0; j < all_tiles(it); ++j, vr.next()) {
           if (!(ok = wait(at(ctl.v_full[vr.slot]), vr.turn))) break;
-          const int tile = it.t0 + j, rows = tile_rows(it, tile);
+          const int tile = tile_of(it, j), rows = tile_rows(it, tile);
           if (hides(it, tile)) {
 #pragma unroll 1
             for (int r = lane; r < kTile; r += 32) {
@@ -975,9 +1005,10 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
     bool ok = true;
     ItemT it;
     for (; ok && get_item(item, &it); ++item) {
-      const int tile_tok0 = it.tok0 + (PAIR ? i * p.tile_tok : 0);
+      const int tile_tok0 = it.tok0 + (MODE == kPair ? i * p.tile_tok : 0);
+      const int head = it.h + (HEADS ? i : 0);
       const int tok = tile_tok0 + tr, nt = i ? it.nt1 : it.nt0;
-      const bool valid = tr < p.tile_tok && tok < it.n_tok;
+      const bool valid = tr < p.tile_tok && tok < it.n_tok && (!HEADS || nt > 0);
       const bool any_valid = __any_sync(~0u, valid);
       uint64_t bits = 1;  // (a prompt's token attends itself)
       if (p.is_tree && valid) {
@@ -1078,18 +1109,18 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
               }
             }
           };
-          if constexpr (FORM == kScored && !PAIR) {
+          if constexpr (FORM == kScored && MODE != kPair) {
             if (p.scores != nullptr && valid) {
               const int tiles = (it.row_end + kTile - 1) / kTile;
               float* const d =
                   p.scores + kTile * ((int64_t)p.block_pre[it.b] * (p.H * p.G) +
-                                      ((int64_t)(it.h * p.G + g) * it.n_tok + tok) * tiles + tile);
+                                      ((int64_t)(head * p.G + g) * it.n_tok + tok) * tiles + tile);
 #pragma unroll
               for (int k = 0; k < kTile; k += 8) st32(d + k, x + k);
             }
           }
           move_max(row_max());
-          if (PAIR && r == 0) ctl.turn[i] = (int)s_count;
+          if (MODE == kPair && r == 0) ctl.turn[i] = (int)s_count;
           l += half_row(0);
           tmem_wait_st();
         }
@@ -1130,17 +1161,17 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         constexpr int kCols = PAIR ? DP : DP / 2;
         const int c0 = PAIR ? 0 : i * kCols;
         // slot 0: the CTA's first piece, 1: its last
-        constexpr int kRows = PAIR ? 2 * kTile : kTile;
+        constexpr int kRows = MODE == kPair ? 2 * kTile : kTile;
         float* const part =
             p.part + (int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kRows * (p.D + 2);
-        const int prow = (PAIR ? i * kTile : 0) + r;
+        const int prow = (PAIR ? i * (HEADS ? kHeadRows : kTile) : 0) + r;
         uint16_t* const out = p.out + (int64_t)(it.tok_at + tok) * p.out_stride +
-                              (int64_t)(it.h * p.G + g) * p.D;
+                              (int64_t)(head * p.G + g) * p.D;
         if (!whole && valid && (PAIR || i == 0))
           reinterpret_cast<float2*>(part + kRows * p.D)[prow] = make_float2(m * p.c, l);
         if constexpr (FORM == kScored)
           if (whole && valid && (PAIR || i == 0))
-            p.lse[((int64_t)it.h * p.tokens + it.tok_at + tok) * p.G + g] =
+            p.lse[((int64_t)head * p.tokens + it.tok_at + tok) * p.G + g] =
                 m * p.c + log2f(l) - (std::is_same<T, __half>::value ? kHalfUp : 0.f);
 #pragma unroll 1
         for (int k = c0; k < c0 + kCols; k += 32) {
@@ -1201,13 +1232,13 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
         // what it has just written.
         constexpr int kCols = PAIR ? DP : DP / 2;
         const int c0 = PAIR ? 0 : i * kCols, c1 = min(p.D, c0 + kCols);
-        const uint16_t* const v = p.v + ((int64_t)it.b * p.H + it.h) * p.S * (int64_t)p.D;
+        const uint16_t* const v = p.v + ((int64_t)it.b * p.H + head) * p.S * (int64_t)p.D;
         uint32_t* const out = reinterpret_cast<uint32_t*>(
-            p.out + (int64_t)(it.tok_at + tok) * p.out_stride + (int64_t)(it.h * p.G + g) * p.D);
-        constexpr int kRows = PAIR ? 2 * kTile : kTile;
+            p.out + (int64_t)(it.tok_at + tok) * p.out_stride + (int64_t)(head * p.G + g) * p.D);
+        constexpr int kRows = MODE == kPair ? 2 * kTile : kTile;
         float* const part =
             p.part + (int64_t)(blockIdx.x * 2 + (item == 0 ? 0 : 1)) * kRows * (p.D + 2) +
-            (int64_t)((PAIR ? i * kTile : 0) + r) * p.D;
+            (int64_t)((PAIR ? i * (HEADS ? kHeadRows : kTile) : 0) + r) * p.D;
 #pragma unroll 1
         for (int tile = it.t0; tile < it.t0 + it.n; ++tile) {
           if (!hides(it, tile)) continue;
@@ -1268,15 +1299,17 @@ struct JoinParams {
 template <typename T, int FORM>
 __device__ __forceinline__ void join(const JoinParams& p, int i0, int y, int ny) {
   const Divided d = p.divided[i0];
-  const int d4 = p.D / 4, n = d.tokens * p.G * d4, pieces = d.last - i0 + 1;
+  const int d4 = p.D / 4, rows = d.tokens * p.G, n = rows * d4 * d.heads, pieces = d.last - i0 + 1;
   const int64_t slot = (int64_t)p.rows * (p.D + 2);
   const auto piece = [&](int i) { return p.part + slot * (2 * (i0 + i) + (i == 0 ? d.slot : 0)); };
 #pragma unroll 1
   for (int e = y * kJoinThreads + threadIdx.x; e < n; e += ny * kJoinThreads) {
-    const int q = e / d4, c = e - q * d4;
+    int q = e / d4;
+    const int c = e - q * d4, head = q >= rows ? 1 : 0;
+    q -= head * rows;
     const int tok = q / p.G, g = q - tok * p.G;
     const int tile = tok / p.tile_tok;
-    const int r = tile * kTile + (tok - tile * p.tile_tok) * p.G + g;
+    const int r = tile * kTile + (tok - tile * p.tile_tok) * p.G + g + head * kHeadRows;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -1313,10 +1346,10 @@ __device__ __forceinline__ void join(const JoinParams& p, int i0, int y, int ny)
     const float inv = 1.f / l;
     if constexpr (FORM == kScored)
       if (c == 0)
-        p.lse[((int64_t)(d.head / p.G) * p.tokens + d.tok + tok) * p.G + g] =
+        p.lse[((int64_t)(d.head / p.G + head) * p.tokens + d.tok + tok) * p.G + g] =
             m + log2f(l) - (std::is_same<T, __half>::value ? kHalfUp : 0.f);
     uint16_t* const out =
-        p.out + (int64_t)(d.tok + tok) * p.out_stride + (int64_t)(d.head + g) * p.D;
+        p.out + (int64_t)(d.tok + tok) * p.out_stride + (int64_t)(d.head + head * p.G + g) * p.D;
     reinterpret_cast<uint2*>(out)[c] =
         make_uint2(Pack2<T>::pack(o.x * inv, o.y * inv), Pack2<T>::pack(o.z * inv, o.w * inv));
   }
@@ -1332,7 +1365,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const __grid_constan
 
 // How a call is cut into units and CTAs.
 struct Schedule {
-  bool pair;
+  bool pair, heads;
   int tile_tok, unit_tok;
   int64_t total;  // cost: tiles, and unit_cost for each unit
   int unit_cost;
@@ -1372,7 +1405,8 @@ constexpr int kMinTiles = 2;
 // short sequences took twice as long as the others (decode of a ragged batch:
 // 346 us at 0, 252 at 1, 232 at 2, 246 at 5; ragged prompts: 902 at 0, 823 at 1,
 // 814 at 2, 828 at 3, where prompts of 1000 take 57, 53, 55, 55).
-constexpr int kUnitCostPair = 1, kUnitCostSplit = 2;
+constexpr int kUnitCostPair = 1, kUnitCostSplit = 2, kUnitCostHeads = 1;
+constexpr int kHeadsUnits = 4;  // an SM: with fewer, HEADS would leave SMs without a pair of heads
 
 // Rows of a K copy's innermost run: a chunk row's S rows of 16 bytes are one run, so it may be
 // as many as divide S, up to the 256 elements a box may have: 512 bytes where 32 divide
@@ -1405,7 +1439,13 @@ Schedule schedule(const Plan& p, int group, const Extra& x, int32_t* cost_pre) {
   s.tile_tok = kTile / group;
   s.pair = p.max_len > s.tile_tok;
   s.unit_tok = s.tile_tok * (s.pair ? 2 : 1);
-  s.unit_cost = s.pair ? kUnitCostPair : kUnitCostSplit;
+  // HEADS where there are many units of few rows (its slots hold kHeadRows of a head)
+  int64_t split = 0;
+  for (int b = 0; b < p.B; ++b) split += p.seq_len[b] > 0 ? p.H : 0;
+  s.heads = FORM != kPlain && !s.pair && p.H > 1 && p.max_len * group <= kHeadRows &&
+            split >= kHeadsUnits * (int64_t)sm_count();
+  s.unit_cost = s.heads ? kUnitCostHeads : s.pair ? kUnitCostPair : kUnitCostSplit;
+  const int heads = s.heads ? (p.H + 1) / 2 : p.H;
   s.total = s.units = 0;
   int64_t all_tiles = 0;
   const struct {
@@ -1417,11 +1457,11 @@ Schedule schedule(const Plan& p, int group, const Extra& x, int32_t* cost_pre) {
     int64_t tiles = 0;
     for (int64_t u = 0; u < n; u += s.unit_tok) {
       tiles += unit_span<FORM>(up, first, n, (int)u).tiles;
-      s.total += (int64_t)s.unit_cost * p.H;
-      s.units += p.H;
+      s.total += (int64_t)s.unit_cost * heads;
+      s.units += heads;
     }
-    s.total += tiles * p.H;
-    all_tiles += tiles * p.H;
+    s.total += tiles * heads;
+    all_tiles += tiles * heads;
   }
   if (cost_pre) cost_pre[p.B] = (int32_t)s.total;
   const int64_t sms = sm_count();
@@ -1491,13 +1531,14 @@ inline JoinParams join_params(const Plan& p, const dv_queries& q, const Schedule
 }
 // Blocks that join a unit.
 inline unsigned join_blocks(const Plan& p, const dv_queries& q, const Schedule& s) {
-  const int unit = (s.unit_tok < p.max_len ? s.unit_tok : p.max_len) * (q.q_heads / p.H) * (p.D / 4);
+  const int unit = (s.unit_tok < p.max_len ? s.unit_tok : p.max_len) * (q.q_heads / p.H) *
+                   (p.D / 4) * (s.heads ? 2 : 1);
   return (unsigned)((unit + kJoinThreads - 1) / kJoinThreads);
 }
 
-template <typename T, int DP, bool PAIR, int MAXB, int FORM>
+template <typename T, int DP, int MODE, int MAXB, int FORM>
 cudaError_t launch_kernel(const AttnParams<MAXB, FORM>& kp, int ctas, cudaStream_t stream) {
-  void (*const kernel)(AttnParams<MAXB, FORM>) = attention_kernel<T, DP, PAIR, MAXB, FORM>;
+  void (*const kernel)(AttnParams<MAXB, FORM>) = attention_kernel<T, DP, MODE, MAXB, FORM>;
   constexpr int kBytes = Smem<DP, FORM>::kBytes;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
@@ -1555,13 +1596,17 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, const Extra& x, f
     kp.tokens = (int32_t)p.tokens;
     if (x.scores) score_blocks(p, kp.block_pre);
   }
-  cudaError_t err;
-  if (p.D <= 64)
-    err = s.pair ? launch_kernel<T, 64, true, MAXB, FORM>(kp, s.ctas, stream)
-                 : launch_kernel<T, 64, false, MAXB, FORM>(kp, s.ctas, stream);
-  else
-    err = s.pair ? launch_kernel<T, 128, true, MAXB, FORM>(kp, s.ctas, stream)
-                 : launch_kernel<T, 128, false, MAXB, FORM>(kp, s.ctas, stream);
+  const auto launch = [&](auto mode) {
+    constexpr int kMode = decltype(mode)::value;
+    return p.D <= 64 ? launch_kernel<T, 64, kMode, MAXB, FORM>(kp, s.ctas, stream)
+                     : launch_kernel<T, 128, kMode, MAXB, FORM>(kp, s.ctas, stream);
+  };
+  cudaError_t err = cudaErrorInvalidValue;
+  if constexpr (FORM != kPlain)
+    if (s.heads) err = launch(std::integral_constant<int, kHeads>());
+  if (!s.heads)
+    err = s.pair ? launch(std::integral_constant<int, kPair>())
+                 : launch(std::integral_constant<int, kSplit>());
   if (err != cudaSuccess) return cuda_fail(err, "attention launch");
   if (s.ctas > 1 && !x.join_later) {
     const JoinParams jp = join_params(p, q, s, x, part);

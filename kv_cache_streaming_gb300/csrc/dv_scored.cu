@@ -561,7 +561,7 @@ struct FewParams {
   float* mass;
   int32_t H, S, last, chunks;
   int32_t join_ctas, join_blocks;  // blocks that join pieces of outputs: a unit's, of each cut
-  int32_t ctas, share, extra, unit_cost;  // of the attention kernel
+  int32_t ctas, share, extra, unit_cost, heads;  // of the attention kernel
   float c;
   SeqTable<MAXB> seq;
   int32_t block_pre[MAXB + 1];
@@ -581,7 +581,8 @@ template <typename T, typename P>
 __device__ __forceinline__ float row_lse(const P& p, int b, int h, int r) {
   const int n = p.seq.pre[b + 1] - p.seq.pre[b], G = p.join.G;
   const int tiles = (p.seq.start[b] + n + kTile - 1) / kTile;
-  const int pos = p.cost_pre[b] + h * (p.unit_cost + tiles);
+  const int pos = p.cost_pre[b] + (p.heads ? h >> 1 : h) * (p.unit_cost + tiles);
+  const int row = p.heads ? (h & 1) * kHeadRows + r : r;
   const int i0 = owner(p, pos + p.unit_cost), i1 = owner(p, pos + p.unit_cost + tiles - 1);
   if (i0 == i1) return -p.join.lse[((int64_t)h * p.join.tokens + p.seq.pre[b]) * G + r];
   const int64_t slot = (int64_t)p.join.rows * (p.join.D + 2);
@@ -595,7 +596,7 @@ __device__ __forceinline__ float row_lse(const P& p, int b, int h, int r) {
       ml[k] = i + k <= i1
                   ? reinterpret_cast<const float2*>(
                         p.join.part + slot * (2 * (i + k) + (i + k == i0 ? first : 0)) +
-                        (int64_t)p.join.rows * p.join.D)[r]
+                        (int64_t)p.join.rows * p.join.D)[row]
                   : make_float2(-INFINITY, 0.f);
     const float m_new =
         fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
@@ -735,6 +736,7 @@ dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t l
     fp.share = (int32_t)(sch.total / sch.ctas);
     fp.extra = (int32_t)(sch.total % sch.ctas);
     fp.unit_cost = sch.unit_cost;
+    fp.heads = sch.heads ? 1 : 0;
     fp.scores = x.scores;
     fp.mass = x.mass;
     fp.H = p.H;

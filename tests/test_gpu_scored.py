@@ -82,6 +82,12 @@ CASES = [
     (4, 64, 1, 128, 1500, (600, 900), (40, 600), 0),    # more units than SMs
     (5, 70, 1, 128, 1200, (0, 1130), (1, 16), 9),
     (2, 3, 16, 64, 900, (300, 400), (1, 1), 0),
+    # many units of few rows: two heads at a time, an odd number of them, cut among CTAs
+    (11, 71, 1, 128, 700, (0, 690), (1, 3), 2),
+    (10, 63, 4, 64, 500, (300, 480), (0, 16), 0),
+    (310, 2, 2, 40, 321, (0, 300), (1, 5), 3),
+    (3, 301, 1, 72, 900, (800, 899), (1, 1), 0),
+    (10, 61, 16, 64, 300, (200, 299), (1, 1), 0),
 ]
 
 

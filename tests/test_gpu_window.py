@@ -71,6 +71,11 @@ CASES = [
     (1, 2, 4, 128, 30000, (29000, 29900), (1, 1), 20000, 64),  # cut among many CTAs
     (4, 64, 1, 128, 1500, (600, 900), (40, 600), 333, 7),       # more units than SMs
     (5, 70, 1, 128, 1200, (0, 1130), (1, 20), 100, 4),
+    # many units of few rows: two heads at a time, an odd number of them, cut among CTAs
+    (11, 71, 1, 128, 700, (0, 690), (1, 3), 200, 4),
+    (10, 63, 4, 64, 500, (300, 480), (0, 16), 130, 33),
+    (310, 2, 2, 40, 321, (0, 300), (1, 5), 64, 0),
+    (3, 301, 1, 72, 900, (800, 899), (1, 1), 700, 100),
     (2, 2, 1, 64, 900, (300, 400), (1, 400), 900, 0),           # windows that hide nothing
     (2, 2, 2, 128, 900, (300, 400), (1, 64), 50, 900),          # first rows that hide nothing
     (1, 1, 1, 64, 257, (0, 0), (257, 257), 1, 1),
