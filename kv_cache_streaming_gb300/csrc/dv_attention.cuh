@@ -1440,10 +1440,8 @@ Schedule schedule(const Plan& p, int group, const Extra& x, int32_t* cost_pre) {
   s.pair = p.max_len > s.tile_tok;
   s.unit_tok = s.tile_tok * (s.pair ? 2 : 1);
   // HEADS where there are many units of few rows (its slots hold kHeadRows of a head)
-  int64_t split = 0;
-  for (int b = 0; b < p.B; ++b) split += p.seq_len[b] > 0 ? p.H : 0;
   s.heads = FORM != kPlain && !s.pair && p.H > 1 && p.max_len * group <= kHeadRows &&
-            split >= kHeadsUnits * (int64_t)sm_count();
+            (int64_t)p.active * p.H >= kHeadsUnits * (int64_t)sm_count();
   s.unit_cost = s.heads ? kUnitCostHeads : s.pair ? kUnitCostPair : kUnitCostSplit;
   const int heads = s.heads ? (p.H + 1) / 2 : p.H;
   s.total = s.units = 0;

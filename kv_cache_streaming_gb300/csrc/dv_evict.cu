@@ -141,6 +141,7 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
   // ---- the border ----
   const int c0 = p.sinks, c1 = n - p.recent;
   uint32_t need = m - p.sinks - p.recent, bits = 0, mask = 0;
+  bool fit = false;  // all of those at the border
   if (need == 0) {
     bits = mask = ~0u;
   } else {
@@ -198,7 +199,8 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
       bits |= border[0] << shift;
       mask |= field << shift;
       need = border[1];
-      if (shift == 0 || border[2] == need) break;  // (then all of them fit)
+      fit = border[2] == need;
+      if (shift == 0 || fit) break;
     }
   }
 
@@ -206,8 +208,8 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
   const auto side = [&](int i, int end, float x, bool* above, bool* level) {
     const uint32_t key = order_key(x) & mask;
     const bool candidate = i >= c0 && i < c1;
-    *above = i < end && (!candidate || key > bits);
-    *level = i < end && candidate && key == bits;
+    *above = i < end && (!candidate || key > bits || (fit && key == bits));
+    *level = !fit && i < end && candidate && key == bits;
   };
   const uint32_t lower = (1u << lane) - 1;
   const bool listed = ctas == 1 && m <= kBins;  // the list is kept in place of the histogram too
@@ -220,9 +222,11 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
     for (int i0 = w0; i0 < w1; i0 += 32) {
       bool up, eq;
       side(i0 + lane, w1, i0 + lane < w1 ? weight(i0 + lane) : 0.f, &up, &eq);
-      a += __popc(__ballot_sync(~0u, up));
-      e += __popc(__ballot_sync(~0u, eq));
+      a += up;
+      e += eq;
     }
+    a = __reduce_add_sync(~0u, a);
+    e = __reduce_add_sync(~0u, e);
     if (lane == 0) totals[0][warp] = make_uint2(a, e);
     __syncthreads();
     a = e = 0;
@@ -242,27 +246,33 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
         counts[1] = all_e;
       }
       cluster_sync();
-      for (int r = 0; r < rank; ++r) {
-        a += remote_word(&counts[0], r);
-        e += remote_word(&counts[1], r);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster - 1; ++r) {
+        a += r < rank ? remote_word(&counts[0], r) : 0;
+        e += r < rank ? remote_word(&counts[1], r) : 0;
       }
     }
     // (every weight has been read from memory: they may be overwritten)
+#pragma unroll 2
     for (int i0 = w0; i0 < w1; i0 += 32) {
       const int i = i0 + lane;
       const float x = i < w1 ? weight(i) : 0.f;
       bool up, eq;
       side(i, w1, x, &up, &eq);
-      const uint32_t ups = __ballot_sync(~0u, up), eqs = __ballot_sync(~0u, eq);
-      const uint32_t at_i = e + __popc(eqs & lower);
-      if (up || (eq && at_i < need)) {
-        const uint32_t to = a + __popc(ups & lower) + min(at_i, need);
+      const uint32_t ups = __ballot_sync(~0u, up);
+      uint32_t to = a + __popc(ups & lower);
+      if (!fit) {
+        const uint32_t eqs = __ballot_sync(~0u, eq), at_i = e + __popc(eqs & lower);
+        to += min(at_i, need);
+        up |= eq && at_i < need;
+        e += __popc(eqs);
+      }
+      if (up) {
         keep[to] = i;
         if (listed) hist[to] = i;
         out[to] = x;
       }
       a += __popc(ups);
-      e += __popc(eqs);
     }
   } else {
     // in order of rows, so that none is overwritten before it is read
@@ -288,7 +298,7 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
       a += __popc(ups & lower);
       e += __popc(eqs & lower);
       if (up || (eq && e < need)) {
-        const uint32_t to = a + min(e, need);
+        const uint32_t to = a + (fit ? 0 : min(e, need));
         keep[to] = i;
         if (listed) hist[to] = i;
         out[to] = x;
