@@ -36,6 +36,11 @@
  *                    written with rotary positions, attention over them for
  *                    prompts, for trees of drafted tokens and for decode
  *                    steps, and rows moved together in place.
+ *   dv_window_attention, dv_scored_attention, dv_kv_evict
+ *                    (no counterpart either) what keeps the cache within a
+ *                    bound: attention of a window and a few first rows, the
+ *                    weight each row receives added up, and the rows that
+ *                    received least given up.
  *   dv_host_alloc    pinned, mapped host memory on huge pages for replica
  *                    arenas and swap buffers (the host side of every
  *                    transfer above).
@@ -595,9 +600,10 @@ void dv_delta_streamer_destroy(dv_delta_streamer* ds);
 
 /* The operators a decoder layer applies to the cache between two transfers:
  * the new tokens' rows are written (dv_kv_append), read by attention
- * (dv_prompt_attention, dv_tree_attention), and an accepted path of drafted
- * tokens, or the rows an eviction leaves, are moved together
- * (dv_kv_compact).  The pages have no counterpart: their compute is the
+ * (dv_prompt_attention, dv_tree_attention, dv_window_attention,
+ * dv_scored_attention), and an accepted path of drafted tokens
+ * (dv_kv_compact), or the rows an eviction leaves (dv_kv_evict), are moved
+ * together.  The pages have no counterpart: their compute is the
  * host framework's.  [seq_start, seq_end) are, here too, host arrays of row
  * ranges: the rows of the NEW tokens of each sequence.  Buffers with one entry per new
  * token hold the sequences' tokens one after the other (packed, no padding),
@@ -606,9 +612,6 @@ void dv_delta_streamer_destroy(dv_delta_streamer* ds);
  * dv_attention_check can be captured in a CUDA graph. */
 
 typedef enum { DV_DTYPE_FP16 = 0, DV_DTYPE_BF16 = 1 } dv_dtype;
-
-/* dv_window_attention, dv_scored_attention and dv_kv_evict: max_seq at most 2^31 - 16385, else
- * DV_ERR_UNSUPPORTED. */
 
 #define DV_MAX_ROT 256   /* rotated elements of a head */
 #define DV_MAX_TREE 64   /* drafted tokens of a sequence in one dv_tree_attention */
@@ -733,7 +736,8 @@ dv_status dv_tree_attention(const dv_cache* cache, int32_t layer, const int32_t*
  * to its own and the first `sinks` of the sequence (which stay visible: "attention sinks"; 0:
  * none).  Rows that no token attends are not read, and have no effect.  `workspace` and its size
  * as for dv_prompt_attention.  window >= 1, sinks >= 0 (else DV_ERR_INVALID_ARG); a window of
- * max_seq rows or more is plain causal attention. */
+ * max_seq rows or more is plain causal attention.  max_seq at most 2^31 - 16385 (else
+ * DV_ERR_UNSUPPORTED), here and in the two calls below. */
 dv_status dv_window_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
                               const int32_t* seq_end, const dv_queries* queries, int32_t window,
                               int32_t sinks, void* workspace, size_t workspace_bytes,

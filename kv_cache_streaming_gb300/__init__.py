@@ -9,7 +9,8 @@ replica of decode deltas that a cache can be restored from.
 
 Over the same cache, the operators of a decoder layer between two transfers:
 new tokens appended with rotary positions, causal prompt attention, attention
-of drafted token trees (and plain decode), and rows compacted in place.
+of drafted token trees (and plain decode), and rows compacted in place; attention
+through a window, attention that adds up each row's weight, and eviction by it.
 
 All work runs in the hand-written sm_103a kernels of ``libdv.so`` behind the C
 ABI of ``include/dv.h``; this package only marshals arguments (see

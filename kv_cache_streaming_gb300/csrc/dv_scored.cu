@@ -21,6 +21,16 @@
 // units), 17 issues the products into two buffers of tensor memory for each tile, 18 fetches lse.
 //
 // Every wait gives up after a number of tries, as in the attention kernel.
+//
+// Measured (bf16, heads of 128): a decode step of 32 sequences of 64 to 1791 rows, 112 heads, 300
+// us, of which few_kernel takes 14 to 16 (6.3 TB/s); two contexts of 115000, 64 query heads on 8, 159
+// us (few_kernel 19); 32 prompts of 64 to 1536 tokens, 112 heads, 1464 us, of which mass_kernel takes
+// 448: about 1000 cycles a tile of 128 x 128, where its products and its exponentials take 512
+// each.  It is bound by the instructions around them (2400 a tile for 1170 of loads, sums and
+// exponentials), with the tensor cores 47% and the special functions 42% active.  On the way:
+// units of 128 keys 582 us (560 without products, 404 without exponentials: L2, which then fetched
+// the queries twice as often), of 256 552, hidden columns skipped 501, sixteen warps 464, one wait
+// and one arrival a tile 448.
 #include <algorithm>
 
 #include "dv_attention.cuh"
