@@ -106,8 +106,8 @@ __device__ __forceinline__ uint4 load_sparse(const uint4* src) {
   return x;
 }
 
-// HELD: the weights are in shared memory (else there is one CTA a unit, which reads them from
-// memory each time).
+// HELD: the weights are in shared memory (else they are more than a cluster's holds: one CTA
+// of it searches, and reads them from memory each time).
 template <int MAXB, bool HELD>
 __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
     const __grid_constant__ EvictParams<MAXB> p) {
@@ -118,8 +118,7 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
   __shared__ uint2 totals[2][kWarps];
   __shared__ uint32_t counts[2];  // of this CTA: rows above the border and at it
   ops_pdl_enter();
-  const int ctas = p.ctas, rank = HELD ? (int)(blockIdx.x % ctas) : 0;
-  const int unit = HELD ? blockIdx.x / ctas : blockIdx.x;
+  const int ctas = p.ctas, rank = (int)(blockIdx.x % ctas), unit = blockIdx.x / ctas;
   const int B = p.seq.batch, b = unit % B, lh = unit / B;
   const int l = lh / p.H, h = lh - l * p.H;
   const int n = p.seq.rows[b], m = p.seq.pre[b + 1] - p.seq.pre[b];
@@ -128,11 +127,12 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
   float* const out = p.mass_out + at;
   int32_t* const keep = p.keep + (int64_t)lh * p.seq.pre[B] + p.seq.pre[b];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const auto sync = [&]() {
+  const auto sync = [&]() {  // of the CTAs that search
     if (HELD && ctas > 1) cluster_sync(); else __syncthreads();
   };
   // this CTA's rows [lo, hi)
-  const int run = (n + ctas - 1) / ctas, lo = min(rank * run, n), hi = min(lo + run, n);
+  const int run = HELD || n == m ? (n + ctas - 1) / ctas : n;
+  const int lo = min(rank * run, n), hi = min(lo + run, n);
   if (n == m) {  // (the same for every CTA of the cluster)
     for (int i = lo + tid; i < hi; i += kEvictThreads) {
       keep[i] = i;
@@ -147,176 +147,179 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
   }
   const auto weight = [&](int i) { return HELD ? held[i - lo] : mass[i]; };
 
-  // ---- the border ----
-  const int c0 = p.sinks, c1 = n - p.recent;
-  uint32_t need = m - p.sinks - p.recent, bits = 0, mask = 0;
-  bool fit = false;  // all of those at the border
-  if (need == 0) {
-    bits = mask = ~0u;
-  } else {
-#pragma unroll 1
-    for (int shift = 21;; shift = shift == 21 ? 10 : 0) {  // 11, 11 and the last 10 bits
-      const uint32_t field = shift == 0 ? 1023u : 2047u;
-#pragma unroll
-      for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
-      __syncthreads();
-#pragma unroll 4
-      for (int i = max(lo, c0) + tid; i < min(hi, c1); i += kEvictThreads) {
-        const uint32_t key = order_key(weight(i));
-        if ((key & mask) == bits) atomicAdd(&hist[key >> shift & field], 1u);
-      }
-      sync();
-      // four bins a thread, the largest first
-      const uint32_t* const bins = &hist[kBins - 4 - 4 * tid];
-      uint4 four = make_uint4(0, 0, 0, 0);
-      if (HELD && ctas > 1) {
-        uint4 of[kMaxCluster];
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          of[r] = r < ctas ? remote_words(bins, r) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          four = make_uint4(four.x + of[r].x, four.y + of[r].y, four.z + of[r].z, four.w + of[r].w);
-      } else {
-        four = *reinterpret_cast<const uint4*>(bins);
-      }
-      const uint32_t mine[4] = {four.w, four.z, four.y, four.x};
-      const uint32_t sum = (four.x + four.y) + (four.z + four.w);
-      uint32_t before = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const uint32_t x = __shfl_up_sync(~0u, before, d);
-        if (lane >= d) before += x;
-      }
-      if (lane == 31) sums[warp] = before;
-      sync();  // (the histograms have been read)
-      before -= sum;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) before += w < warp ? sums[w] : 0;
-      if (before < need && need <= before + sum) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (before < need && need <= before + mine[e]) {
-            border[0] = kBins - 1 - 4 * tid - e;
-            border[1] = need - before;
-            border[2] = mine[e];
-          }
-          before += mine[e];
-        }
-      }
-      __syncthreads();
-      bits |= border[0] << shift;
-      mask |= field << shift;
-      need = border[1];
-      fit = border[2] == need;
-      if (shift == 0 || fit) break;
-    }
-  }
-
-  // ---- places: kept rows before each one ----
-  const auto side = [&](int i, int end, float x, bool* above, bool* level) {
-    const uint32_t key = order_key(x) & mask;
-    const bool candidate = i >= c0 && i < c1;
-    *above = i < end && (!candidate || key > bits || (fit && key == bits));
-    *level = !fit && i < end && candidate && key == bits;
-  };
-  const uint32_t lower = (1u << lane) - 1;
   const bool listed = ctas == 1 && m <= kBins;  // the list is kept in place of the histogram too
-  if constexpr (HELD) {
-    // a warp's rows [w0, w1)
-    const int part = ((run + kWarps - 1) / kWarps + 31) & ~31;
-    const int w0 = min(lo + warp * part, hi), w1 = min(w0 + part, hi);
-    uint32_t a = 0, e = 0;
-#pragma unroll 4
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      bool up, eq;
-      side(i0 + lane, w1, i0 + lane < w1 ? weight(i0 + lane) : 0.f, &up, &eq);
-      a += up;
-      e += eq;
-    }
-    a = __reduce_add_sync(~0u, a);
-    e = __reduce_add_sync(~0u, e);
-    if (lane == 0) totals[0][warp] = make_uint2(a, e);
-    __syncthreads();
-    a = e = 0;
-    uint32_t all_a = 0, all_e = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const uint2 t = totals[0][w];
-      if (w < warp) {
-        a += t.x;
-        e += t.y;
-      }
-      all_a += t.x;
-      all_e += t.y;
-    }
-    if (ctas > 1) {
-      if (tid == 0) {
-        counts[0] = all_a;
-        counts[1] = all_e;
-      }
-      cluster_sync();
+  if (HELD || rank == 0) {
+    // ---- the border ----
+    const int c0 = p.sinks, c1 = n - p.recent;
+    uint32_t need = m - p.sinks - p.recent, bits = 0, mask = 0;
+    bool fit = false;  // all of those at the border
+    if (need == 0) {
+      bits = mask = ~0u;
+    } else {
+#pragma unroll 1
+      for (int shift = 21;; shift = shift == 21 ? 10 : 0) {  // 11, 11 and the last 10 bits
+        const uint32_t field = shift == 0 ? 1023u : 2047u;
 #pragma unroll
-      for (int r = 0; r < kMaxCluster - 1; ++r) {
-        a += r < rank ? remote_word(&counts[0], r) : 0;
-        e += r < rank ? remote_word(&counts[1], r) : 0;
+        for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int i = max(lo, c0) + tid; i < min(hi, c1); i += kEvictThreads) {
+          const uint32_t key = order_key(weight(i));
+          if ((key & mask) == bits) atomicAdd(&hist[key >> shift & field], 1u);
+        }
+        sync();
+        // four bins a thread, the largest first
+        const uint32_t* const bins = &hist[kBins - 4 - 4 * tid];
+        uint4 four = make_uint4(0, 0, 0, 0);
+        if (HELD && ctas > 1) {
+          uint4 of[kMaxCluster];
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            of[r] = r < ctas ? remote_words(bins, r) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            four = make_uint4(four.x + of[r].x, four.y + of[r].y, four.z + of[r].z, four.w + of[r].w);
+        } else {
+          four = *reinterpret_cast<const uint4*>(bins);
+        }
+        const uint32_t mine[4] = {four.w, four.z, four.y, four.x};
+        const uint32_t sum = (four.x + four.y) + (four.z + four.w);
+        uint32_t before = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const uint32_t x = __shfl_up_sync(~0u, before, d);
+          if (lane >= d) before += x;
+        }
+        if (lane == 31) sums[warp] = before;
+        sync();  // (the histograms have been read)
+        before -= sum;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) before += w < warp ? sums[w] : 0;
+        if (before < need && need <= before + sum) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (before < need && need <= before + mine[e]) {
+              border[0] = kBins - 1 - 4 * tid - e;
+              border[1] = need - before;
+              border[2] = mine[e];
+            }
+            before += mine[e];
+          }
+        }
+        __syncthreads();
+        bits |= border[0] << shift;
+        mask |= field << shift;
+        need = border[1];
+        fit = border[2] == need;
+        if (shift == 0 || fit) break;
       }
     }
-    // (every weight has been read from memory: they may be overwritten)
-#pragma unroll 2
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int i = i0 + lane;
-      const float x = i < w1 ? weight(i) : 0.f;
-      bool up, eq;
-      side(i, w1, x, &up, &eq);
-      const uint32_t ups = __ballot_sync(~0u, up);
-      uint32_t to = a + __popc(ups & lower);
-      if (!fit) {
-        const uint32_t eqs = __ballot_sync(~0u, eq), at_i = e + __popc(eqs & lower);
-        to += min(at_i, need);
-        up |= eq && at_i < need;
-        e += __popc(eqs);
+
+    // ---- places: kept rows before each one ----
+    const auto side = [&](int i, int end, float x, bool* above, bool* level) {
+      const uint32_t key = order_key(x) & mask;
+      const bool candidate = i >= c0 && i < c1;
+      *above = i < end && (!candidate || key > bits || (fit && key == bits));
+      *level = !fit && i < end && candidate && key == bits;
+    };
+    const uint32_t lower = (1u << lane) - 1;
+    if constexpr (HELD) {
+      // a warp's rows [w0, w1)
+      const int part = ((run + kWarps - 1) / kWarps + 31) & ~31;
+      const int w0 = min(lo + warp * part, hi), w1 = min(w0 + part, hi);
+      uint32_t a = 0, e = 0;
+#pragma unroll 4
+      for (int i0 = w0; i0 < w1; i0 += 32) {
+        bool up, eq;
+        side(i0 + lane, w1, i0 + lane < w1 ? weight(i0 + lane) : 0.f, &up, &eq);
+        a += up;
+        e += eq;
       }
-      if (up) {
-        keep[to] = i;
-        if (listed) hist[to] = i;
-        out[to] = x;
-      }
-      a += __popc(ups);
-    }
-  } else {
-    // in order of rows, so that none is overwritten before it is read
-    uint32_t above = 0, level = 0;
-    for (int base = 0, turn = 0; base < n; base += kEvictThreads, turn ^= 1) {
-      const int i = base + tid;
-      const float x = i < n ? mass[i] : 0.f;
-      bool up, eq;
-      side(i, n, x, &up, &eq);
-      const uint32_t ups = __ballot_sync(~0u, up), eqs = __ballot_sync(~0u, eq);
-      if (lane == 0) totals[turn][warp] = make_uint2(__popc(ups), __popc(eqs));
+      a = __reduce_add_sync(~0u, a);
+      e = __reduce_add_sync(~0u, e);
+      if (lane == 0) totals[0][warp] = make_uint2(a, e);
       __syncthreads();
-      uint32_t a = above, e = level;
+      a = e = 0;
+      uint32_t all_a = 0, all_e = 0;
       for (int w = 0; w < kWarps; ++w) {
-        const uint2 t = totals[turn][w];
+        const uint2 t = totals[0][w];
         if (w < warp) {
           a += t.x;
           e += t.y;
         }
-        above += t.x;
-        level += t.y;
+        all_a += t.x;
+        all_e += t.y;
       }
-      a += __popc(ups & lower);
-      e += __popc(eqs & lower);
-      if (up || (eq && e < need)) {
-        const uint32_t to = a + (fit ? 0 : min(e, need));
-        keep[to] = i;
-        if (listed) hist[to] = i;
-        out[to] = x;
+      if (ctas > 1) {
+        if (tid == 0) {
+          counts[0] = all_a;
+          counts[1] = all_e;
+        }
+        cluster_sync();
+#pragma unroll
+        for (int r = 0; r < kMaxCluster - 1; ++r) {
+          a += r < rank ? remote_word(&counts[0], r) : 0;
+          e += r < rank ? remote_word(&counts[1], r) : 0;
+        }
       }
+      // (every weight has been read from memory: they may be overwritten)
+#pragma unroll 2
+      for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const float x = i < w1 ? weight(i) : 0.f;
+        bool up, eq;
+        side(i, w1, x, &up, &eq);
+        const uint32_t ups = __ballot_sync(~0u, up);
+        uint32_t to = a + __popc(ups & lower);
+        if (!fit) {
+          const uint32_t eqs = __ballot_sync(~0u, eq), at_i = e + __popc(eqs & lower);
+          to += min(at_i, need);
+          up |= eq && at_i < need;
+          e += __popc(eqs);
+        }
+        if (up) {
+          keep[to] = i;
+          if (listed) hist[to] = i;
+          out[to] = x;
+        }
+        a += __popc(ups);
+      }
+    } else {
+      // in order of rows, so that none is overwritten before it is read
+      uint32_t above = 0, level = 0;
+      for (int base = 0, turn = 0; base < n; base += kEvictThreads, turn ^= 1) {
+        const int i = base + tid;
+        const float x = i < n ? mass[i] : 0.f;
+        bool up, eq;
+        side(i, n, x, &up, &eq);
+        const uint32_t ups = __ballot_sync(~0u, up), eqs = __ballot_sync(~0u, eq);
+        if (lane == 0) totals[turn][warp] = make_uint2(__popc(ups), __popc(eqs));
+        __syncthreads();
+        uint32_t a = above, e = level;
+        for (int w = 0; w < kWarps; ++w) {
+          const uint2 t = totals[turn][w];
+          if (w < warp) {
+            a += t.x;
+            e += t.y;
+          }
+          above += t.x;
+          level += t.y;
+        }
+        a += __popc(ups & lower);
+        e += __popc(eqs & lower);
+        if (up || (eq && e < need)) {
+          const uint32_t to = a + (fit ? 0 : min(e, need));
+          keep[to] = i;
+          if (listed) hist[to] = i;
+          out[to] = x;
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    for (int i = max(m, lo) + tid; i < hi; i += kEvictThreads) out[i] = 0.f;
   }
-  for (int i = max(m, lo) + tid; i < hi; i += kEvictThreads) out[i] = 0.f;
-  sync();  // the list is complete (and no CTA leaves while others read its counts)
+  // the list is complete (and no CTA leaves while others read its counts)
+  if (ctas > 1) cluster_sync(); else __syncthreads();
 
   // ---- the copy ----
 #pragma unroll 1
@@ -418,9 +421,9 @@ cudaError_t launch_evict(const Plan& p, int32_t sinks, int32_t recent, const flo
   while (ctas < kMaxCluster && (most > ctas * kHeld || (most > ctas * kLeastRun &&
                                                         units * ctas * 2 <= 2 * 152)))
     ctas *= 2;
+  kp.ctas = ctas;
   const int64_t run = ((int64_t)most + ctas - 1) / ctas;
   const bool held = run <= kMostHeld;
-  kp.ctas = held ? ctas : 1;
   // Each CTA copies a slice of K and one of V, of 32 to 256 bytes a row.
   int slices = std::max((p.C + 15) / 16, kp.ctas);
   kp.slice = std::max((p.C + slices - 1) / slices, std::min(2, p.C));

@@ -99,6 +99,7 @@ CASES = [
     (1, 2, 1, 64, 9000, 2, [8999, 8192], [8998, 100], 4, 0, "ties"),
     (1, 2, 2, 128, 30000, 2, [29999, 20000], [5000, 19999], 4, 1000, "ties"),
     (1, 1, 1, 16, 420000, 2, [419999], [2000], 4, 100, "few"), 
+    (1, 2, 1, 16, 420000, 2, [419999, 300], [2000, 300], 4, 100, "ties"),
     (8, 4, 40, 64, 200, 2, [200, 150, 199, 60], [100, 60, 198, 60], 4, 16, "few"),
 ]
 
@@ -162,6 +163,48 @@ def test_evict_in_a_graph_on_a_side_stream():
         for h in range(4):
             for b, m in enumerate(kept.tolist()):
                 assert torch.equal(K[0, b, h, :, :m], K0[0, b, h][:, torch.tensor(lists[0][h][b], device="cuda")])
+
+
+def test_two_evictions_in_flight_on_two_streams_and_a_captured_one():
+    """Clusters (two long sequences) and single CTAs at once, eager and replayed."""
+    gen = _gen(8)
+    jobs = []
+    for L, B, H, S, rows, kept in ((1, 1, 2, 30000, [29000], [4000]), (4, 4, 20, 300, [300, 200, 150, 299], [90] * 4)):
+        cache, K, V, k, v = _cache(L, B, H, 64, S, 2, gen)
+        mass = _weights("few", (L, B, H, S), gen)
+        rows, kept = np.array(rows, np.int32), np.array(kept, np.int32)
+        keep = torch.zeros(L, H, int(kept.sum()), dtype=torch.int32, device="cuda")
+        out = torch.zeros_like(mass)
+        jobs.append((cache, K, V, K.clone(), V.clone(), mass, out, rows, kept, keep, torch.cuda.Stream(), torch.cuda.CUDAGraph()))
+    def check():
+        torch.cuda.synchronize()
+        for cache, K, V, K0, V0, mass, out, rows, kept, keep, _, _ in jobs:
+            lists = W.evict_rows(mass, rows, kept, 4, 20)
+            assert keep.tolist() == [[sum(x, []) for x in y] for y in lists]
+            for l, h, b in ((0, 0, 0), (K.shape[0] - 1, K.shape[2] - 1, K.shape[1] - 1)):
+                at = torch.tensor(lists[l][h][b], device="cuda")
+                assert torch.equal(K[l, b, h, :, :kept[b]], K0[l, b, h][:, at])
+                assert torch.equal(V[l, b, h, :kept[b]], V0[l, b, h][at])
+                assert torch.equal(out[l, b, h, :kept[b]], mass[l, b, h][at])
+            K.copy_(K0)
+            V.copy_(V0)
+            keep.zero_()
+        torch.cuda.synchronize()
+    def call(j):
+        cache, _, _, _, _, mass, out, rows, kept, keep, stream, _ = j
+        dv.dv_kv_evict(cache, 0, cache.num_layers, rows, kept, 4, 20, mass, keep, mass_out=out, stream=stream)
+    torch.cuda.synchronize()
+    for j in jobs:
+        call(j)
+    check()
+    for j in jobs:
+        with torch.cuda.graph(j[-1], stream=j[-2]):
+            call(j)
+    for _ in range(2):
+        for j in jobs:
+            with torch.cuda.stream(j[-2]):
+                j[-1].replay()
+        check()
 
 
 def test_a_cache_past_2_31_elements():

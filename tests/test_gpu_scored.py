@@ -188,6 +188,36 @@ def test_scored_in_a_graph_on_a_side_stream():
             R.assert_within(mass, m, mtol)
 
 
+def test_two_streams_in_flight_together():
+    """Prompts on one stream, decode steps of another cache on a second, several calls each:
+    the bits of the same calls one after the other."""
+    gen = _gen(31)
+    jobs = []
+    for s, e, H, G in (([0, 10, 300], [900, 500, 800], 6, 2), ([700, 20, 900], [701, 21, 901], 24, 4)):
+        s, e = np.array(s, np.int32), np.array(e, np.int32)
+        cache, K, V = R.make_cache("bf16", 1, 3, H, 128, 1024, gen)
+        q = torch.empty(int((e - s).sum()), H * G, 128, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+        jobs.append((cache, s, e, q, torch.zeros_like(q), _ws(cache, s, e, H * G), torch.zeros(3, H, 1024, device="cuda"),
+                     torch.cuda.Stream()))
+    def call(j, stream):
+        cache, s, e, q, out, ws, mass, _ = j
+        for _ in range(5):
+            dv.dv_scored_attention(cache, 0, s, e, q, out, 0.1, mass, ws, last=100, stream=stream)
+    want = []
+    for j in jobs:
+        call(j, None)
+        torch.cuda.synchronize()
+        want.append((j[4].clone(), j[6].clone()))
+        j[4].zero_()
+        j[6].zero_()
+    torch.cuda.synchronize()
+    for j in jobs:
+        call(j, j[-1])
+    torch.cuda.synchronize()
+    for j, (out, mass) in zip(jobs, want):
+        assert torch.equal(j[4], out) and torch.equal(j[6], mass)
+
+
 @pytest.mark.parametrize("new", [1, 700])
 def test_a_wait_that_gives_up_is_reported(new):
     gen = _gen(12)
