@@ -170,3 +170,26 @@ def test_rows_that_32_bits_hardly_count_are_refused():
     import ctypes
     assert dv.lib.dv_scored_attention(c.ref, 0, n, n, ctypes.byref(a), 0, None, None, 0, None) == dv.DV_ERR_UNSUPPORTED
     assert dv.lib.dv_kv_evict(c.ref, 0, 1, n, n, 0, 0, None, None, None, 0, None) == dv.DV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_the_workspace_of_causal_attention_is_enough_for_any_window(seed):
+    """The size check comes before any pointer is looked up: what is refused here is not the size."""
+    rng = np.random.default_rng(seed)
+    for _ in range(60):
+        B, H, G = int(rng.integers(1, 40)), int(rng.integers(1, 90)), int(rng.choice([1, 2, 3, 4, 8, 71, 128]))
+        S = int(np.exp(rng.uniform(1, 9)))
+        s = rng.integers(0, S, size=B).astype(np.int32)
+        e = np.minimum(S, s + rng.integers(0, int(rng.choice([2, 4, 70, 700])), size=B)).astype(np.int32)
+        n = int((e - s).sum())
+        if n * H * G > 1 << 21:  # (some megabytes of tokens)
+            continue
+        c = dv.Cache(1, B, H, 64, S, 2, 0x1000, 0x2000)
+        q, o = torch.empty(n, H * G, 64, dtype=F16), torch.empty(n, H * G, 64, dtype=F16)
+        size = dv.dv_attention_workspace(c, s, e, H * G)
+        for window, sinks in ((1, 0), (1, 1), (5, 33), (100, 4), (129, 128), (S, 0)):
+            try:
+                dv.dv_window_attention(c, 0, s, e, q, o, 0.1, window, sinks, (1 << 40, size), stream=0)
+                assert n == 0
+            except dv.DvError as x:
+                assert x.status != dv.DV_ERR_BUFFER_TOO_SMALL, x
