@@ -156,6 +156,7 @@ template <int MAXB, int FORM>
 struct AttnParams : AttnBase<MAXB> {};
 template <int MAXB>
 struct AttnParams<MAXB, kWindow> : AttnBase<MAXB> {
+  CUtensorMap v_few;  // as v_part, 64 x 8 x 1: the first rows
   int32_t window, sinks;  // a token at row r attends rows (r - window, r] and [0, sinks)
 };
 template <int MAXB>
@@ -722,9 +723,9 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                       on);
         };
         // In the order K0 V0 K1 V1 ...; a unit's queries before its first K.
-        // The V tile that is due (none: v_rows 0): its first v_sinks rows from v_row on, the others
-        // v_skip rows later.
-        int j = 0, head = 0, v_head = 0, v_row = 0, v_rows = 0, v_sinks = 0, v_skip = 0;
+        // The V tile that is due (none: v_rows 0): its first v_sinks rows are v_first boxes of 8
+        // from v_row on, the others come v_skip rows later.
+        int j = 0, head = 0, v_head = 0, v_row = 0, v_rows = 0, v_sinks = 0, v_first = 0, v_skip = 0;
         bool fetch = true, step = true;  // the next unit is to be published; to be begun
 #pragma unroll 1
         while (ok) {
@@ -734,17 +735,22 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
             // a whole tile in one copy a half, else in boxes of 32 rows
             const uint32_t bar = at(ctl.v_full[vr.slot]);
             const uint32_t dst = base + SM::kVAt + vr.slot * SM::kSlot;
-            const int boxes = (v_rows + 31) / 32;
-            const bool one = boxes == 4 && (v_sinks == 0 || v_sinks == kTile);
+            const int boxes = (v_rows + 31) / 32 - v_sinks / 32;
+            const bool one = boxes == 4;
             const int copies = one ? 1 : boxes;
             const CUtensorMap* const map = one ? &p.v_map : &p.v_part;
-            bar_expect(bar, boxes * (DP / 64) * 4096, on);
+            bar_expect(bar, boxes * (DP / 64) * 4096 + v_first * (DP / 64) * 1024, on);
 #pragma unroll 1
-            for (int x = 0; x < copies; ++x)
+            for (int x = v_sinks / 32; x < v_sinks / 32 + copies; ++x)
               for (int half = 0; half < DP / 64; ++half)
                 tma_load3(dst + half * (kTile * 128) + x * 4096, map, half * 64,
-                          v_row + x * 32 + (x * 32 < v_sinks ? 0 : v_skip), HEADS ? v_head : head, bar,
-                          on);
+                          v_row + x * 32 + v_skip, HEADS ? v_head : head, bar, on);
+            if constexpr (FORM == kWindow)
+#pragma unroll 1
+              for (int x = 0; x < v_first; ++x)
+                for (int half = 0; half < DP / 64; ++half)
+                  tma_load3(dst + half * (kTile * 128) + x * 1024, &p.v_few, half * 64,
+                            v_row + x * 8, HEADS ? v_head : head, bar, on);
             vr.next();
             ++nv;
             v_rows = 0;
@@ -775,15 +781,18 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           const uint32_t bar = at(ctl.k_full[kr.slot]);
           const uint32_t dst = base + SM::kKAt + kr.slot * SM::kSlot;
           const int pad = p.C & 1;  // zeros for the other half of the last contraction step
-          bar_expect(bar, p.C * rows * 16 + pad * (kTile * 16), on);
-          if (rows == kTile && (sinks == 0 || sinks == kTile)) {
+          int first = 0;  // kWindow: of the first rows, those that are not there for the rounding alone
+          if constexpr (FORM == kWindow)
+            if (sinks > 0) first = min(sinks, p.sinks - tile * kTile);
+          bar_expect(bar, p.C * (rows - sinks + first) * 16 + pad * (kTile * 16), on);
+          if (rows == kTile && (sinks == 0 || first == kTile)) {
             tma_load4(dst, &p.k_map, 0, tile_row(it, tile, 0) / p.k_rows, 0, k_head, bar, on);
           } else {
             const uint4* src = p.k + (int64_t)k_head * p.C * p.S;
 #pragma unroll 1
             for (int c = 0; c < p.C; ++c, src += p.S) {
               if (FORM == kWindow && sinks > 0)
-                bulk_load(dst + c * (kTile * 16), src + tile * kTile, sinks * 16, bar, on);
+                bulk_load(dst + c * (kTile * 16), src + tile * kTile, first * 16, bar, on);
               if (FORM != kWindow || sinks < rows)
                 bulk_load(dst + (c * kTile + sinks) * 16, src + tile_row(it, tile, sinks),
                           (rows - sinks) * 16, bar, on);
@@ -797,6 +806,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
           v_rows = rows;
           if constexpr (FORM == kWindow) {
             v_sinks = sinks;
+            v_first = (first + 7) / 8;
             v_skip = it.skip;
           }
           fetch = j == 0;
@@ -1592,6 +1602,9 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, const Extra& x, f
   kp.tries = attention_tries();
   fill_table(p, &kp.seq);
   if constexpr (FORM == kWindow) {
+    const cuuint32_t vf[3] = {64, 8, 1};
+    if (!encode(&kp.v_few, fp16, 3, v, vd, vs, vf, true))
+      return fail(DV_ERR_CUDA, "cuTensorMapEncodeTiled refused the cache");
     kp.window = x.window;
     kp.sinks = x.sinks;
   }
