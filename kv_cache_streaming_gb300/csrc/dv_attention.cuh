@@ -83,8 +83,9 @@
 // and a window of 500 take 7 tiles, of whose products 56% are attended): ragged prompts
 // through 500 rows, 40 heads, 135 us; 4096 tokens behind 120000 rows through 4096, 64 query
 // heads on 8, 407 us, 1.36 PFLOP/s attended; a decode step of 32 sequences through 512
-// rows, 112 heads, 149 us, 5.5 TB/s.  On the way: the first rows in a tile of their own, 430 us
-// for the 4096 tokens and 178 for the decode step; before HEADS, 409 and 166.
+// rows, 112 heads, 147 us, 5.6 TB/s.  On the way: the first rows in a tile of their own, 430 us
+// for the 4096 tokens and 178 for the decode step; before HEADS, 409 and 166; with the
+// first rows fetched 32 at a time, 150.
 #pragma once
 
 #include <cuda.h>
