@@ -734,13 +734,17 @@ dv_status dv_tree_attention(const dv_cache* cache, int32_t layer, const int32_t*
 /* As dv_prompt_attention, of prompts and of decode steps alike, through a window: the token
  * at row r attends the rows j <= r with j > r - window or j < sinks, the last `window` rows up
  * to its own and the first `sinks` of the sequence (which stay visible: "attention sinks"; 0:
- * none).  Rows that no token attends are not read, and have no effect.  `workspace` and its size
+ * none).  Rows that no token attends are not read, and have no effect.  `tree`: NULL, or the new
+ * tokens are drafted ones, at most DV_MAX_TREE of a sequence, which attend the new rows of their
+ * bits as in dv_tree_attention, and of rows [0, seq_start) those that the row seq_start + (set
+ * bits - 1) attends, the token's place after its ancestors; window at least DV_MAX_TREE (else
+ * DV_ERR_UNSUPPORTED).  `workspace` and its size
  * as for dv_prompt_attention.  window >= 1, sinks >= 0 (else DV_ERR_INVALID_ARG); a window of
  * max_seq rows or more is plain causal attention.  max_seq at most 2^31 - 16385 (else
  * DV_ERR_UNSUPPORTED), here and in the two calls below. */
 dv_status dv_window_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
                               const int32_t* seq_end, const dv_queries* queries, int32_t window,
-                              int32_t sinks, void* workspace, size_t workspace_bytes,
+                              int32_t sinks, const uint64_t* tree, void* workspace, size_t workspace_bytes,
                               dv_stream stream);
 
 /* As dv_prompt_attention, of prompts and of decode steps alike, and adds the weight that each

@@ -414,7 +414,8 @@ __host__ __device__ __forceinline__ Span unit_span(const P& p, int start, int n,
   s.tiles = (int)(((uint32_t)s.row_end + kTile - 1) / kTile);
   s.sinks = s.skip = 0;
   if constexpr (FORM == kWindow) {
-    const int first = start + tok0 - p.window + 1;
+    // (a drafted token stands at least where the first does)
+    const int first = start + (p.is_tree ? 0 : tok0) - p.window + 1;
     const int sinks = (int)(((uint32_t)p.sinks + 31) & ~31u);
     const int skip = (first > 0 ? first & -p.k_rows : 0) - sinks;  // (k_rows: a power of two)
     const int tiles = (int)((uint32_t)(s.row_end - skip + kTile - 1) / kTile);
@@ -485,7 +486,7 @@ struct Walk {
     it->n_tok = n_tok;
     it->tok_at = at;
     it->bad = 0;
-    it->masked = (p.is_tree ? start : start + tok0 + 1 - sp.skip) / kTile;
+    it->masked = (start + (p.is_tree ? 0 : tok0 + 1) - sp.skip) / kTile;
     if constexpr (FORM == kWindow) {
       it->sinks = sp.sinks;
       it->skip = sp.skip;
@@ -1035,10 +1036,15 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
       }
       // the first tile that hides a column from some row of the chain's tile
       int masked = p.is_tree ? it.masked : (it.start + tile_tok0 + 1) / kTile;
-      int clear = 0;
+      int clear = 0, row_at = it.start + tok;  // (kWindow: the row that the window ends at)
       if constexpr (FORM == kWindow) {
-        masked = (it.start + tile_tok0 + 1 - it.skip) / kTile;
-        clear = it.start + min(tile_tok0 + p.tile_tok, it.n_tok) - 1 - p.window;
+        if (p.is_tree) {
+          row_at = it.start + max(__popcll(bits) - 1, 0);
+          clear = it.clear;
+        } else {
+          masked = (it.start + tile_tok0 + 1 - it.skip) / kTile;
+          clear = it.start + min(tile_tok0 + p.tile_tok, it.n_tok) - 1 - p.window;
+        }
       }
       if (!PAIR && item > 0) {  // the other chain has read this chain's last O
         const uint32_t w = item - 1;
@@ -1084,7 +1090,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
               uint32_t w = p.is_tree ? tree_mask(bits, col - it.start)
                                      : causal_mask(it.start + tok - col);
               if constexpr (FORM == kWindow)
-                w &= ~causal_mask(it.start + tok - p.window - col) | causal_mask(p.sinks - 1 - col);
+                w &= ~causal_mask(row_at - p.window - col) | causal_mask(p.sinks - 1 - col);
               if (__all_sync(~0u, w == ~0u)) continue;
               uint32_t y[32];
               tmem_ld32(y, ts + k);
@@ -1268,7 +1274,7 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
                 !(p.is_tree ? (bits >> (row - it.start) & 1) != 0 : row <= it.start + tok))
               continue;
             if constexpr (FORM == kWindow)
-              if (row <= it.start + tok - p.window && row >= p.sinks) continue;
+              if (row <= row_at - p.window && row >= p.sinks) continue;
 #pragma unroll 1
             for (int c = c0; c < c1; c += 2) {
               float2 f = Pack2<T>::unpack(

@@ -136,7 +136,7 @@ _prompt_attention = _sig("dv_prompt_attention", [_CP, _I32, _I32P, _I32P,
 _tree_attention = _sig("dv_tree_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
                                              _P, _P, _SZ, _P])
 _window_attention = _sig("dv_window_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
-                                                 _I32, _I32, _P, _SZ, _P])
+                                                 _I32, _I32, _P, _P, _SZ, _P])
 _scored_attention = _sig("dv_scored_attention", [_CP, _I32, _I32P, _I32P, ctypes.POINTER(dv_queries),
                                                  _I32, _P, _P, _SZ, _P])
 _scored_workspace = _sig("dv_scored_attention_workspace", [_CP, _I32P, _I32P, _I32,
@@ -939,15 +939,17 @@ def _int32(x, name):
 
 
 def dv_window_attention(cache: Cache, layer, seq_start, seq_end, q, out, scale, window, sinks=0,
-                        workspace=None, stream=None) -> None:
+                        workspace=None, tree=None, stream=None) -> None:
     """Causal attention in which the token at row r attends the last ``window``
     rows up to its own and the first ``sinks`` rows.  Everything else as
-    ``dv_prompt_attention``; serves decode steps too."""
+    ``dv_prompt_attention``; serves decode steps too, and with ``tree`` (as
+    ``dv_tree_attention``) drafted tokens, whose windows end at their depth."""
     s, e, sp, ep = _ranges(seq_start, seq_end, cache.c.batch)
-    _, a = _queries(cache, q, out, scale)
+    n, a = _queries(cache, q, out, scale)
     w, wn = _buf(workspace)
+    t = None if tree is None else _words_of(tree, "tree", n, 8)
     _check(_window_attention(cache.ref, layer, sp, ep, ctypes.byref(a), _int32(window, "window"),
-                             _int32(sinks, "sinks"), w, wn, _stream(stream)))
+                             _int32(sinks, "sinks"), t, w, wn, _stream(stream)))
 
 
 def _mass(t, name, shape):

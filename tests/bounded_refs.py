@@ -38,9 +38,10 @@ def weights_ref(k, q, ok, scale):
     return w, 2 * D * 2.0 ** -24 * qk + 2.0 ** -21 + (z + 8) * 2.0 ** -24 + 2 * 2.0 ** -23 * (qk * 1.45 + 2 * math.log2(z + 1))
 
 
-def attend_ref(K, V, s, e, q, scale, window=1 << 40, sinks=0, last=0, mass=None):
+def attend_ref(K, V, s, e, q, scale, window=1 << 40, sinks=0, last=0, mass=None, masks=None):
     """(outputs, bounds, mass, bounds) in 64 bits; K, V: one layer; q [T, Hq, D]; mass
-    [B, H, S] (or None), to which the weights of the last `last` tokens (0: all) are added.
+    [B, H, S] (or None), to which the weights of the last `last` tokens (0: all) are added; masks:
+    what the tokens of each sequence attend, [z - a, z] (None: by the window).
 
     Outputs, with u half a step of the type and A = sum_j w_j |v_j|: u A for the weights'
     rounding to the type before the product with V, weights_ref's bound times A (its sum
@@ -60,7 +61,7 @@ def attend_ref(K, V, s, e, q, scale, window=1 << 40, sinks=0, last=0, mass=None)
         n = z - a
         if n == 0:
             continue
-        ok = window_mask(a, z, window, sinks, q.device)
+        ok = window_mask(a, z, window, sinks, q.device) if masks is None else masks[b]
         counted = n if last == 0 else min(n, last)
         for h in range(H):
             k = K[b, h, :, :z].transpose(0, 1).reshape(z, D)

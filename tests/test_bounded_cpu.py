@@ -53,8 +53,21 @@ def test_window_refusals():
         call(q=(_qo()[0], _qo(n=4)[1]))
     call(s=[4, 3], e=[4, 3])  # nothing to do: no pointer is looked at
     n = np.zeros(2, np.int32).ctypes.data
-    assert dv.lib.dv_window_attention(None, 0, n, n, None, 4, 1, None, 0, None) == dv.DV_ERR_INVALID_ARG
-    assert dv.lib.dv_window_attention(_cache().ref, 0, n, n, None, 4, 1, None, 0, None) == dv.DV_ERR_INVALID_ARG
+    assert dv.lib.dv_window_attention(None, 0, n, n, None, 4, 1, None, None, 0, None) == dv.DV_ERR_INVALID_ARG
+    assert dv.lib.dv_window_attention(_cache().ref, 0, n, n, None, 4, 1, None, None, 0, None) == dv.DV_ERR_INVALID_ARG
+
+
+def test_window_refusals_of_trees():
+    def call(n=5, window=64, bits=None, c=None, s=S2, e=E2):
+        q, o = _qo(n)
+        bits = torch.ones(n, dtype=torch.int64) if bits is None else bits
+        dv.dv_window_attention(c or _cache(), 0, s, e, q, o, 0.125, window, 1, None, tree=bits, stream=0)
+
+    _refused(dv.DV_ERR_UNSUPPORTED, lambda: call(window=63))
+    _refused(dv.DV_ERR_UNSUPPORTED, lambda: call(n=65, c=_cache(S=200), s=[4, 0], e=[69, 0]))
+    for bits in (torch.ones(4, dtype=torch.int64), torch.ones(5, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            call(bits=bits)
 
 
 def test_scored_refusals():

@@ -135,6 +135,59 @@ def test_random_windows(seed):
     assert bool(torch.isnan(out[0]).all() and torch.isnan(out[-1]).all())  # what lies around it is as it was
 
 
+TREES = [
+    # B, H, G, D, S, ctx, new, window, sinks
+    (3, 2, 1, 128, 700, (0, 630), (1, 9), 64, 4),
+    (3, 2, 4, 128, 1000, (100, 936), (1, 64), 100, 0),
+    (2, 2, 8, 64, 2000, (1500, 1900), (33, 64), 257, 130),
+    (2, 1, 71, 64, 400, (0, 390), (1, 3), 80, 5),
+    (2, 1, 128, 128, 500, (400, 430), (64, 64), 64, 1),      # windows that end among the new rows
+    (3, 2, 3, 40, 260, (0, 140), (1, 64), 65, 0),
+    (2, 2, 1, 72, 517, (200, 400), (1, 64), 1000, 3),         # windows that hide nothing
+    (11, 71, 1, 128, 700, (0, 600), (1, 3), 200, 4),          # two heads at a time
+    (10, 63, 4, 64, 500, (300, 480), (0, 16), 130, 33),
+    (1, 2, 4, 128, 30000, (29000, 29900), (31, 31), 20000, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("B, H, G, D, S, ctx, new, window, sinks", TREES)
+def test_window_over_trees(dtype, B, H, G, D, S, ctx, new, window, sinks):
+    """Drafted tokens: the new rows of their bits, and of the rows before those within the window that
+    ends at their depth; a token without any bits too."""
+    rng = np.random.default_rng(S + window)
+    gen = _gen(S + D)
+    s = rng.integers(ctx[0], ctx[1] + 1, size=B).astype(np.int32)
+    n = rng.integers(new[0], new[1] + 1, size=B).astype(np.int32)
+    e = (s + np.minimum(n, S - s)).astype(np.int32)
+    cache, K, V = R.make_cache(dtype, 1, B, H, D, S, gen)
+    bits, masks = [], []
+    for a, z in zip(s.tolist(), e.tolist()):
+        m = z - a
+        own = R.random_tree(m, rng)[0]
+        if m > 2:
+            own[m // 2] = 0
+        at = torch.tensor([a + max(x.bit_count() - 1, 0) for x in own], device="cuda")[:, None]
+        j = torch.arange(z, device="cuda")
+        ok = ((j < a) & ((j > at - window) | (j < sinks)))
+        for i, x in enumerate(own):
+            for k in range(m):
+                ok[i, a + k] = bool(x >> k & 1)
+        masks.append(ok)
+        bits += own
+    q = torch.empty(int((e - s).sum()), H * G, D, dtype=R.DT[dtype], device="cuda").normal_(generator=gen) * 2
+    want, tol, _, _ = W.attend_ref(K[0], V[0], s, e, q, 0.1, masks=masks)
+    for b, (a, z) in enumerate(zip(s.tolist(), e.tolist())):  # garbage where no token looks
+        hidden = torch.ones(S, dtype=torch.bool, device="cuda")
+        hidden[:z] = ~masks[b].any(0) if z > a else True
+        K[0, b].masked_fill_(hidden[None, None, :, None], math.nan)
+        V[0, b].masked_fill_(hidden[None, :, None], math.inf)
+    out = torch.full_like(q, math.nan)
+    tree = R.bits_tensor(bits)
+    dv.dv_window_attention(cache, 0, s, e, q, out, 0.1, window, sinks, _ws(cache, s, e, H * G), tree=tree)
+    R.assert_within(out, want, tol)
+
+
 def test_values_that_are_not_finite_reach_the_tokens_that_attend_them_alone():
     """An infinity in the first rows, a NaN at a window's edge: for each token as its row says."""
     gen = _gen(9)
