@@ -11,7 +11,8 @@
 // it still fit; it ends early when all of them do.  Each kept row's place is the number of kept
 // ones before it, those above the border and of those at it the first that fit.  The weights
 // are read once and stay in shared memory; in a cluster each CTA takes a run of the rows, and
-// the histograms and counts are added through distributed shared memory.
+// the histograms and counts are added through distributed shared memory.  Weights that are more
+// than a cluster's shared memory holds (400000) one CTA reads again in each pass.
 //
 // The copy: row i <- row keep[i] >= i, of K and V.  A CTA takes slices of the rows' 16-byte
 // chunks and walks the destinations upwards; a step's reads come before its writes, and later

@@ -57,7 +57,8 @@ constexpr int kFewWave = 8 * 152;
 constexpr int kUnit = 2 * kTile;  // rows of a unit of mass_kernel
 constexpr int kSumWarps = 16;
 constexpr int kMassThreads = 32 * (kSumWarps + 3);
-// What a unit costs besides its tiles (its keys' fetch, the sums' exchange), in tiles.
+// What a unit costs besides its tiles (its keys' fetch, the sums' exchange), in tiles of keys: 32
+// ragged prompts, 112 heads, 490, 464, 473 us at 1, 2, 3 (and one wait a tile more than now).
 constexpr int kMassUnitCost = 2;
 
 struct MassDivided {
@@ -574,7 +575,7 @@ struct FewParams {
   float* mass;
   int32_t H, S, last, chunks;
   int32_t join_ctas, join_blocks;  // blocks that join pieces of outputs: a unit's, of each cut
-  int32_t ctas, share, extra, unit_cost, heads;  // of the attention kernel
+  int32_t share, extra, unit_cost, heads;  // of the attention kernel's schedule
   float c;
   SeqTable<MAXB> seq;
   int32_t block_pre[MAXB + 1];
@@ -745,7 +746,6 @@ dv_status add_mass(const Plan& p, const dv_queries& q, const Extra& x, int32_t l
     fp.join = join_params(p, q, sch, x, reinterpret_cast<const float*>(ws));
     fp.join_ctas = x.join_later ? sch.ctas - 1 : 0;
     fp.join_blocks = (int32_t)join_blocks(p, q, sch);
-    fp.ctas = sch.ctas;
     fp.share = (int32_t)(sch.total / sch.ctas);
     fp.extra = (int32_t)(sch.total % sch.ctas);
     fp.unit_cost = sch.unit_cost;
