@@ -135,9 +135,17 @@ __global__ __launch_bounds__(kEvictThreads, 2) void evict_kernel(
   const int run = HELD || n == m ? (n + ctas - 1) / ctas : n;
   const int lo = min(rank * run, n), hi = min(lo + run, n);
   if (n == m) {  // (the same for every CTA of the cluster)
-    for (int i = lo + tid; i < hi; i += kEvictThreads) {
-      keep[i] = i;
-      out[i] = mass[i];
+    for (int i = lo + tid; i < hi; i += kEvictThreads) keep[i] = i;
+    if (out == mass) return;
+#pragma unroll 1
+    for (int i0 = lo + tid; i0 < hi; i0 += kEvictThreads * kCells) {
+      float x[kCells];
+#pragma unroll
+      for (int u = 0; u < kCells; ++u)
+        x[u] = i0 + u * kEvictThreads < hi ? mass[i0 + u * kEvictThreads] : 0.f;
+#pragma unroll
+      for (int u = 0; u < kCells; ++u)
+        if (i0 + u * kEvictThreads < hi) out[i0 + u * kEvictThreads] = x[u];
     }
     return;
   }
@@ -414,12 +422,17 @@ cudaError_t launch_evict(const Plan& p, int32_t sinks, int32_t recent, const flo
   kp.recent = recent;
   fill_table(p, &kp.seq);
   // As many CTAs a unit as hold its weights, and where there are few units as fill the SMs
-  // with runs of kLeastRun rows.
+  // with runs of kLeastRun rows.  Sequences that keep all have no say in the first: one of 131072
+  // rows beside 31 brought from 2000 to 1000, 8 heads of 64, 39 us (53 with a mass_out of its
+  // own); with clusters as for its rows, 170.
   const int64_t units = (int64_t)(p.l1 - p.l0) * p.H * p.B;
-  int32_t most = 0;
-  for (int b = 0; b < p.B; ++b) most = std::max(most, kp.seq.rows[b]);
+  int32_t most = 0, longest = 0;  // rows of a unit that searches; of one that moves weights
+  for (int b = 0; b < p.B; ++b) {
+    if (p.seq_len[b] > 0) most = std::max(most, kp.seq.rows[b]);
+    if (p.seq_len[b] > 0 || mass_out != mass) longest = std::max(longest, kp.seq.rows[b]);
+  }
   int ctas = 1;
-  while (ctas < kMaxCluster && (most > ctas * kHeld || (most > ctas * kLeastRun &&
+  while (ctas < kMaxCluster && (most > ctas * kHeld || (longest > ctas * kLeastRun &&
                                                         units * ctas * 2 <= 2 * 152)))
     ctas *= 2;
   kp.ctas = ctas;

@@ -131,6 +131,47 @@ def test_random_evictions(seed):
     _check(cache, K, V, k, v, l0, l1, rows, kept, sinks, recent, mass, bool(rng.integers(2)))
 
 
+UNTOUCHED = [
+    # L, B, H, D, S, rows, kept: sequences that keep all beside others that give rows up
+    (1, 2, 2, 16, 420000, [420000, 600], [420000, 300]),
+    (1, 3, 1, 64, 30000, [700, 29999, 650], [350, 29999, 64]),
+    (2, 2, 1, 64, 9000, [8999, 8192], [8999, 8192]),
+    (1, 2, 1, 64, 17000, [16999, 9000], [16999, 1000]),
+]
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("L, B, H, D, S, rows, kept", UNTOUCHED)
+def test_long_sequences_that_keep_all_beside_short_ones(L, B, H, D, S, rows, kept, in_place):
+    gen = _gen(S)
+    cache, K, V, k, v = _cache(L, B, H, D, S, 2, gen, gap=16)
+    mass = _weights("signs", (L, B, H, S), gen)
+    _check(cache, K, V, k, v, 0, L, np.array(rows, np.int32), np.array(kept, np.int32), 4, 20, mass, in_place)
+
+
+def test_sequences_that_keep_all_do_not_choose_the_kernel():
+    """More rows than a cluster's shared memory holds weights of, none of which is searched: the
+    short sequence's weights are held in shared memory all the same."""
+    from torch.profiler import ProfilerActivity, profile
+
+    gen = _gen(9)
+    cache, _, _, _, _ = _cache(1, 2, 1, 16, 420000, 2, gen)
+    mass = _weights("few", (1, 2, 1, 420000), gen)
+    keep = torch.empty(1, 1, 420300, dtype=torch.int32, device="cuda")
+    rows, kept = np.array([420000, 600], np.int32), np.array([420000, 300], np.int32)
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA]):  # (a process's first recording may miss kernels)
+        keep.zero_()
+        torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA]) as prof:
+        dv.dv_kv_evict(cache, 0, 1, rows, kept, 4, 20, mass, keep)
+        torch.cuda.synchronize()
+    names = [e.name for e in prof.events() if "evict_kernel" in e.name]
+    if not names:
+        pytest.skip("the profiler records no kernels here")
+    assert len(names) == 1 and "true>" in names[0], names
+
+
 def test_nothing_to_do():
     gen = _gen(3)
     cache, K, V, k, v = _cache(2, 2, 2, 64, 50, 2, gen)
