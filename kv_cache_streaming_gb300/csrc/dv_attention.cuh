@@ -90,6 +90,7 @@
 
 #include <cuda.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "dv_ops.h"
@@ -115,6 +116,9 @@ constexpr float kHalfUp = 7.f;
 // Waits in attention kernels that gave up, one for each lane; only ever grows, so that no
 // caller's check takes another's record away.
 __device__ unsigned long long g_attention_gave_up;
+// Whether this process has launched (or captured) this form: if not, its count is 0, and need
+// not be fetched, which would load its kernels.
+std::atomic<bool> g_launched{false};
 // The second half of the last contraction step when head_dim is an odd number of chunks.
 __device__ uint4 g_zero_rows[kTile];
 
@@ -1409,6 +1413,14 @@ struct Extra {
   bool join_later = false;  // by the kernel that adds up the scores
 };
 
+// Where this form counts the waits that gave up, on the current device; NULL: none has.
+inline cudaError_t waits_address(void** address) {
+  *address = nullptr;
+  return g_launched.load(std::memory_order_relaxed)
+             ? cudaGetSymbolAddress(address, g_attention_gave_up)
+             : cudaSuccess;
+}
+
 inline int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1626,6 +1638,7 @@ dv_status launch_attention(const Plan& p, const dv_queries& q, const Extra& x, f
     return p.D <= 64 ? launch_kernel<T, 64, kMode, MAXB, FORM>(kp, s.ctas, stream)
                      : launch_kernel<T, 128, kMode, MAXB, FORM>(kp, s.ctas, stream);
   };
+  g_launched.store(true, std::memory_order_relaxed);
   cudaError_t err = cudaErrorInvalidValue;
   if constexpr (FORM != kPlain)
     if (s.heads) err = launch(std::integral_constant<int, kHeads>());

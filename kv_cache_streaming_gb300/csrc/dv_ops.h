@@ -168,7 +168,7 @@ inline bool overlaps_layers(const Plan& p, const void* a, size_t n) {
 }
 
 // What the attention forms' translation units share: the tries of a wait, and where each one's
-// kernels count the waits that gave up (on the current device).
+// kernels count the waits that gave up (on the current device; NULL before the first launch).
 uint32_t attention_tries();
 cudaError_t plain_waits(void** address);
 cudaError_t window_waits(void** address);

@@ -37,9 +37,7 @@
 
 namespace dv {
 
-cudaError_t scored_waits(void** address) {
-  return cudaGetSymbolAddress(address, g_attention_gave_up);
-}
+cudaError_t scored_waits(void** address) { return waits_address(address); }
 
 namespace {
 

@@ -6,9 +6,7 @@
 
 namespace dv {
 
-cudaError_t window_waits(void** address) {
-  return cudaGetSymbolAddress(address, g_attention_gave_up);
-}
+cudaError_t window_waits(void** address) { return waits_address(address); }
 
 }  // namespace dv
 
