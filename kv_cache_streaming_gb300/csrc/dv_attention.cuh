@@ -1421,16 +1421,6 @@ inline cudaError_t waits_address(void** address) {
              : cudaSuccess;
 }
 
-inline int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    n = 152;
-  }
-  return n;
-}
-
 // A CTA's share is not cut below this many tiles, one for each chain, where
 // there are fewer units than SMs: a finer cut gains nothing that the join does
 // not take (one sequence's decode step over 1000 rows, 8 key heads: 8.7 us at 2

@@ -431,9 +431,10 @@ cudaError_t launch_evict(const Plan& p, int32_t sinks, int32_t recent, const flo
     if (p.seq_len[b] > 0) most = std::max(most, kp.seq.rows[b]);
     if (p.seq_len[b] > 0 || mass_out != mass) longest = std::max(longest, kp.seq.rows[b]);
   }
+  const int64_t places = 2 * sm_count();  // two CTAs an SM
   int ctas = 1;
   while (ctas < kMaxCluster && (most > ctas * kHeld || (longest > ctas * kLeastRun &&
-                                                        units * ctas * 2 <= 2 * 152)))
+                                                        units * ctas * 2 <= places)))
     ctas *= 2;
   kp.ctas = ctas;
   const int64_t run = ((int64_t)most + ctas - 1) / ctas;

@@ -93,6 +93,17 @@ cudaError_t ops_launch(void (*kernel)(Params...), dim3 grid, unsigned threads, s
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
+// SMs of the current device.
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    n = 152;
+  }
+  return n;
+}
+
 // Validates one layer's ranges for an operator on 2-byte elements.
 inline dv_status plan_layer(const dv_cache* c, int32_t layer, const int32_t* s, const int32_t* e,
                             int32_t dtype, Plan* p) {

@@ -47,11 +47,11 @@ namespace {
 // heads, with 16, 32, 64 tokens: 87, 109, 158 and 102, 106, 118.
 constexpr int kFewRows = 16;
 constexpr int kFewThreads = kJoinThreads, kFewPer = 4;
-// Blocks of the sums up to which they also join what the cuts divided: 8 an SM.  One launch less
+// Blocks of the sums, an SM, up to which they also join what the cuts divided.  One launch less
 // (8 short sequences, 25 heads of 64: 17.4 us, 20.3 with two), but every block of a divided
 // unit goes through its pieces' statistics (two contexts of 115000, 8 key heads: 165 us, 160 with
 // two launches; 32 sequences, 112 heads: 309 and 304).
-constexpr int kFewWave = 8 * 152;
+constexpr int kFewWave = 8;
 constexpr int kUnit = 2 * kTile;  // rows of a unit of mass_kernel
 constexpr int kSumWarps = 16;
 constexpr int kMassThreads = 32 * (kSumWarps + 3);
@@ -843,7 +843,7 @@ extern "C" dv_status dv_scored_attention(const dv_cache* cache, int32_t layer,
   if (dv::keeps_scores(p, group)) {
     x.scores = reinterpret_cast<float*>(rest);
     work = dv::few_chunks(p) * p.H * p.B;
-    x.join_later = work <= dv::kFewWave;
+    x.join_later = work <= dv::kFewWave * (int64_t)dv::sm_count();
   } else {
     work = dv::mass_cost(p, dv::kTile / group, last, nullptr, &tiles);
   }
