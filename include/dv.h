@@ -734,14 +734,15 @@ dv_status dv_tree_attention(const dv_cache* cache, int32_t layer, const int32_t*
 /* As dv_prompt_attention, of prompts and of decode steps alike, through a window: the token
  * at row r attends the rows j <= r with j > r - window or j < sinks, the last `window` rows up
  * to its own and the first `sinks` of the sequence (which stay visible: "attention sinks"; 0:
- * none).  Rows that no token attends are not read, and have no effect.  `tree`: NULL, or the new
- * tokens are drafted ones, at most DV_MAX_TREE of a sequence, which attend the new rows of their
- * bits as in dv_tree_attention, and of rows [0, seq_start) those that the row seq_start + (set
- * bits - 1) attends, the token's place after its ancestors; window at least DV_MAX_TREE (else
- * DV_ERR_UNSUPPORTED).  `workspace` and its size
- * as for dv_prompt_attention.  window >= 1, sinks >= 0 (else DV_ERR_INVALID_ARG); a window of
- * max_seq rows or more is plain causal attention.  max_seq at most 2^31 - 16385 (else
- * DV_ERR_UNSUPPORTED), here and in the two calls below. */
+ * none).  Rows that no token attends have no effect; of those beside a window or the first rows
+ * some may be read all the same.  `tree`: NULL, or the new tokens are drafted ones, at most
+ * DV_MAX_TREE of a sequence, which attend the new rows of their bits as in dv_tree_attention, and
+ * of rows [0, seq_start) those that the row seq_start + max(set bits - 1, 0) attends, the token's
+ * place after its ancestors (bits at or past the sequence's token count are not counted; a token
+ * without bits has the window of row seq_start); window at least DV_MAX_TREE (else
+ * DV_ERR_UNSUPPORTED).  `workspace` and its size as for dv_prompt_attention.  window >= 1, sinks
+ * >= 0 (else DV_ERR_INVALID_ARG); a window of max_seq rows or more is plain causal attention.
+ * max_seq at most 2^31 - 16385 (else DV_ERR_UNSUPPORTED), here and in the two calls below. */
 dv_status dv_window_attention(const dv_cache* cache, int32_t layer, const int32_t* seq_start,
                               const int32_t* seq_end, const dv_queries* queries, int32_t window,
                               int32_t sinks, const uint64_t* tree, void* workspace, size_t workspace_bytes,
@@ -782,7 +783,8 @@ dv_status dv_attention_check(dv_stream stream);
  * layers that are moved (else DV_ERR_INVALID_ARG).  An entry that is negative, not
  * below max_seq, or below its own destination row leaves that row as it was
  * (so that a list of fixed length can be padded with -1).  Rows outside the
- * ranges are untouched.  Any elem_bytes. */
+ * ranges are untouched.  Any elem_bytes.  A dv_replica's earlier records hold the rows
+ * as they were: a record of the ranges follows, as for dv_kv_evict. */
 dv_status dv_kv_compact(const dv_cache* cache, int32_t l0, int32_t l1, const int32_t* seq_start,
                         const int32_t* seq_end, const int32_t* keep, int64_t count,
                         dv_stream stream);
@@ -802,7 +804,13 @@ dv_status dv_kv_compact(const dv_cache* cache, int32_t l0, int32_t l1, const int
  *                   the other; `count` entries (else DV_ERR_INVALID_ARG).
  * All device memory, 4-byte aligned, on none of the layers (else DV_ERR_INVALID_ARG).  Positions
  * of the rows that stay are theirs still: tokens appended behind them are given theirs with
- * dv_new_tokens.positions.  Any elem_bytes. */
+ * dv_new_tokens.positions.  Any elem_bytes.
+ *
+ * Records that a dv_replica took before hold the rows as they were, and a restore would bring
+ * them back: after the call a record of rows [0, kept[b]) of layers [l0, l1) is appended before
+ * the next deltas, to the same log (later records win) or, to have the old ones' memory back, to
+ * one truncated to nothing.  No record holds the weights: who restores a cache to evict from it
+ * again keeps them. */
 dv_status dv_kv_evict(const dv_cache* cache, int32_t l0, int32_t l1, const int32_t* rows,
                       const int32_t* kept, int32_t sinks, int32_t recent, const float* mass,
                       float* mass_out, int32_t* keep, int64_t count, dv_stream stream);

@@ -248,6 +248,76 @@ def test_two_evictions_in_flight_on_two_streams_and_a_captured_one():
         check()
 
 
+@pytest.mark.parametrize("fresh", [False, True])
+def test_an_evicted_cache_and_its_replica(fresh):
+    """A replica's records hold rows as they were.  After an eviction a record of [0, kept) goes to
+    the log (or, `fresh`, is the first of an emptied one) and the deltas go on; a restore gives every
+    row in use, from where the kept weights choose the same rows again.  Without that record the
+    restore brings given-up rows back."""
+    gen = _gen(12)
+    L, B, H, D, S, P = 2, 3, 3, 64, 120, 2
+    cache, K, V, k, v = _cache(L, B, H, D, S, P, gen)
+    mass = _weights("few", (L, B, H, S), gen)
+    used, zero = np.array([80, 33, 100], np.int32), np.zeros(B, np.int32)
+    kept = np.array([40, 33, 52], np.int32)
+
+    def arena():
+        return torch.empty(L * B * H * D * S * P * 8, dtype=torch.uint8).pin_memory()
+
+    rep, bare = (dv.Replica(arena(), B) for _ in range(2))
+    step = 0
+
+    def record(logs, s, e):
+        nonlocal step
+        for r in logs:
+            r.append(cache, 0, L, s, e, step)
+        step += 1
+
+    def decode(logs, steps):
+        nonlocal used
+        for _ in range(steps):
+            for b in range(B):
+                K[:, b, :, :, used[b]].random_(generator=gen)
+                V[:, b, :, used[b]].random_(generator=gen)
+                mass[:, b, :, used[b]] = torch.rand(L, H, generator=gen, device="cuda")
+            record(logs, used, used + 1)
+            used = (used + 1).astype(np.int32)
+
+    def restored(r, batched):
+        back, BK, BV, bk, bv = _cache(L, B, H, D, S, P, gen)
+        (r.restore_batched if batched else r.restore)(back)
+        torch.cuda.synchronize()
+        same = all(torch.equal(BK[:, b, :, :, :n], K[:, b, :, :, :n]) and torch.equal(BV[:, b, :, :n], V[:, b, :, :n])
+                   for b, n in enumerate(used.tolist()))
+        return same, (back, BK, BV)
+
+    record((rep, bare), zero, used)
+    decode((rep, bare), 5)
+    assert restored(rep, True)[0]
+    keep = torch.empty(L, H, int(kept.sum()), dtype=torch.int32, device="cuda")
+    dv.dv_kv_evict(cache, 0, L, used, kept, 4, 8, mass, keep)
+    used = kept
+    torch.cuda.synchronize()
+    if fresh:
+        rep.truncate(0)
+        assert rep.info() == (0, 0)
+    record((rep,), zero, kept)
+    decode((rep, bare), 4)
+    torch.cuda.synchronize()
+    for batched in (False, True):
+        same, (back, BK, BV) = restored(rep, batched)
+        assert same
+        assert not restored(bare, batched)[0]
+    again, lists = np.array([20, 37, 30], np.int32), []
+    for c in (cache, back):
+        keep = torch.empty(L, H, int(again.sum()), dtype=torch.int32, device="cuda")
+        dv.dv_kv_evict(c, 0, L, used, again, 4, 8, mass, keep, mass_out=torch.empty_like(mass))
+        lists.append(keep)
+    assert torch.equal(*lists)
+    for b, n in enumerate(again.tolist()):
+        assert torch.equal(BK[:, b, :, :, :n], K[:, b, :, :, :n]) and torch.equal(BV[:, b, :, :n], V[:, b, :, :n])
+
+
 def test_a_cache_past_2_31_elements():
     """The last head of a layer of 2^31 elements: rows far apart moved to its front."""
     B, H, D, S = 2, 64, 128, 131072
