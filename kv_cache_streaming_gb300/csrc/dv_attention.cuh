@@ -83,7 +83,9 @@
 // and a window of 500 take 7 tiles, of whose products 56% are attended): ragged prompts
 // through 500 rows, 40 heads, 135 us; 4096 tokens behind 120000 rows through 4096, 64 query
 // heads on 8, 407 us, 1.36 PFLOP/s attended; a decode step of 32 sequences through 512
-// rows, 112 heads, 147 us, 5.6 TB/s.  On the way: the first rows in a tile of their own, 430 us
+// rows, 112 heads, 147 us, 5.6 TB/s; one token of 32 sequences through 4096 rows behind 30000, 64
+// query heads on 8, 90 us, 6.0 TB/s; 8 x 64 drafted nodes there, 76 us (35 through 512).  Its SPLIT
+// form spills two registers, whose loads lie in the loop: 11 a tile of 1350 instructions.  On the way: the first rows in a tile of their own, 430 us
 // for the 4096 tokens and 178 for the decode step; before HEADS, 409 and 166; with the
 // first rows fetched 32 at a time, 150.
 #pragma once
@@ -1432,7 +1434,14 @@ constexpr int kMinTiles = 2;
 // 346 us at 0, 252 at 1, 232 at 2, 246 at 5; ragged prompts: 902 at 0, 823 at 1,
 // 814 at 2, 828 at 3, where prompts of 1000 take 57, 53, 55, 55).
 constexpr int kUnitCostPair = 1, kUnitCostSplit = 2, kUnitCostHeads = 1;
-constexpr int kHeadsUnits = 4;  // an SM: with fewer, HEADS would leave SMs without a pair of heads
+// Units an SM from which on HEADS is taken: with fewer it would leave SMs without a pair of heads.
+// HEADS and SPLIT in us, one token a sequence, heads of 128: through windows of 512, 1024, 2048, 4096
+// rows (5, 9, 17, 33 tiles a unit) 32 sequences of 40 heads 67, 113, 209, 390 and 81, 116, 205, 388, 128
+// sequences of 64 query heads on 8 60, 95, 171, 320 and 66, 97, 171, 321; scored, the same 128 over
+// 500, 1000, 4000, 16000 rows 66, 110, 372, 1400 and 68, 109, 372, 1388.  So it pays up to some 8 tiles
+// and is level beyond.  An odd last head costs a pair's place on the line: 100 sequences of 56 query
+// heads on 7, through the windows, 47, 73, 126, 234 and 50, 71, 120, 221.
+constexpr int kHeadsUnits = 4;
 
 // Rows of a K copy's innermost run: a chunk row's S rows of 16 bytes are one run, so it may be
 // as many as divide S, up to the 256 elements a box may have: 512 bytes where 32 divide

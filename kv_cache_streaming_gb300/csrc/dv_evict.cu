@@ -12,17 +12,19 @@
 // ones before it, those above the border and of those at it the first that fit.  The weights
 // are read once and stay in shared memory; in a cluster each CTA takes a run of the rows, and
 // the histograms and counts are added through distributed shared memory.  Weights that are more
-// than a cluster's shared memory holds (400000) one CTA reads again in each pass.
+// than a cluster's shared memory holds (409600) one CTA reads again in each pass.
 //
 // The copy: row i <- row keep[i] >= i, of K and V.  A CTA takes slices of the rows' 16-byte
 // chunks and walks the destinations upwards; a step's reads come before its writes, and later
 // steps read rows past what earlier ones have written.
 //
 // Bound by memory, and on K by the rate of DRAM accesses: in the x-interleaved layout a kept row's
-// chunk is 16 bytes between others that go, of which a miss fetches 64.  Measured: the rows
-// of 8 sequences x 40 heads of 128 halved in 8 layers (1.79 GB asked for) 344 us; two contexts of
-// 110000 rows cut to a tenth, 8 heads of 128, 4 layers (0.86 GB asked for, 1.2 GB of DRAM traffic, 12.5
-// million K chunks) 341 us; 8 sequences x 25 heads brought from 433 to 400 rows 14.1 us.  Tried
+// chunk is 16 bytes between others that go, of which a miss fetches 64.  Measured, calls in a
+// loop: the rows of 8 sequences x 40 heads of 128 halved in 8 layers (1.79 GB asked for) 344 us (like
+// rows of 1-, 2- and 4-byte elements 199, 338, 648); two contexts of 110000 rows cut to a tenth, 8 heads of 128, 4
+// layers (0.86 GB asked for, 1.2 GB of DRAM traffic, 12.5 million K chunks) 340 to 345 us; two of
+// 450000 rows, beyond shared memory, cut to 20000, 2 heads of 64, 0.92 ms; in a replayed graph, 8
+// sequences x 25 heads brought from 433 to 400 rows 14.2 us (17 in a loop, the host's call).  Tried
 // and slower: the search a launch of its own (413, 654, 16.4 us); K chunks by whole lines (436 us on
 // the long contexts); the weights read again from the caches in each pass, four CTAs of 256
 // threads an SM (437, 401, 24 us).
@@ -439,7 +441,10 @@ cudaError_t launch_evict(const Plan& p, int32_t sinks, int32_t recent, const flo
   kp.ctas = ctas;
   const int64_t run = ((int64_t)most + ctas - 1) / ctas;
   const bool held = run <= kMostHeld;
-  // Each CTA copies a slice of K and one of V, of 32 to 256 bytes a row.
+  // Slices of K and of V, 32 to 256 bytes of a row each (16 where it has no more), which a unit's
+  // CTAs take in turn, K's first.  With heads of 128 each of 8 CTAs gets one of K and one of V;
+  // with heads of 64, 4 slices of each, half of them copy K alone and half V (two contexts of
+  // 110000 cut to 12000, 8 heads, 4 layers: 211 us).
   int slices = std::max((p.C + 15) / 16, kp.ctas);
   kp.slice = std::max((p.C + slices - 1) / slices, std::min(2, p.C));
   kp.slices = (p.C + kp.slice - 1) / kp.slice;

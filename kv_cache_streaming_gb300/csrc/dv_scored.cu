@@ -20,13 +20,19 @@
 // keys, two to a quarter of the rows with half of the columns each; 16 loads (and walks over the
 // units), 17 issues the products into two buffers of tensor memory for each tile, 18 fetches lse.
 //
+// A group that does not divide 128 leaves columns of each tile without a token, which takes the
+// masked sums for its last 32 columns: 8 prompts of 64 to 1536 tokens at groups of 4, 5, 6, 7, 8
+// give 430, 422, 416, 413, 440 TFLOP/s attended.  (Two spilled registers of mass_kernel are stored and
+// loaded a few times a unit, not in the loop over its tiles.)
+//
 // Every wait gives up after a number of tries, as in the attention kernel.
 //
 // Measured (bf16, heads of 128): a decode step of 32 sequences of 64 to 1791 rows, 112 heads, 300
-// us, of which few_kernel takes 14 to 16 (6.3 TB/s); two contexts of 115000, 64 query heads on 8, 159
-// us (few_kernel 19); 32 prompts of 64 to 1536 tokens, 112 heads, 1464 us, of which mass_kernel takes
-// 448: about 1000 cycles a tile of 128 x 128, where its products and its exponentials take 512
-// each.  It is bound by the instructions around them (2400 a tile for 1170 of loads, sums and
+// us, of which few_kernel takes 14 to 16 (6.3 TB/s); two contexts of 115000, 64 query heads on 8, 160
+// us (few_kernel 19); 32 prompts of 64 to 1536 tokens, 112 heads, 1387 us in a short loop: attention
+// 925, its join 13, mass_kernel 447, its join 3; under the power cap of a long one 1477: 988, 14, 471,
+// 3.  mass_kernel takes about 1000 cycles a tile of 128 x 128, where its products and its
+// exponentials take 512 each.  It is bound by the instructions around them (2400 a tile for 1170 of loads, sums and
 // exponentials), with the tensor cores 47% and the special functions 42% active.  On the way:
 // units of 128 keys 582 us (560 without products, 404 without exponentials: L2, which then fetched
 // the queries twice as often), of 256 552, hidden columns skipped 501, sixteen warps 464, one wait
