@@ -920,9 +920,12 @@ __global__ __launch_bounds__(kThreadsAttn, 1) void attention_kernel(
 #pragma unroll 1
             while (jv < jk) {
               const bool own = mine(jv);
-              // (hidden rows have been looked at where the tile has any)
-              if (!wait(at(own && hides(it, tile_of(it, jv)) ? ctl.v_ok[vr.slot] : ctl.v_full[vr.slot]),
-                            vr.turn))
+              // The tile has come, and its hidden rows have been looked at where it has any.  (A
+              // parity tells a turn from the next only to who has seen the one before: the chain
+              // waits for v_full at every turn, and v_ok, which it asks for in some, is not a turn
+              // behind once v_full has come, as the look lets a slot go after it.)
+              if (!wait(at(ctl.v_full[vr.slot]), vr.turn) ||
+                  (own && hides(it, tile_of(it, jv)) && !wait(at(ctl.v_ok[vr.slot]), vr.turn)))
                 return false;
               if (own) {
                 const uint64_t vd =
