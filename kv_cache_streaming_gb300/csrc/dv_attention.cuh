@@ -68,10 +68,10 @@
 // rows, 112 heads (1.52 GB) 230 to 232 us, 6.5 to 6.6 TB/s.
 // PAIR is bound by the chain scores - softmax - products of a tile, about 3100
 // cycles for a pair of tiles whose products take 2048 on the tensor cores: 4096
-// tokens after 28672, 64 query heads on 8, 2.72 to 2.81 ms, 1.47 to 1.52 PFLOP/s (2.63
+// tokens after 28672, 64 query heads on 8, 2.72 to 2.86 ms, 1.46 to 1.52 PFLOP/s (2.63
 // to 2.68 alone); on short prompts the filling and draining of the chains come on
 // top, and the half of the diagonal tiles that is hidden: 32 prompts of 64 to 1536
-// tokens, 112 heads, 0.85 to 0.86 ms, 0.84 PFLOP/s attended.
+// tokens, 112 heads, 0.85 to 0.88 ms, 0.82 to 0.84 PFLOP/s attended.
 // Heads of 64 halve the products but not the softmax: 8 prompts of 1000, 25
 // heads (fp16), 54 us.  What was tried and was slower: S in halves of 64
 // columns two steps ahead; two buffers of 96 columns for heads of 64; the
